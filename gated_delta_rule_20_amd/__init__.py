@@ -17,11 +17,14 @@ import os
 import torch
 
 __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "NOALLOC_WORKSPACE_BYTES", "recurrent_step", "recurrent_replay", "chunk_fwd_workspace_size", "load_library",
-           "Fusion", "KDAError", "LIB_PATH", "EXPORTED_SYMBOLS"]
+           "Fusion", "KDAError", "LIB_PATH", "EXPORTED_SYMBOLS",
+           "linear_recurrent_step", "cache_copy", "cache_fork", "cache_free", "cache_compact"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 EXPORTED_SYMBOLS = ("kda_chunk_fwd_workspace_size", "kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_recurrent_step",
-                    "kda_recurrent_replay", "kda_status_string", "kda_last_error_message")
+                    "kda_recurrent_replay", "kda_status_string", "kda_last_error_message",
+                    "kda_linear_recurrent_step", "kda_cache_copy", "kda_cache_fork", "kda_cache_free",
+                    "kda_cache_compact")
 
 KDA_F32, KDA_BF16 = 0, 1
 _DTYPES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
@@ -142,6 +145,21 @@ class Fusion:
         return self.conv_weight is not None
 
 
+class LinearStepArgs(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32), ("Dk", ctypes.c_int32),
+                ("Dv", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("g", ctypes.c_void_p), ("g_per_head", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("slots", ctypes.c_void_p), ("n_slots", ctypes.c_int32), ("state", ctypes.c_void_p),
+                ("new_state", ctypes.c_void_p), ("o", ctypes.c_void_p)]
+
+
+class CachePool(ctypes.Structure):
+    _fields_ = [("dst", ctypes.c_void_p), ("src", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t)]
+
+
+CACHE_MAX_POOLS = 8  # KDA_CACHE_MAX_POOLS
+
 _lib = None
 
 
@@ -163,6 +181,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.kda_recurrent_step.restype = ctypes.c_int
     lib.kda_recurrent_replay.argtypes = [ctypes.POINTER(ReplayArgs), ctypes.c_void_p]
     lib.kda_recurrent_replay.restype = ctypes.c_int
+    ptr, i32 = ctypes.c_void_p, ctypes.c_int32
+    pools = [ctypes.POINTER(CachePool), i32]
+    for name, argtypes in (
+            ("kda_linear_recurrent_step", [ctypes.POINTER(LinearStepArgs), ptr]),
+            ("kda_cache_copy", pools + [i32, i32, ptr, ptr, i32, ptr]),
+            ("kda_cache_fork", pools + [i32, ptr, i32, i32, ptr, ptr, ptr, i32, ptr, ptr, ptr]),
+            ("kda_cache_free", [ptr, i32, i32, ptr, i32, ptr, i32, ptr]),
+            ("kda_cache_compact", pools + [i32, ptr, i32, i32, ptr, ptr, ptr, ptr, ptr])):
+        getattr(lib, name).argtypes = argtypes
+        getattr(lib, name).restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_last_error_message.argtypes = []
@@ -453,3 +481,8 @@ def recurrent_replay(q, k, v, g, beta, state, *, replay=None, n_replay=None, n_c
         a.fusion = ctypes.pointer(fa)
     _check(lib, "kda_recurrent_replay", lib.kda_recurrent_replay(ctypes.byref(a), _stream(stream, state.device)))
     return out
+
+
+# Re-exported last: these modules build on the helpers above.
+from .cache import cache_compact, cache_copy, cache_fork, cache_free  # noqa: E402
+from .linear import linear_recurrent_step  # noqa: E402

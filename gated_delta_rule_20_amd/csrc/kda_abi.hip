@@ -7,15 +7,10 @@
 #include <mutex>
 
 #include "kda.h"
+#include "kda_abi.h"
 #include "kda_prefill.h"
 
-// Workspace of kda_chunk_fwd_noalloc: one copy of this array lives on every
-// device that loads the library, for the life of the process.  In host code
-// its name is only a stand-in; the device address comes from
-// hipGetSymbolAddress (once per device, below).
-static __device__ __align__(256) char scratch[KDA_NOALLOC_WORKSPACE_BYTES];
-
-namespace {
+namespace kda_abi {
 
 thread_local char g_err[512] = "";
 
@@ -28,7 +23,18 @@ kda_status_t fail(kda_status_t st, const char *fmt, ...)
     return st;
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+}  // namespace kda_abi
+
+using namespace kda_abi;
+
+// Workspace of kda_chunk_fwd_noalloc: one copy of this array lives on every
+// device that loads the library, for the life of the process.  In host code
+// its name is only a stand-in; the device address comes from
+// hipGetSymbolAddress (once per device, below).
+static __device__ __align__(256) char scratch[KDA_NOALLOC_WORKSPACE_BYTES];
+
+namespace {
+
 bool head_dim_ok(int d) { return d == 64 || d == 128; }
 
 kda_status_t check_common(int dtype, int Dk, int Dv, const float *A_log, float g_min)
@@ -143,11 +149,6 @@ kda_status_t plan_chunk(const kda_chunk_fwd_args_t *a, ChunkPlan *pl)
     pl->blocks = pairs ? 0 : (size_t)a->H * (size_t)cap * block;
     pl->total = pl->table + pl->blocks;
     return KDA_SUCCESS;
-}
-
-kda_status_t hip_fail(hipError_t e, const char *what)
-{
-    return fail(KDA_ERROR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 // Device address of `scratch` on the current device, looked up once per device.

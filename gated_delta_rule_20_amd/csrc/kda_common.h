@@ -183,4 +183,14 @@ __device__ __forceinline__ float clamp_logdecay(float g, float g_min) {
     return fminf(fmaxf(g, g_min), 0.0f);
 }
 
+// A log-decay of linear attention in units of log 2, for exp2: at most 0, and at
+// least -256, whose exp2 is 0 in float32 like that of everything below it, so
+// that sums and differences of a chunk stay finite (-inf included).  NaN passes.
+__device__ __forceinline__ float log2_decay(float g)
+{
+    float x = g * 1.44269504088896340736f;
+    x = x > 0.0f ? 0.0f : x;
+    return x < -256.0f ? -256.0f : x;
+}
+
 }  // namespace kda

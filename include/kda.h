@@ -295,6 +295,108 @@ typedef struct {
 
 KDA_API kda_status_t kda_recurrent_replay(const kda_replay_args_t *args, void *stream);
 
+/*
+ * Linear attention with a decay for each head.  The recurrence next to eq. (1)
+ * that writes without the delta rule and forgets with one scalar per head:
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,   S in R^{Dk x Dv}.
+ * The conventions at the top of this header hold, with these differences:
+ *   - g is float32 whatever the dtype (its sums over many tokens decide what is
+ *     remembered): [H] constant log-decays when g_per_head is set, else one per
+ *     token and value head.  Values above 0 count as 0; values of -177 and
+ *     below, -inf among them, forget the state (exp(g) is 0 in float32).
+ *   - Hk query / key heads serve H value heads (H a multiple of Hk): value head
+ *     h reads query / key head h / (H / Hk).  Hk = H is the plain layout.
+ *   - q and k need no norm bound.
+ * Sums, states and decays are held in float32 or more.
+ */
+
+/*
+ * One token for each of N sequences:
+ *   q, k : [N, Hk, Dk]   v, o : [N, H, Dv]   g : [N, H] or [H]
+ *   state : [n_slots, H, Dk, Dv] float32, read; new_state : the same shape,
+ *   written; pass the same pointer to update in place (they must not overlap
+ *   otherwise).
+ * slots ([N] int32 on the device) names the slot of each sequence's state, or
+ * NULL for slot n = sequence n (n_slots >= N).  A row whose slot is outside
+ * [0, n_slots) is an empty place of a padded batch: its o is zero and no state
+ * is touched.  A slot that several rows name belongs to the first of them; the
+ * others count as empty places.  Slots that no row names are left as they were.
+ */
+typedef struct {
+    int32_t N, H, Hk, Dk, Dv;
+    int32_t dtype;                 /* kda_dtype_t */
+    const void *q, *k, *v;
+    const float *g;
+    int32_t g_per_head;
+    float scale;
+    const int32_t *slots;
+    int32_t n_slots;
+    const float *state;
+    float *new_state;
+    void *o;
+} kda_linear_step_args_t;
+
+KDA_API kda_status_t kda_linear_recurrent_step(const kda_linear_step_args_t *args, void *stream);
+
+/*
+ * Pages of a state cache ("Kimi K3 Technical Report", §5.4.1: states live in a
+ * paged pool; prefix snapshots are read-only, shared, and copied into private
+ * states).  A page is a fixed number of bytes in each of n_pools pools (a
+ * recurrent state, its convolution state, ...), at page * page_bytes from the
+ * pool's base; any page size and element type.
+ * refcount [n_pages] int32 counts how many page-table entries hold each page; a
+ * page is free when it is not above 0.  table [rows, per_row] int32 lists each
+ * sequence's pages in order, -1 where there is none; the last page of a row
+ * is the one still being written, the ones before it are read only.
+ * All tables are device memory (4-byte aligned); pages and rows out of range
+ * are skipped and never accessed.  The arrays must not overlap.
+ */
+typedef struct {
+    void *dst;                     /* pool that is written (compact, fork: the pool) */
+    const void *src;               /* pool that is read (kda_cache_copy only; NULL = dst) */
+    size_t page_bytes;
+} kda_cache_pool_t;
+
+#define KDA_CACHE_MAX_POOLS 8
+
+/* Copies page src_pages[i] of every src pool to page dst_pages[i] of its dst
+ * pool, i < n.  Of several pairs with one destination the last counts.  Within
+ * one pool no page may be both a source and a destination (its copy would hold
+ * either content), and src and dst pools must be the same or not overlap. */
+KDA_API kda_status_t kda_cache_copy(const kda_cache_pool_t *pools, int32_t n_pools, int32_t n_dst_pages,
+                                    int32_t n_src_pages, const int32_t *dst_pages, const int32_t *src_pages,
+                                    int32_t n, void *stream);
+
+/* Makes row children[i] a continuation of row parents[i], i < n: it shares the
+ * parent's pages (their refcount rises) except the last one, which is copied to
+ * a free page of its own; the i-th fork that needs a page takes the i-th lowest
+ * free one.  new_pages[i] and old_pages[i] receive the copy and its original,
+ * or -1.  A fork of a row without pages gives a row without pages.  A fork for
+ * which no page is left, one with a row out of range, one whose child is any
+ * fork's parent and one whose child an earlier fork names changes nothing but
+ * new_pages[i] = old_pages[i] = -1 (and, where no page is left, sets the
+ * child's row to -1).  The child's row is overwritten: free it first. */
+KDA_API kda_status_t kda_cache_fork(const kda_cache_pool_t *pools, int32_t n_pools, int32_t n_pages, int32_t *table,
+                                    int32_t rows, int32_t per_row, int32_t *refcount, const int32_t *parents,
+                                    const int32_t *children, int32_t n, int32_t *old_pages, int32_t *new_pages,
+                                    void *stream);
+
+/* Gives up the pages of rows free_rows[i], i < n: every entry's refcount falls by
+ * one (not below 0) and the row becomes -1.  A row named twice is freed once. */
+KDA_API kda_status_t kda_cache_free(int32_t *table, int32_t rows, int32_t per_row, int32_t *refcount, int32_t n_pages,
+                                    const int32_t *free_rows, int32_t n, void *stream);
+
+/* Moves the live pages to the front of the pool: live pages below their number
+ * stay, and the i-th live page at or above it moves to the i-th free page below
+ * it.  refcount and table follow (entries of free pages become -1).
+ *   moved_to [n_pages]: each page's new place, -1 for a free page
+ *   moves [n_pages]:    the moves as (from, to) pairs, lowest first; the rest is
+ *                       left unspecified
+ *   counts [2]:         live pages, moves */
+KDA_API kda_status_t kda_cache_compact(const kda_cache_pool_t *pools, int32_t n_pools, int32_t n_pages, int32_t *table,
+                                       int32_t rows, int32_t per_row, int32_t *refcount, int32_t *moved_to,
+                                       int32_t *moves, int32_t *counts, void *stream);
+
 /* Static description of a status code. */
 KDA_API const char *kda_status_string(kda_status_t status);
 

@@ -1,0 +1,155 @@
+"""The entry points of linear attention and of the cache's pages reject bad arguments with a status before anything
+is enqueued (CPU only: no call here reaches a kernel launch)."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+import gated_delta_rule_20_amd as kda
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(kda.LIB_PATH):
+        from gated_delta_rule_20_amd import build
+        build.build()
+    return kda.load_library()
+
+
+def _message(lib):
+    return lib.kda_last_error_message().decode()
+
+
+def _step_args(**over):
+    a = kda.LinearStepArgs(N=4, H=4, Hk=2, Dk=128, Dv=64, dtype=kda.KDA_BF16, scale=1.0, n_slots=8, g_per_head=0)
+    for f in ("q", "k", "v", "g", "slots", "o"):
+        setattr(a, f, 0x10000)
+    a.state, a.new_state = 0x1000000, 0x1000000
+    for key, val in over.items():
+        setattr(a, key, val)
+    return a
+
+
+@pytest.mark.parametrize("over,status,msg", [
+    (dict(Dk=96), 2, "head dims"),
+    (dict(Dv=256), 2, "head dims"),
+    (dict(dtype=2), 1, "dtype"),
+    (dict(H=0), 1, "multiple"),
+    (dict(Hk=0), 1, "multiple"),
+    (dict(Hk=3), 1, "multiple"),
+    (dict(N=-1), 1, "N >= 0"),
+    (dict(N=1 << 29), 2, "too large"),
+    (dict(n_slots=-1), 1, "n_slots"),
+    (dict(slots=None, n_slots=3), 1, "at least N"),
+    (dict(slots=0x10002), 1, "slots"),
+    (dict(scale=float("nan")), 1, "scale"),
+    (dict(scale=float("inf")), 1, "scale"),
+    (dict(g=None), 1, "g is NULL"),
+    (dict(g=0x10001), 1, "g is not"),
+    (dict(q=None), 1, "q is NULL"),
+    (dict(k=0x10008), 1, "k is not 16-byte"),
+    (dict(v=None), 1, "v is NULL"),
+    (dict(state=None), 1, "state is NULL"),
+    (dict(new_state=0x1000004), 1, "new_state is not"),
+    (dict(new_state=0x1000000 + 8 * 4 * 128 * 64 * 4 - 16), 1, "overlaps"),
+    (dict(new_state=0x1000000 - 16), 1, "overlaps"),
+    (dict(o=None), 1, "o is NULL"),
+])
+def test_step_rejects(lib, over, status, msg):
+    assert lib.kda_linear_recurrent_step(ctypes.byref(_step_args(**over)), None) == status
+    assert msg in _message(lib)
+
+
+def test_step_null_and_empty(lib):
+    assert lib.kda_linear_recurrent_step(None, None) == 1
+    assert lib.kda_linear_recurrent_step(ctypes.byref(_step_args(N=0, q=None, g=None, state=None)), None) == 0
+
+
+def _pool(dst=0x100000, src=None, page=64):
+    return (kda.CachePool * 1)(kda.CachePool(dst, src, page))
+
+
+A = 0x10000  # an aligned address that nothing dereferences
+
+
+@pytest.mark.parametrize("args,status,msg", [
+    ((_pool(), -1, 4, 4, A, A, 1), 1, "n_pools"),
+    ((_pool(), 9, 4, 4, A, A, 1), 1, "n_pools"),
+    ((None, 1, 4, 4, A, A, 1), 1, "pools is NULL"),
+    ((_pool(dst=None), 1, 4, 4, A, A, 1), 1, "pool 0 is NULL"),
+    ((_pool(page=0), 1, 4, 4, A, A, 1), 1, "no page bytes"),
+    ((_pool(page=1 << 41), 1, 4, 4, A, A, 1), 2, "1 TiB"),
+    ((_pool(), 1, -1, 4, A, A, 1), 1, "page counts"),
+    ((_pool(), 1, 4, 4, A, A, -1), 1, "n=-1"),
+    ((_pool(), 1, 4, 4, None, A, 1), 1, "dst_pages is NULL"),
+    ((_pool(), 1, 4, 4, A, A + 2, 1), 1, "src_pages is not"),
+    ((_pool(src=0x100040), 1, 4, 4, A, A, 1), 1, "overlaps"),
+    ((_pool(page=1 << 39), 1, 4, 4, A, A, 1 << 20), 2, "too many"),
+])
+def test_copy_rejects(lib, args, status, msg):
+    assert lib.kda_cache_copy(*args, None) == status
+    assert msg in _message(lib)
+
+
+def test_cache_noops(lib):
+    assert lib.kda_cache_copy(_pool(), 1, 4, 4, None, None, 0, None) == 0
+    assert lib.kda_cache_copy(None, 0, 4, 4, A, A, 3, None) == 0
+    assert lib.kda_cache_fork(_pool(), 1, 4, A, 2, 2, A, None, None, 0, None, None, None) == 0
+    assert lib.kda_cache_free(A, 2, 2, A, 4, None, 0, None) == 0
+    assert lib.kda_cache_free(None, 0, 2, A, 4, A, 3, None) == 0
+
+
+@pytest.mark.parametrize("args,msg", [
+    ((_pool(), 1, -1, A, 2, 2, A, A, A, 1, A, A), "n_pages"),
+    ((_pool(), 1, 1 << 30, A, 2, 2, A, A, A, 1, A, A), "n_pages"),
+    ((_pool(), 1, 4, A, -2, 2, A, A, A, 1, A, A), "rows"),
+    ((_pool(), 1, 4, None, 2, 2, A, A, A, 1, A, A), "table is NULL"),
+    ((_pool(), 1, 4, A, 2, 2, None, A, A, 1, A, A), "refcount is NULL"),
+    ((_pool(), 1, 4, A + 1, 2, 2, A, A, A, 1, A, A), "4-byte"),
+    ((_pool(), 1, 4, A, 2, 2, A, None, A, 1, A, A), "parents"),
+    ((_pool(), 1, 4, A, 2, 2, A, A, None, 1, A, A), "children"),
+    ((_pool(), 1, 4, A, 2, 2, A, A, A, -1, A, A), "n=-1"),
+    ((_pool(), 1, 4, A, 2, 2, A, A, A, 1, None, A), "old_pages"),
+    ((_pool(), 1, 4, A, 2, 2, A, A, A, 1, A, None), "new_pages"),
+])
+def test_fork_rejects(lib, args, msg):
+    assert lib.kda_cache_fork(*args, None) == 1
+    assert msg in _message(lib)
+
+
+@pytest.mark.parametrize("args,msg", [
+    ((A, 2, -1, A, 4, A, 1), "per_row"),
+    ((None, 2, 2, A, 4, A, 1), "table is NULL"),
+    ((A, 2, 2, None, 4, A, 1), "refcount is NULL"),
+    ((A, 2, 2, A, 4, None, 1), "free_rows"),
+])
+def test_free_rejects(lib, args, msg):
+    assert lib.kda_cache_free(*args, None) == 1
+    assert msg in _message(lib)
+
+
+@pytest.mark.parametrize("args,msg", [
+    ((_pool(), 1, 4, None, 2, 2, A, A, A, A), "table is NULL"),
+    ((_pool(), 1, 4, A, 2, 2, A, None, A, A), "moved_to"),
+    ((_pool(), 1, 4, A, 2, 2, A, A, None, A), "moves"),
+    ((_pool(), 1, 4, A, 2, 2, A, A, A, None), "counts"),
+])
+def test_compact_rejects(lib, args, msg):
+    assert lib.kda_cache_compact(*args, None) == 1
+    assert msg in _message(lib)
+
+
+def test_binding_requires_device_tensors(lib):
+    x, s = torch.zeros(3, 2, 64), torch.zeros(3, 2, 64, 64)
+    i = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="device tensor"):
+        kda.linear_recurrent_step(x, x, x, torch.zeros(2), s)
+    with pytest.raises(ValueError, match="unsupported dtype"):
+        kda.linear_recurrent_step(x.half(), x.half(), x.half(), torch.zeros(2), s)
+    with pytest.raises(ValueError, match="device tensor"):
+        kda.cache_copy(s, None, i, i)
+    with pytest.raises(ValueError, match="pools"):
+        kda.cache_copy([], None, i, i)
+    with pytest.raises(ValueError, match="device tensor"):
+        kda.cache_free(i.view(1, 3), i, i)
