@@ -18,11 +18,14 @@ import torch
 
 __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "NOALLOC_WORKSPACE_BYTES", "recurrent_step", "recurrent_replay", "chunk_fwd_workspace_size", "load_library",
            "Fusion", "KDAError", "LIB_PATH", "EXPORTED_SYMBOLS",
+           "linear_chunk_fwd", "linear_chunk_fwd_workspace_size", "linear_chunk_bwd", "linear_chunk_bwd_workspace_size",
            "linear_recurrent_step", "cache_copy", "cache_fork", "cache_free", "cache_compact"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 EXPORTED_SYMBOLS = ("kda_chunk_fwd_workspace_size", "kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_recurrent_step",
                     "kda_recurrent_replay", "kda_status_string", "kda_last_error_message",
+                    "kda_linear_chunk_fwd_workspace_size", "kda_linear_chunk_fwd",
+                    "kda_linear_chunk_bwd_workspace_size", "kda_linear_chunk_bwd",
                     "kda_linear_recurrent_step", "kda_cache_copy", "kda_cache_fork", "kda_cache_free",
                     "kda_cache_compact")
 
@@ -145,6 +148,29 @@ class Fusion:
         return self.conv_weight is not None
 
 
+class LinearFwdArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("Dk", ctypes.c_int32), ("Dv", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("g", ctypes.c_void_p), ("g_per_head", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("cu_seqlens", ctypes.c_void_p), ("N", ctypes.c_int32), ("initial_state", ctypes.c_void_p),
+                ("o", ctypes.c_void_p), ("final_state", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("checkpoints", ctypes.c_void_p),
+                ("checkpoint_every", ctypes.c_int32), ("checkpoint_slots", ctypes.c_int32)]
+
+
+class LinearBwdArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("Dk", ctypes.c_int32), ("Dv", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("g", ctypes.c_void_p), ("g_per_head", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("cu_seqlens", ctypes.c_void_p), ("N", ctypes.c_int32), ("initial_state", ctypes.c_void_p),
+                ("d_o", ctypes.c_void_p), ("d_final_state", ctypes.c_void_p),
+                ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), ("dg", ctypes.c_void_p),
+                ("d_initial_state", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 class LinearStepArgs(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32), ("Dk", ctypes.c_int32),
                 ("Dv", ctypes.c_int32), ("dtype", ctypes.c_int32),
@@ -184,6 +210,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     ptr, i32 = ctypes.c_void_p, ctypes.c_int32
     pools = [ctypes.POINTER(CachePool), i32]
     for name, argtypes in (
+            ("kda_linear_chunk_fwd_workspace_size", [ctypes.POINTER(LinearFwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
+            ("kda_linear_chunk_fwd", [ctypes.POINTER(LinearFwdArgs), ptr]),
+            ("kda_linear_chunk_bwd_workspace_size", [ctypes.POINTER(LinearBwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
+            ("kda_linear_chunk_bwd", [ctypes.POINTER(LinearBwdArgs), ptr]),
             ("kda_linear_recurrent_step", [ctypes.POINTER(LinearStepArgs), ptr]),
             ("kda_cache_copy", pools + [i32, i32, ptr, ptr, i32, ptr]),
             ("kda_cache_fork", pools + [i32, ptr, i32, i32, ptr, ptr, ptr, i32, ptr, ptr, ptr]),
@@ -485,4 +515,5 @@ def recurrent_replay(q, k, v, g, beta, state, *, replay=None, n_replay=None, n_c
 
 # Re-exported last: these modules build on the helpers above.
 from .cache import cache_compact, cache_copy, cache_fork, cache_free  # noqa: E402
-from .linear import linear_recurrent_step  # noqa: E402
+from .linear import (linear_chunk_bwd, linear_chunk_bwd_workspace_size, linear_chunk_fwd,  # noqa: E402
+                     linear_chunk_fwd_workspace_size, linear_recurrent_step)

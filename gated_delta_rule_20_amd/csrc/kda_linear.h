@@ -22,6 +22,48 @@ struct LinearStepParams {
 
 hipError_t launch_linear_step(int bf16, int Dk, int Dv, const LinearStepParams &p, hipStream_t stream);
 
+// Whole sequences.  q, k, v name the walk's operands (see kda_linear_chunk.hip).
+struct LinearChunkParams {
+    const void *q, *k, *v;
+    const float *g;                   // [rows, H], or [H] when g_per_head
+    int g_per_head;
+    float scale;
+    const int32_t *cu;                // [N + 1] or null
+    int N, T, rows;                   // sequences; tokens per sequence (all rows when cu); rows
+    int H, group;                     // value heads; value heads per query / key head
+    int seg, n_seg;                   // tokens per segment, segments at most
+    const float *h0;                  // [N, H, Dk, Dv] or null
+    float *hT;                        // [N, H, Dk, Dv] or null
+    void *o;
+    float *part, *dec;                // [n_part, H, Dk, Dv] and [n_part, H] of the first pass, or null: no pass
+    int n_part;
+    int defer;                        // entering and resulting states share memory, and there is a first pass
+    float *ckpt;                      // [N, ckpt_slots, H, Dk, Dv] or null
+    int ckpt_every, ckpt_slots;
+    // backward
+    const void *q_rows;               // q, for y
+    float *y;                         // [rows, H] or null
+    float *anchors;                   // [n_anchors (+ N), H, Dk, Dv] or null: states every anchor_tokens
+    int anchor_tokens, n_anchors;     // anchor_tokens divides seg
+    int anchor_end;                   // the sequences' last states are kept too, behind the others
+    int wide;                         // dq, dk as float32 per value head
+};
+
+struct LinearBwdParams {
+    LinearChunkParams c;
+    const void *d_o;
+    const float *dhT;
+    float *dh0;
+    void *dq, *dk, *dv;               // dq, dk: float32 [rows, H, Dk] when c.wide
+    void *dq_out, *dk_out;            // then their sums over the value heads of a query / key head
+    float *dg;                        // or null
+    double *dg_part;                  // [n_seg, H] when g_per_head
+    float *part_fwd, *dec_fwd;        // the forward states' first pass (c.part, c.dec: the gradients')
+};
+
+hipError_t launch_linear_fwd(int bf16, int Dk, int Dv, const LinearChunkParams &p, hipStream_t stream);
+hipError_t launch_linear_bwd(int bf16, int Dk, int Dv, const LinearBwdParams &p, hipStream_t stream);
+
 // One pool of pages; unit: widest access (16, 4, 2 or 1 bytes) that its base
 // addresses and page size allow.
 struct CachePool {

@@ -46,6 +46,12 @@ kda_status_t check_decay(const float *g)
     return KDA_SUCCESS;
 }
 
+bool overlap(const void *a, const void *b, size_t bytes)
+{
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + bytes && y < x + bytes;
+}
+
 kda_status_t plan_pools(const kda_cache_pool_t *pools, int n, bool two, kda::CachePools *out)
 {
     out->n = 0;
@@ -100,6 +106,151 @@ kda_status_t check_grid(const kda::CachePools &pools, long long pages)
     return KDA_SUCCESS;
 }
 
+// Tokens per segment and what the workspace holds.  A sequence is cut only
+// where its (sequence, head) pairs leave compute units idle: about SEGMENTS
+// segments in all keep two workgroups on each of the 256 units, and a segment is at least MIN_SEGMENT
+// tokens, so that the first pass stays cheaper than the walk it shortens.
+constexpr int MIN_SEGMENT = 256, SEGMENTS = 512, ANCHOR = 512;
+
+struct LinearPlan {
+    int N, rows, seg, anchor, n_seg, n_part, n_anchors;
+    bool first_pass;
+};
+
+struct LinearShape {
+    int32_t B, T, H, Hk, Dk, Dv, dtype;
+    const int32_t *cu;
+    int32_t N;
+    float scale;
+};
+
+kda_status_t plan_linear(const LinearShape &a, LinearPlan *pl)
+{
+    const kda_status_t st = check_heads(a.dtype, a.H, a.Hk, a.Dk, a.Dv, a.scale);
+    if (st != KDA_SUCCESS) return st;
+    if (a.B < 1 || a.T < 0) return fail(KDA_ERROR_INVALID_VALUE, "need B >= 1, T >= 0 (got B=%d T=%d)", a.B, a.T);
+    if (a.cu) {
+        if (a.B != 1) return fail(KDA_ERROR_INVALID_VALUE, "cu_seqlens requires B == 1 (got B=%d)", a.B);
+        if (a.N < 1) return fail(KDA_ERROR_INVALID_VALUE, "cu_seqlens requires N >= 1 (got N=%d)", a.N);
+        if (!aligned4(a.cu)) return fail(KDA_ERROR_INVALID_VALUE, "cu_seqlens is not 4-byte aligned");
+    }
+    const long long rows = (long long)a.B * a.T;
+    pl->N = a.cu ? a.N : a.B;
+    if (rows > 0x7fffffffLL || (long long)pl->N * a.H > 0x0fffffffLL || (long long)a.H * a.Dk > 0x7fffffLL)
+        return fail(KDA_ERROR_NOT_SUPPORTED, "problem too large for 32-bit token/pair indices");
+    pl->rows = (int)rows;
+    long long seg = rows * a.H / SEGMENTS;
+    seg = seg < MIN_SEGMENT ? MIN_SEGMENT : (seg + MIN_SEGMENT - 1) / MIN_SEGMENT * MIN_SEGMENT;
+    if (seg > ANCHOR) seg = (seg + ANCHOR - 1) / ANCHOR * ANCHOR;
+    if (seg > (1 << 30)) seg = 1 << 30;
+    pl->seg = (int)seg;
+    pl->anchor = seg < ANCHOR ? (int)seg : ANCHOR;
+    const auto over = [](int len, int by) { return len <= 0 ? 0 : (len - 1) / by; };  // pieces behind the first
+    const long long n = a.cu ? rows / seg + a.N : (long long)a.B * (over(a.T, pl->seg) + 1);
+    if (n * a.H > 0x7fffffffLL) return fail(KDA_ERROR_NOT_SUPPORTED, "too many segments");
+    pl->n_seg = (int)n;
+    pl->n_part = (int)(a.cu ? rows / seg : (long long)a.B * over(a.T, pl->seg));
+    pl->n_anchors = (int)(a.cu ? rows / pl->anchor : (long long)a.B * over(a.T, pl->anchor));
+    pl->first_pass = over(a.T, pl->seg) > 0;     // packed: some sequence may be that long
+    return KDA_SUCCESS;
+}
+
+struct Carver {
+    size_t used = 0;
+    char *base;
+    explicit Carver(void *b) : base((char *)b) {}
+    void *take(size_t bytes)
+    {
+        const size_t at = used;
+        used += (bytes + 255) / 256 * 256;
+        return base ? base + at : nullptr;
+    }
+};
+
+kda_status_t check_workspace(void *ws, size_t have, size_t need)
+{
+    if (need == 0) return KDA_SUCCESS;
+    if (!ws) return fail(KDA_ERROR_WORKSPACE, "workspace is NULL but %zu bytes are needed", need);
+    if (have < need) return fail(KDA_ERROR_WORKSPACE, "workspace has %zu bytes, needs %zu", have, need);
+    if ((uintptr_t)ws & 255u) return fail(KDA_ERROR_WORKSPACE, "workspace is not 256-byte aligned");
+    return KDA_SUCCESS;
+}
+
+LinearShape shape_of(const kda_linear_fwd_args_t *a)
+{
+    return {a->B, a->T, a->H, a->Hk, a->Dk, a->Dv, a->dtype, a->cu_seqlens, a->N, a->scale};
+}
+LinearShape shape_of(const kda_linear_bwd_args_t *a)
+{
+    return {a->B, a->T, a->H, a->Hk, a->Dk, a->Dv, a->dtype, a->cu_seqlens, a->N, a->scale};
+}
+
+template <typename A> kda::LinearChunkParams chunk_params(const A *a, const LinearPlan &pl)
+{
+    kda::LinearChunkParams p = {};
+    p.q = a->q; p.k = a->k; p.v = a->v; p.g = a->g; p.g_per_head = a->g_per_head != 0;
+    p.scale = a->scale;
+    p.cu = a->cu_seqlens; p.N = pl.N; p.T = a->T; p.rows = pl.rows;
+    p.H = a->H; p.group = a->H / a->Hk;
+    p.seg = pl.seg; p.n_seg = pl.n_seg; p.n_part = pl.n_part;
+    p.anchor_tokens = pl.anchor; p.n_anchors = pl.n_anchors;
+    p.h0 = a->initial_state;
+    return p;
+}
+
+// The first pass's buffers.
+void take_parts(Carver &c, const LinearPlan &pl, int H, size_t state, float **part, float **dec)
+{
+    *part = (float *)c.take(state * pl.n_part);
+    *dec = (float *)c.take(sizeof(float) * (size_t)H * pl.n_part);
+}
+
+size_t plan_fwd(const kda_linear_fwd_args_t *a, const LinearPlan &pl, void *ws, kda::LinearChunkParams *p)
+{
+    Carver c(ws);
+    *p = chunk_params(a, pl);
+    p->hT = a->final_state;
+    p->o = a->o;
+    p->ckpt = a->checkpoints;
+    p->ckpt_every = a->checkpoint_every;
+    p->ckpt_slots = a->checkpoint_slots;
+    const size_t state = sizeof(float) * a->H * a->Dk * a->Dv;
+    if (pl.first_pass) {
+        take_parts(c, pl, a->H, state, &p->part, &p->dec);
+        p->defer = overlap(a->initial_state, a->final_state, state * pl.N);
+    }
+    return c.used;
+}
+
+size_t plan_bwd(const kda_linear_bwd_args_t *a, const LinearPlan &pl, void *ws, kda::LinearBwdParams *b)
+{
+    Carver c(ws);
+    *b = {};
+    b->c = chunk_params(a, pl);
+    b->d_o = a->d_o; b->dhT = a->d_final_state; b->dh0 = a->d_initial_state;
+    b->dq = a->dq; b->dk = a->dk; b->dv = a->dv; b->dg = a->dg;
+    const size_t state = sizeof(float) * a->H * a->Dk * a->Dv;
+    if (pl.first_pass) {
+        take_parts(c, pl, a->H, state, &b->c.part, &b->c.dec);
+        b->c.defer = overlap(a->d_final_state, a->d_initial_state, state * pl.N);
+        take_parts(c, pl, a->H, state, &b->part_fwd, &b->dec_fwd);
+    }
+    if (a->dg) {
+        b->c.y = (float *)c.take(sizeof(float) * (size_t)a->H * pl.rows);
+        b->c.anchor_end = a->d_final_state != nullptr;
+        b->c.anchors = (float *)c.take(state * ((size_t)pl.n_anchors + (b->c.anchor_end ? pl.N : 0)));
+        if (a->g_per_head) b->dg_part = (double *)c.take(sizeof(double) * (size_t)a->H * pl.n_seg);
+    }
+    if (a->H != a->Hk) {
+        const size_t bytes = sizeof(float) * (size_t)pl.rows * a->H * a->Dk;
+        b->c.wide = 1;
+        b->dq_out = a->dq; b->dk_out = a->dk;
+        b->dq = c.take(bytes);
+        b->dk = c.take(bytes);
+    }
+    return c.used;
+}
+
 }  // namespace
 
 #define KDA_TRY(x)                              \
@@ -109,6 +260,74 @@ kda_status_t check_grid(const kda::CachePools &pools, long long pages)
     } while (0)
 
 extern "C" {
+
+kda_status_t kda_linear_chunk_fwd_workspace_size(const kda_linear_fwd_args_t *a, size_t *bytes)
+{
+    if (!a || !bytes) return fail(KDA_ERROR_INVALID_VALUE, "args or bytes is NULL");
+    LinearPlan pl;
+    KDA_TRY(plan_linear(shape_of(a), &pl));
+    kda::LinearChunkParams p;
+    *bytes = plan_fwd(a, pl, nullptr, &p);
+    return ok();
+}
+
+kda_status_t kda_linear_chunk_fwd(const kda_linear_fwd_args_t *a, void *stream)
+{
+    if (!a) return fail(KDA_ERROR_INVALID_VALUE, "args is NULL");
+    LinearPlan pl;
+    KDA_TRY(plan_linear(shape_of(a), &pl));
+    if (pl.rows > 0) {
+        KDA_TRY(check_decay(a->g));
+        const Ptr req[] = {{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->o, "o"}};
+        KDA_TRY(check_required(req, 4));
+    }
+    if (!aligned16(a->initial_state)) return fail(KDA_ERROR_INVALID_VALUE, "initial_state is not 16-byte aligned");
+    if (!aligned16(a->final_state)) return fail(KDA_ERROR_INVALID_VALUE, "final_state is not 16-byte aligned");
+    if (a->checkpoints) {
+        if (!aligned16(a->checkpoints)) return fail(KDA_ERROR_INVALID_VALUE, "checkpoints is not 16-byte aligned");
+        if (a->checkpoint_every < 1 || a->checkpoint_slots < 1 || a->checkpoint_every > 0x1ffffff)
+            return fail(KDA_ERROR_INVALID_VALUE, "need 1 <= checkpoint_every < 2^25 and checkpoint_slots >= 1 (got %d, %d)",
+                        a->checkpoint_every, a->checkpoint_slots);
+    }
+    kda::LinearChunkParams p;
+    KDA_TRY(check_workspace(a->workspace, a->workspace_bytes, plan_fwd(a, pl, a->workspace, &p)));
+    if (pl.rows == 0 && !a->final_state) return ok();
+    const hipError_t e = kda::launch_linear_fwd(a->dtype == KDA_BF16, a->Dk, a->Dv, p, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "kda_linear_chunk_fwd launch");
+    return ok();
+}
+
+kda_status_t kda_linear_chunk_bwd_workspace_size(const kda_linear_bwd_args_t *a, size_t *bytes)
+{
+    if (!a || !bytes) return fail(KDA_ERROR_INVALID_VALUE, "args or bytes is NULL");
+    LinearPlan pl;
+    KDA_TRY(plan_linear(shape_of(a), &pl));
+    kda::LinearBwdParams b;
+    *bytes = plan_bwd(a, pl, nullptr, &b);
+    return ok();
+}
+
+kda_status_t kda_linear_chunk_bwd(const kda_linear_bwd_args_t *a, void *stream)
+{
+    if (!a) return fail(KDA_ERROR_INVALID_VALUE, "args is NULL");
+    LinearPlan pl;
+    KDA_TRY(plan_linear(shape_of(a), &pl));
+    if (pl.rows > 0) {
+        KDA_TRY(check_decay(a->g));
+        const Ptr req[] = {{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->d_o, "d_o"}, {a->dq, "dq"}, {a->dk, "dk"}, {a->dv, "dv"}};
+        KDA_TRY(check_required(req, 7));
+    }
+    if (!aligned4(a->dg)) return fail(KDA_ERROR_INVALID_VALUE, "dg is not 4-byte aligned");
+    if (!aligned16(a->initial_state)) return fail(KDA_ERROR_INVALID_VALUE, "initial_state is not 16-byte aligned");
+    if (!aligned16(a->d_final_state)) return fail(KDA_ERROR_INVALID_VALUE, "d_final_state is not 16-byte aligned");
+    if (!aligned16(a->d_initial_state)) return fail(KDA_ERROR_INVALID_VALUE, "d_initial_state is not 16-byte aligned");
+    kda::LinearBwdParams b;
+    KDA_TRY(check_workspace(a->workspace, a->workspace_bytes, plan_bwd(a, pl, a->workspace, &b)));
+    if (pl.rows == 0 && !a->d_initial_state && !(a->dg && a->g_per_head)) return ok();
+    const hipError_t e = kda::launch_linear_bwd(a->dtype == KDA_BF16, a->Dk, a->Dv, b, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "kda_linear_chunk_bwd launch");
+    return ok();
+}
 
 kda_status_t kda_linear_recurrent_step(const kda_linear_step_args_t *a, void *stream)
 {

@@ -1,0 +1,944 @@
+// kda_linear_chunk.hip -- linear attention with a decay per head over whole
+// sequences, forward and backward, in the chunkwise-parallel form.
+//
+// With G the inclusive sum of log-decays inside a chunk, D_rs = e^{G_r - G_s} for s <= r,
+// and S the state that enters the chunk:
+//   O      = scale * ((Q K^T . D) V + e^G . (Q S))
+//   S_next = e^{G_end} S + (e^{G_end - G} . K)^T V
+// The gradients are the same product with other operands.  dQ walks the chunks
+// forwards with (dO, V, K) in place of (Q, K, V) and the state transposed:
+//   dQ = scale * ((dO V^T . D) K + e^G . (dO S^T))
+// dV and dK walk them backwards (D_rs = e^{G_s - G_r} for s >= r) with (K, Q, dO) and
+// (V, dO, Q), carrying dS, the gradient of the state that leaves the chunk:
+//   dV = scale * (K Q^T . D) dO + e^{G_end - G} . (K dS),  dK = scale * (V dO^T . D) Q + e^{G_end - G} . (V dS^T)
+//   dS_prev = e^{G_end} dS + scale * (e^G . Q)^T dO
+// so one set of building blocks with an operand "Q" of the output rows r, an
+// operand "K" of the source rows s, the values "V" and a state [rows of K, columns of V] serves
+// all of them.
+//
+// The decay of a token pair is formed from differences of G held as two floats
+// (sum in float64), so it neither overflows nor loses its small value next to a
+// large |G|; it is at most 1.
+//
+// A sequence is walked in order by one workgroup with the state in registers,
+// so its traffic is its inputs and outputs.  Where sequences are few, they are
+// cut into segments: a first pass walks every segment from a zero state (reading
+// K and V only) and leaves its contribution; the second starts each segment from
+// the sum of those before it.  That trades half again the traffic for as many workgroups as
+// the chip holds.
+//
+// Roundings: operands of the matrix cores are bf16 for bf16 inputs.  What the state adds
+// (decayed V) enters as three bf16 terms, which together hold all 24 bits, so states are exact to
+// float32 over any length; the decayed scores and the state as an operand of the outputs are rounded
+// once to bf16, as the output is.  The state as an operand of dg's terms keeps three terms too.
+#include "kda_common.h"
+#include "kda_linear.h"
+
+namespace kda {
+
+template <typename T> constexpr int chunk_of = sizeof(T) == 2 ? 64 : 32;  // tokens per chunk
+// LDS row lengths: 32 bytes (bf16) or 16 bytes (fp32) of padding keep the transposing and the row reads off
+// one another's banks.
+template <typename T> __host__ __device__ constexpr int ld_of(int d) { return d + (sizeof(T) == 2 ? 16 : 4); }
+template <typename T> constexpr int ldp_of = chunk_of<T> + (sizeof(T) == 2 ? 8 : 4);
+template <typename T> constexpr int split_of = sizeof(T) == 2 ? 3 : 1;    // operand terms that hold a float32
+
+typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
+
+// Fragment whose k-axis is the rows of a row-major LDS tile: value e of lane
+// (x, g) is tile[k0 + kmap(g, e)][base + step * (x / 4) + x % 4].  bf16 uses the
+// transposing LDS read: each lane names 4 elements of a row, and lane x of a 16-lane group receives column x of
+// the 4 x 16 block the group named.
+__device__ __forceinline__ bf16x8 col_frag(const bf16 *tile, int ld, int k0, int base, int step)
+{
+    const int l = lane_id(), x = l & 15, g = l >> 4;
+    typedef __attribute__((address_space(3))) bf16x4v *lds_ptr;
+    const bf16 *p = tile + (k0 + 4 * g + (x >> 2)) * ld + base + step * (x & 3);
+    const bf16x4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)p);
+    const bf16x4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)(p + 16 * ld));
+    bf16x8 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { f[i] = lo[i]; f[4 + i] = hi[i]; }
+    return f;
+}
+__device__ __forceinline__ f32x8 col_frag(const float *tile, int ld, int k0, int base, int step)
+{
+    const int l = lane_id(), x = l & 15, g = l >> 4;
+    f32x8 f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = tile[(k0 + kmap(g, e)) * ld + base + step * (x >> 2) + (x & 3)];
+    return f;
+}
+
+// x as a sum of NS operand fragments.
+template <int NS> __device__ __forceinline__ void split(const float *x, bf16x8 *f)
+{
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = x[e];
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[n][e] = (bf16)r[e];
+            r[e] -= (float)f[n][e];
+        }
+}
+template <int NS> __device__ __forceinline__ void split(const float *x, f32x8 *f)
+{
+    static_assert(NS == 1, "float operands need no terms");
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[0][e] = x[e];
+}
+
+// One chunk tile [C][D] on its way from global memory to LDS, NT threads.
+template <typename T, int D, int NT> struct Stage {
+    static constexpr int C = chunk_of<T>, PER = 16 / sizeof(T), ROW = D / PER, N = C * ROW / NT;
+    static_assert(N * NT == C * ROW, "tile divides evenly");
+    f32x4 r[N];
+    // rows [0, n) of base, `stride` elements apart; the others are zero
+    __device__ __forceinline__ void load(const T *base, size_t stride, int n, int t)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = t + i * NT, row = e / ROW;
+            r[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (row < n) r[i] = *reinterpret_cast<const f32x4 *>(base + (size_t)row * stride + (e % ROW) * PER);
+        }
+    }
+    __device__ __forceinline__ void store(T *tile, int t) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = t + i * NT;
+            *reinterpret_cast<f32x4 *>(tile + (e / ROW) * ld_of<T>(D) + (e % ROW) * PER) = r[i];
+        }
+    }
+};
+
+// Decay vectors of one chunk.
+template <int C> struct Decay {
+    float hi[C], lo[C];      // G in units of log 2, as hi + lo
+    float inter[C];          // factor of the state's part of output row r
+    float state[C];          // factor of source row s in the state
+    float total;             // e^{G_end}
+};
+
+// One wave: lane u holds the log-decay x of token u (0 behind the chunk's last).
+template <int C, bool REV> __device__ __forceinline__ void make_decay(Decay<C> *d, float x, float scale)
+{
+    const int u = lane_id();
+    double G = u < C ? (double)x : 0.0;
+#pragma unroll
+    for (int s = 1; s < C; s *= 2) {
+        const double y = __shfl_up(G, s);
+        if (u >= s) G += y;
+    }
+    const double end = __shfl(G, C - 1);
+    const float in = __builtin_amdgcn_exp2f((float)G), out = __builtin_amdgcn_exp2f((float)(end - G));
+    if (u < C) {
+        const float hi = (float)G;
+        d->hi[u] = hi;
+        d->lo[u] = (float)(G - (double)hi);
+        d->inter[u] = REV ? out : scale * in;
+        d->state[u] = REV ? scale * in : out;
+    }
+    if (u == C - 1) d->total = in;
+}
+
+__device__ __forceinline__ double wave_total(double v)
+{
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
+    return v;
+}
+
+// The work of four waves on one chunk: output columns (and state columns) are
+// dealt 16 * NCT to a wave.  DK: contracted width, DV: output width.
+template <typename T, int DK, int DV, bool REV> struct Group {
+    static constexpr int C = chunk_of<T>, NT = C / 16, NRT = DK / 16, NCT = DV / 64, KS = DK / 32, CK = C / 32;
+    static constexpr int LDK = ld_of<T>(DK), LDV = ld_of<T>(DV), LDP = ldp_of<T>;
+
+    // With two column tiles a lane's rows of both tiles are made neighbours (8 columns: one wide access).
+    static __device__ __forceinline__ int col0(int w, int ct) { return NCT == 2 ? 32 * w + 4 * ct : 16 * w; }
+    static constexpr int STEP = NCT == 2 ? 8 : 4;
+
+    // ---- state, accumulator layout: value i of lane (x, g) in tile [rt][ct] is S[16 rt + 4 g + i][column x of ct]
+    f32x4 S[NRT][NCT];
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    // S = f * S + m, m in memory as [DK][DV], or [DV][DK] when TR
+    template <bool TR> __device__ __forceinline__ f32x4 fetch(const float *m, int w, int rt, int ct) const
+    {
+        const int l = lane_id(), x = l & 15, g = l >> 4;
+        const int col = col0(w, ct) + STEP * (x >> 2) + (x & 3), row = 16 * rt + 4 * g;
+        if (TR) return *reinterpret_cast<const f32x4 *>(m + (size_t)col * DK + row);
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = m[(size_t)(row + i) * DV + col];
+        return v;
+    }
+    template <bool TR> __device__ __forceinline__ void add(const float *m, float f, int w)
+    {
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = S[rt][ct] * f + fetch<TR>(m, w, rt, ct);
+    }
+    template <bool TR> __device__ __forceinline__ void put(float *m, int w) const
+    {
+        const int l = lane_id(), x = l & 15, g = l >> 4;
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                const int col = col0(w, ct) + STEP * (x >> 2) + (x & 3), row = 16 * rt + 4 * g;
+                if (TR)
+                    *reinterpret_cast<f32x4 *>(m + (size_t)col * DK + row) = S[rt][ct];
+                else
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m[(size_t)(row + i) * DV + col] = S[rt][ct][i];
+            }
+    }
+    template <bool TR> __device__ __forceinline__ double dot(const float *m, int w) const
+    {
+        double s = 0.0;
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                const f32x4 y = fetch<TR>(m, w, rt, ct);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s += (double)S[rt][ct][i] * (double)y[i];
+            }
+        return wave_total(s);
+    }
+
+    // The chunk's addition to the state.
+    __device__ __forceinline__ void update(const T *K, const T *V, const Decay<C> &d, int w)
+    {
+        constexpr int NS = split_of<T>;
+        const int g = lane_id() >> 4;
+        const float f = d.total;
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] *= f;
+#pragma unroll
+        for (int ks = 0; ks < CK; ++ks) {
+            frag_t<T> vf[NCT][NS];
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(&d.state[32 * ks + 4 * g]);
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(&d.state[32 * ks + 16 + 4 * g]);
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                const frag_t<T> v = col_frag(V, LDV, 32 * ks, col0(w, ct), STEP);
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { x[e] = to_f<T>(v[e]) * a[e]; x[4 + e] = to_f<T>(v[4 + e]) * b[e]; }
+                split<NS>(x, vf[ct]);
+            }
+#pragma unroll
+            for (int rt = 0; rt < NRT; ++rt) {
+                const frag_t<T> kf = col_frag(K, LDK, 32 * ks, 16 * rt, 4);
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) S[rt][ct] = mma(kf, vf[ct][n], S[rt][ct]);
+            }
+        }
+    }
+
+    // Raw scores of tile (source rows st, output rows rt): value i of lane (x, g) belongs to s = 16 st + 4 g + i, r = 16 rt + x.
+    static __device__ __forceinline__ f32x4 scores(const T *Q, const T *K, int rt, int st)
+    {
+        const int l = lane_id(), x = l & 15, g = l >> 4;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            acc = mma(load_frag_kmap<T>(K + (16 * st + x) * LDK + 32 * ks, g),
+                      load_frag_kmap<T>(Q + (16 * rt + x) * LDK + 32 * ks, g), acc);
+        return acc;
+    }
+    // scale * D of the same tile, 0 where s is not a source of r.
+    static __device__ __forceinline__ f32x4 weights(const Decay<C> &d, float scale, int rt, int st)
+    {
+        const int l = lane_id(), x = l & 15, g = l >> 4;
+        const int r = 16 * rt + x, s = 16 * st + 4 * g;
+        const float rh = d.hi[r], rl = d.lo[r];
+        const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[s]), sl = *reinterpret_cast<const f32x4 *>(&d.lo[s]);
+        f32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float y = REV ? (sh[i] - rh) + (sl[i] - rl) : (rh - sh[i]) + (rl - sl[i]);
+            o[i] = (REV ? s + i >= r : s + i <= r) ? scale * __builtin_amdgcn_exp2f(y) : 0.f;
+        }
+        return o;
+    }
+    static __device__ __forceinline__ bool reached(int rt, int st) { return REV ? st >= rt : st <= rt; }
+
+    // Decayed scores into P[r][s] (rounded to T), tiles dealt to the four waves.
+    static __device__ __forceinline__ void make_scores(T *P, const T *Q, const T *K, const Decay<C> &d, float scale, int w)
+    {
+        const int l = lane_id(), x = l & 15, g = l >> 4;
+#pragma unroll
+        for (int i = 0; i < NT * NT / 4; ++i) {
+            const int tile = w + 4 * i, rt = tile % NT, st = tile / NT;
+            f32x4 p = {0.f, 0.f, 0.f, 0.f};
+            if (reached(rt, st)) {
+                p = scores(Q, K, rt, st);
+                const f32x4 c = weights(d, scale, rt, st);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = c[e] != 0.f ? p[e] * c[e] : 0.f;
+            }
+            *reinterpret_cast<quad_t<T> *>(P + (16 * rt + x) * LDP + 16 * st + 4 * g) = make_quad<T>(p);
+        }
+    }
+
+    // The state's part of the outputs: O[it][ct], value i of lane (x, g) is output column 4 g + i of ct, row 16 it + x.
+    template <int NS> __device__ __forceinline__ void inter(f32x4 (&O)[NT][NCT], const T *Q, const Decay<C> &d) const
+    {
+        const int l = lane_id(), x = l & 15, g = l >> 4;
+#pragma unroll
+        for (int it = 0; it < NT; ++it)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) O[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            frag_t<T> sf[NCT][NS];
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { y[e] = S[2 * ks][ct][e]; y[4 + e] = S[2 * ks + 1][ct][e]; }
+                split<NS>(y, sf[ct]);
+            }
+#pragma unroll
+            for (int it = 0; it < NT; ++it) {
+                const frag_t<T> qf = load_frag_kmap<T>(Q + (16 * it + x) * LDK + 32 * ks, g);
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) O[it][ct] = mma(sf[ct][n], qf, O[it][ct]);
+            }
+        }
+#pragma unroll
+        for (int it = 0; it < NT; ++it) {
+            const float f = d.inter[16 * it + x];
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) O[it][ct] *= f;
+        }
+    }
+
+    // The chunk's own part of the outputs.
+    static __device__ __forceinline__ void intra(f32x4 (&O)[NT][NCT], const T *P, const T *V, int w)
+    {
+        const int l = lane_id(), x = l & 15, g = l >> 4;
+#pragma unroll
+        for (int ks = 0; ks < CK; ++ks) {
+            frag_t<T> vf[NCT];
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) vf[ct] = col_frag(V, LDV, 32 * ks, col0(w, ct), STEP);
+#pragma unroll
+            for (int it = 0; it < NT; ++it) {
+                if (!(reached(it, 2 * ks) || reached(it, 2 * ks + 1))) continue;
+                const frag_t<T> pf = load_frag_kmap<T>(P + (16 * it + x) * LDP + 32 * ks, g);
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) O[it][ct] = mma(vf[ct], pf, O[it][ct]);
+            }
+        }
+    }
+
+    // A lane's output columns of row 16 it + x, from `first` on.
+    static __device__ __forceinline__ int first_col(int w)
+    {
+        const int g = lane_id() >> 4;
+        return NCT == 2 ? 32 * w + 8 * g : 16 * w + 4 * g;
+    }
+    template <typename U>
+    static __device__ __forceinline__ void store(U *o, size_t stride, int n, const f32x4 (&O)[NT][NCT], int w)
+    {
+        const int x = lane_id() & 15;
+#pragma unroll
+        for (int it = 0; it < NT; ++it) {
+            if (16 * it + x >= n) continue;
+            U *p = o + (size_t)(16 * it + x) * stride + first_col(w);
+            if constexpr (NCT == 2) {
+                const float y[8] = {O[it][0][0], O[it][0][1], O[it][0][2], O[it][0][3],
+                                    O[it][1][0], O[it][1][1], O[it][1][2], O[it][1][3]};
+                store8(p, make_frag<U>(y));
+            } else {
+                *reinterpret_cast<quad_t<U> *>(p) = make_quad<U>(O[it][0]);
+            }
+        }
+    }
+    // For each row 16 it + x: the sum over this wave's columns of O times m's row (element type T).
+    static __device__ __forceinline__ void row_dots(float *out, const T *m, size_t stride, int n, const f32x4 (&O)[NT][NCT], int w)
+    {
+        const int l = lane_id(), x = l & 15, g = l >> 4;
+#pragma unroll
+        for (int it = 0; it < NT; ++it) {
+            float s = 0.f;
+            if (16 * it + x < n) {
+                const T *p = m + (size_t)(16 * it + x) * stride + first_col(w);
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    const f32x4 y = quad_to_f<T>(*reinterpret_cast<const quad_t<T> *>(p + 4 * ct));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s += O[it][ct][i] * y[i];
+                }
+            }
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            if (g == 0) out[16 * it + x] = s;
+        }
+    }
+};
+
+// ---- which tokens a workgroup walks ----------------------------------------------------------------------------------
+
+struct Piece {
+    int seq, part, parts;     // segment `part` of the sequence's `parts`
+    int begin, len;           // the sequence's first row and its tokens
+    int slot, anchor;         // index of the sequence's first part in the workspace, and of its first anchor
+};
+
+// Segment `id` of all sequences' segments of L tokens (an empty sequence has
+// one), sequence by sequence; false when there are fewer.  A sequence of n
+// segments has n - 1 parts in the workspace (nothing is left by its last one, or
+// first one backwards).  Every wave finds the segment by itself: 64
+// sequences at a time, a prefix sum over the lanes.  L and LA are at least 256, so the sums fit 32 bits unsigned.
+__device__ __forceinline__ int pieces_of(int len, int L) { return len <= 0 ? 1 : (len - 1) / L + 1; }
+
+__device__ __forceinline__ bool find_piece(const LinearChunkParams &p, int id, Piece &w)
+{
+    const int L = p.seg, LA = p.anchor_tokens;
+    if (!p.cu) {
+        w.parts = pieces_of(p.T, L);
+        w.seq = id / w.parts;
+        w.part = id % w.parts;
+        w.begin = w.seq * p.T;
+        w.len = p.T;
+        w.slot = w.seq * (w.parts - 1);
+        w.anchor = w.seq * (pieces_of(p.T, LA) - 1);
+        return w.seq < p.N;
+    }
+    const int lane = lane_id();
+    unsigned before = 0, abefore = 0;
+    for (int s0 = 0; s0 < p.N; s0 += 64) {
+        const int s = s0 + lane;
+        int a = 0, b = 0, n = 0, na = 0;
+        if (s < p.N) {
+            a = min(max(p.cu[s], 0), p.T);
+            b = min(max(p.cu[s + 1], a), p.T);
+            n = pieces_of(b - a, L);
+            na = pieces_of(b - a, LA);
+        }
+        unsigned x = n, y = na;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const unsigned u = __shfl_up(x, d), v = __shfl_up(y, d);
+            if (lane >= d) { x += u; y += v; }
+        }
+        const unsigned long long over = __ballot(before + x > (unsigned)id);
+        if (over) {
+            const int f = __ffsll(over) - 1;
+            w.seq = s0 + f;
+            w.parts = __builtin_amdgcn_readlane(n, f);
+            w.part = (int)((unsigned)id - before - (__builtin_amdgcn_readlane(x, f) - (unsigned)w.parts));
+            w.begin = __builtin_amdgcn_readlane(a, f);
+            w.len = __builtin_amdgcn_readlane(b, f) - w.begin;
+            w.slot = id - w.part - w.seq;
+            w.anchor = (int)(abefore + __builtin_amdgcn_readlane(y, f) - __builtin_amdgcn_readlane(na, f)) - w.seq;
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(x, 63);
+        abefore += __builtin_amdgcn_readlane(y, 63);
+    }
+    return false;
+}
+
+// Where the state at token `pos` of the sequence is kept for dg, or -1.  Offsets
+// that break the rules of cu_seqlens can ask for more than there is room for.
+__device__ __forceinline__ long anchor_at(const LinearChunkParams &p, const Piece &w, int pos)
+{
+    if (pos == w.len) return p.anchor_end ? (long)p.n_anchors + w.seq : -1;
+    if (pos % p.anchor_tokens != 0) return -1;
+    const long i = (long)w.anchor + pos / p.anchor_tokens - 1;
+    return i < p.n_anchors ? i : -1;
+}
+
+// Where the entering and the resulting states are one array, other segments of a
+// sequence may still read its entry when the segment that forms the result is
+// done.  The result then waits in part i of the sequence, which that segment alone reads.
+__device__ __forceinline__ bool deferred(const LinearChunkParams &p, const Piece &w, int i)
+{
+    return p.defer && w.parts > 1 && w.slot + i < p.n_part;
+}
+
+// The log-decay of a chunk's token u for this lane (log 2 units), 0 behind the last.
+__device__ __forceinline__ float fetch_decay(const LinearChunkParams &p, int row, int h, int n)
+{
+    const int u = lane_id();
+    if (u >= n) return 0.f;
+    return log2_decay(p.g_per_head ? p.g[h] : p.g[(size_t)(row + u) * p.H + h]);
+}
+
+enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ };
+
+// One workgroup walks one segment for one value head (head fastest, so that
+// workgroups that run together read neighbouring rows).
+//   WALK_STATE      q, k, v roles: -, k, v;  writes the segment's part and decay
+//   WALK_STATE_REV  -, q, do, backwards
+//   WALK_OUT        q, k, v;  writes o, final state, checkpoints
+//   WALK_DQ         do, v, k (DK = the problem's Dv, DV = its Dk);  writes dq, y, anchors
+// 66 KiB of LDS and up to 256 registers a lane: two workgroups share a compute
+// unit, and one computes while the other waits for memory.
+template <typename T, int DK, int DV, int MODE>
+__global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkParams p)
+{
+    constexpr bool REV = MODE == WALK_STATE_REV, OUT = MODE == WALK_OUT || MODE == WALK_DQ, TR = MODE == WALK_DQ;
+    using G = Group<T, DK, DV, REV>;
+    constexpr int C = G::C;
+    __shared__ __align__(16) T sQ[OUT ? C * G::LDK : 8];
+    __shared__ __align__(16) T sK[C * G::LDK];
+    __shared__ __align__(16) T sV[C * G::LDV];
+    __shared__ __align__(16) T sP[OUT ? C * G::LDP : 8];
+    __shared__ __align__(16) Decay<C> sD[2];
+    __shared__ float sY[MODE == WALK_DQ ? 4 : 1][C];
+
+    const int h = (int)(blockIdx.x % (unsigned)p.H), id = (int)(blockIdx.x / (unsigned)p.H);
+    Piece w;
+    if (!find_piece(p, id, w)) return;
+    if (MODE == WALK_STATE && w.part == w.parts - 1) return;   // nothing comes after it
+    if (MODE == WALK_STATE_REV && w.part == 0) return;
+    const int slot = w.slot + (MODE == WALK_STATE_REV ? w.part - 1 : w.part);
+    if (!OUT && slot >= p.n_part) return;                      // only with offsets that break the rules
+    const int t = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int first = w.part * p.seg, toks = min(p.seg, w.len - first);
+    const int nc = (max(toks, 0) + C - 1) / C;
+    const int row0 = w.begin + first;
+    const int hk = h / p.group, Hk = p.H / p.group;
+    // strides and heads of the three roles
+    constexpr bool QK_SHARED = MODE != WALK_DQ;                // role q / k carry the query / key heads
+    const size_t sq = (size_t)(QK_SHARED ? Hk : p.H) * DK;
+    const size_t sv = (size_t)(QK_SHARED ? p.H : Hk) * DV;
+    const T *gq = (const T *)p.q + (size_t)(QK_SHARED ? hk : h) * DK;
+    const T *gk = (const T *)p.k + (size_t)(QK_SHARED ? hk : h) * DK;
+    const T *gv = (const T *)p.v + (size_t)(QK_SHARED ? h : hk) * DV;
+
+    G grp;
+    grp.clear();
+    const size_t pair = (size_t)w.seq * p.H + h, part_size = (size_t)DK * DV;
+    if (OUT) {
+        if (p.h0) grp.template add<TR>(p.h0 + pair * part_size, 0.f, wv);
+        for (int i = 0; i < w.part; ++i) {
+            if (w.slot + i >= p.n_part) break;
+            const size_t at = (size_t)(w.slot + i) * p.H + h;
+            grp.template add<TR>(p.part + at * part_size, p.dec[at], wv);
+        }
+    }
+    Stage<T, DK, 256> rq, rk;
+    Stage<T, DV, 256> rv;
+    float rg = 0.f, dec = 1.f;
+    auto fetch = [&](int c) {
+        const int row = row0 + c * C, n = min(C, toks - c * C);
+        if (OUT) rq.load(gq + (size_t)row * sq, sq, n, t);
+        rk.load(gk + (size_t)row * sq, sq, n, t);
+        rv.load(gv + (size_t)row * sv, sv, n, t);
+        rg = fetch_decay(p, row, h, n);
+    };
+    if (nc > 0) {
+        fetch(REV ? nc - 1 : 0);
+        if (wv == 0) make_decay<C, REV>(&sD[0], rg, p.scale);
+    }
+    for (int i = 0; i < nc; ++i) {
+        const int c = REV ? nc - 1 - i : i, n = min(C, toks - c * C), row = row0 + c * C;
+        const Decay<C> &d = sD[i & 1];
+        lds_barrier();                                         // the last chunk has been read
+        if (OUT) rq.store(sQ, t);
+        rk.store(sK, t);
+        rv.store(sV, t);
+        lds_barrier();
+        if (i + 1 < nc) fetch(REV ? c - 1 : c + 1);
+        if constexpr (OUT) {
+            f32x4 O[G::NT][G::NCT];
+            G::make_scores(sP, sQ, sK, d, p.scale, wv);
+            if constexpr (MODE == WALK_DQ) {
+                if (p.y) {
+                    grp.template inter<split_of<T>>(O, sQ, d);
+                    G::row_dots(sY[wv], (const T *)p.q_rows + (size_t)row * Hk * DV + (size_t)hk * DV, (size_t)Hk * DV, n, O, wv);
+                } else {
+                    grp.template inter<1>(O, sQ, d);
+                }
+            } else {
+                grp.template inter<1>(O, sQ, d);
+            }
+            if (wv == 0 && i + 1 < nc) make_decay<C, REV>(&sD[(i + 1) & 1], rg, p.scale);
+            lds_barrier();                                     // P (and y) are whole
+            G::intra(O, sP, sV, wv);
+            if (MODE == WALK_DQ && p.wide)
+                G::store((float *)p.o + ((size_t)row * p.H + h) * DV, (size_t)p.H * DV, n, O, wv);
+            else if (MODE == WALK_DQ)
+                G::store((T *)p.o + ((size_t)row * Hk + hk) * DV, (size_t)Hk * DV, n, O, wv);
+            else
+                G::store((T *)p.o + ((size_t)row * p.H + h) * DV, (size_t)p.H * DV, n, O, wv);
+            if (MODE == WALK_DQ && p.y && t < n)
+                p.y[(size_t)(row + t) * p.H + h] = (sY[0][t] + sY[1 % 4][t]) + (sY[2 % 4][t] + sY[3 % 4][t]);
+        } else {
+            if (wv == 0 && i + 1 < nc) make_decay<C, REV>(&sD[(i + 1) & 1], rg, p.scale);
+            dec *= d.total;
+        }
+        grp.update(sK, sV, d, wv);
+        const int pos = first + c * C + n;                     // tokens of the sequence behind this chunk's end
+        if (MODE == WALK_OUT && p.ckpt && n == C && pos < w.len) {
+            const int every = p.ckpt_every * CHUNK;
+            if (pos % every == 0 && pos / every <= p.ckpt_slots)
+                grp.template put<TR>(p.ckpt + (((size_t)w.seq * p.ckpt_slots + pos / every - 1) * p.H + h) * part_size, wv);
+        }
+        if (MODE == WALK_DQ && p.anchors) {
+            const long a = anchor_at(p, w, pos);
+            if (a >= 0) grp.template put<TR>(p.anchors + ((size_t)a * p.H + h) * part_size, wv);
+        }
+    }
+    if (!OUT) {
+        const size_t at = (size_t)slot * p.H + h;
+        grp.template put<TR>(p.part + at * part_size, wv);
+        if (t == 0) p.dec[at] = dec;
+    }
+    if (MODE == WALK_OUT && p.hT && w.part == w.parts - 1)
+        grp.template put<TR>(deferred(p, w, w.parts - 2) ? p.part + ((size_t)(w.slot + w.parts - 2) * p.H + h) * part_size
+                                                         : p.hT + pair * part_size, wv);
+}
+
+// The states that linear_walk_kernel (backwards: linear_dkdv_kernel) deferred, to their place.
+__global__ __launch_bounds__(256) void linear_deferred_kernel(const LinearChunkParams p, float *out, int backwards, int state)
+{
+    const int h = (int)(blockIdx.x % (unsigned)p.H), id = (int)(blockIdx.x / (unsigned)p.H);
+    Piece w;
+    if (!find_piece(p, id, w) || w.part != 0) return;
+    const int i = backwards ? 0 : w.parts - 2;
+    if (!deferred(p, w, i)) return;
+    const f32x4 *src = reinterpret_cast<const f32x4 *>(p.part + ((size_t)(w.slot + i) * p.H + h) * state);
+    f32x4 *dst = reinterpret_cast<f32x4 *>(out + ((size_t)w.seq * p.H + h) * state);
+    for (int e = threadIdx.x; e < state / 4; e += 256) dst[e] = src[e];
+}
+
+// dV (waves 0-3) and dK (waves 4-7) of one segment for one value head, chunks
+// backwards, from one staging of q, k, v and dO; and dg.  With the terms
+//   y_t = q_t . (state part of dq_t)            (from WALK_DQ)
+//   z_s = k_s . (state part of dk_s)
+//   x_ts = scale D_ts (q_t . k_s)(dO_t . v_s),  t > s
+//   w = e^{G_end} <S, dS>                       (S enters, dS leaves the chunk)
+//   dg_u = sum_{t >= u} y_t + sum_{s < u} z_s + sum_{s < u <= t} x_ts + w
+// none of which cancel.  w follows from R = <state, its gradient> at the chunk's end:
+// w = R - sum z, and R at the chunk's start is w + sum y, both in float64; R is formed anew
+// from the state that WALK_DQ left at every anchor, and w is 0 where e^{G_end} < 2^-24 (then w is below the rounding
+// of R), so the roundings of y and z do not pile up.
+template <typename T, int DK, int DV, bool DG>
+__global__ __launch_bounds__(512, 2) void linear_dkdv_kernel(const LinearBwdParams b)
+{
+    const LinearChunkParams &p = b.c;
+    using GV = Group<T, DK, DV, true>;    // rows k, sources q, values dO, state dS
+    using GK = Group<T, DV, DK, true>;    // rows v, sources dO, values q, state dS^T
+    constexpr int C = GV::C, NT = GV::NT, LK = ld_of<T>(DK), LV = ld_of<T>(DV), LP = ldp_of<T>;
+    extern __shared__ __align__(16) char smem[];
+    T *sQ = (T *)smem, *sK = sQ + C * LK, *sV = sK + C * LK, *sO = sV + C * LV, *sP = sO + C * LV;  // sP: two of them
+    Decay<C> *sD = (Decay<C> *)(sP + 2 * C * LP);
+    float *sZ = (float *)(sD + 2);        // [4][C]
+    float *sX = sZ + 4 * C;               // [4][C] sums over s of x, and [4][C] sums over t
+    double *sR = (double *)(sX + 8 * C);  // [4]
+
+    const int h = (int)(blockIdx.x % (unsigned)p.H), id = (int)(blockIdx.x / (unsigned)p.H);
+    Piece w;
+    if (!find_piece(p, id, w)) return;
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), wv = wave & 3;
+    const bool keys = wave >= 4;
+    const int first = w.part * p.seg, toks = min(p.seg, w.len - first);
+    const int nc = (max(toks, 0) + C - 1) / C;
+    const int row0 = w.begin + first;
+    const int hk = h / p.group, Hk = p.H / p.group;
+    const size_t sk = (size_t)Hk * DK, sv = (size_t)p.H * DV;
+    const size_t pair = (size_t)w.seq * p.H + h, part_size = (size_t)DK * DV;
+
+    union States {                        // a wave is of one kind for good
+        GV v;
+        GK k;
+        __device__ States() {}
+    } st;
+    if (keys) st.k.clear(); else st.v.clear();
+    auto add = [&](const float *m, float f) {
+        if (keys) st.k.template add<true>(m, f, wv); else st.v.template add<false>(m, f, wv);
+    };
+    if (b.dhT) add(b.dhT + pair * part_size, 0.f);
+    for (int i = w.parts - 1; i > w.part; --i) {
+        if (w.slot + i - 1 >= p.n_part) continue;
+        const size_t at = (size_t)(w.slot + i - 1) * p.H + h;
+        add(p.part + at * part_size, p.dec[at]);
+    }
+    Stage<T, DK, 512> rq, rk;
+    Stage<T, DV, 512> rv, ro;
+    float rg = 0.f, ry = 0.f;
+    auto fetch = [&](int c) {
+        const int row = row0 + c * C, n = min(C, toks - c * C);
+        rq.load((const T *)p.q + (size_t)row * sk + (size_t)hk * DK, sk, n, t);
+        rk.load((const T *)p.k + (size_t)row * sk + (size_t)hk * DK, sk, n, t);
+        rv.load((const T *)p.v + (size_t)row * sv + (size_t)h * DV, sv, n, t);
+        ro.load((const T *)b.d_o + (size_t)row * sv + (size_t)h * DV, sv, n, t);
+        rg = fetch_decay(p, row, h, n);
+        if (DG) ry = lane_id() < n ? p.y[(size_t)(row + lane_id()) * p.H + h] : 0.f;
+    };
+    if (nc > 0) {
+        fetch(nc - 1);
+        if (wave == 3) make_decay<C, true>(&sD[0], rg, p.scale);
+    }
+    double R = 0.0, sum_dg = 0.0;
+    for (int i = 0; i < nc; ++i) {
+        const int c = nc - 1 - i, n = min(C, toks - c * C), row = row0 + c * C;
+        const int pos = first + c * C + n;
+        const Decay<C> &d = sD[i & 1];
+        const long anchor = DG ? anchor_at(p, w, pos) : -1;
+        lds_barrier();
+        rq.store(sQ, t);
+        rk.store(sK, t);
+        rv.store(sV, t);
+        ro.store(sO, t);
+        const float y = ry;
+        lds_barrier();
+        if (i + 1 < nc) fetch(c - 1);
+        f32x4 OV[NT][GV::NCT], OK[NT][GK::NCT];
+        if (!keys) {
+            GV::make_scores(sP, sK, sQ, d, p.scale, wv);
+            st.v.template inter<1>(OV, sK, d);
+            if (wave == 3 && i + 1 < nc) make_decay<C, true>(&sD[(i + 1) & 1], rg, p.scale);
+        } else {
+            if constexpr (DG) {
+                // as make_scores, with the pair terms x summed along both axes
+                const int l = lane_id(), x = l & 15, g = l >> 4;
+                T *P = sP + C * LP;
+                float over_t = 0.f;
+#pragma unroll
+                for (int j = 0; j < NT * NT / 4; ++j) {
+                    const int tile = wv + 4 * j, rt = tile % NT, s_t = tile / NT;
+                    f32x4 a = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
+                    if (GK::reached(rt, s_t)) {
+                        a = GK::scores(sV, sO, rt, s_t);
+                        const f32x4 qk = GV::scores(sK, sQ, rt, s_t);
+                        const f32x4 cw = GK::weights(d, p.scale, rt, s_t);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            a[e] = cw[e] != 0.f ? a[e] * cw[e] : 0.f;
+                            xs[e] = 16 * s_t + 4 * g + e > 16 * rt + x ? a[e] * qk[e] : 0.f;
+                            over_t += xs[e];
+                        }
+                    }
+                    *reinterpret_cast<quad_t<T> *>(P + (16 * rt + x) * LP + 16 * s_t + 4 * g) = make_quad<T>(a);
+                    // sum over the tile's 16 rows s = this lane group's x
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                        for (int m = 1; m < 16; m *= 2) xs[e] += __shfl_xor(xs[e], m);
+                    }
+                    if (x == 0) *reinterpret_cast<f32x4 *>(sX + wv * C + 16 * s_t + 4 * g) = xs;
+                }
+                over_t += __shfl_xor(over_t, 16);
+                over_t += __shfl_xor(over_t, 32);
+                if (g == 0) sX[4 * C + wv * C + 16 * (wv % NT) + x] = over_t;
+                st.k.template inter<split_of<T>>(OK, sV, d);
+                GK::row_dots(sZ + wv * C, sK, LK, C, OK, wv);
+                if (anchor >= 0) {
+                    const float *m = p.anchors + ((size_t)anchor * p.H + h) * part_size;
+                    const double r = st.k.template dot<true>(m, wv);
+                    if (l == 0) sR[wv] = r;
+                }
+            } else {
+                GK::make_scores(sP + C * LP, sV, sO, d, p.scale, wv);
+                st.k.template inter<1>(OK, sV, d);
+            }
+        }
+        lds_barrier();
+        if (!keys) {
+            GV::intra(OV, sP, sO, wv);
+            GV::store((T *)b.dv + ((size_t)row * p.H + h) * DV, sv, n, OV, wv);
+            st.v.update(sQ, sO, d, wv);
+            if (DG && wave == 3) {
+                const int u = lane_id();
+                float z = 0.f, cx = 0.f;
+                if (u < C) {
+                    z = (sZ[u] + sZ[C + u]) + (sZ[2 * C + u] + sZ[3 * C + u]);
+                    float xt = 0.f, xo;   // x summed over the earlier rows (this token as t), over the later ones (as s)
+                    if (NT == 4) {
+                        xt = (sX[u] + sX[C + u]) + (sX[2 * C + u] + sX[3 * C + u]);
+                        xo = sX[4 * C + (u / 16) * C + u];
+                    } else {
+                        const int q = u / 16;
+                        xt = sX[2 * q * C + u] + sX[(2 * q + 1) * C + u];
+                        xo = sX[4 * C + q * C + u] + sX[4 * C + (q + 2) * C + u];
+                    }
+                    cx = y + xt - xo;
+                }
+                if (anchor >= 0) R = (sR[0] + sR[1]) + (sR[2] + sR[3]);
+                float up = z, down = cx;                       // inclusive sums from below, from above
+#pragma unroll
+                for (int s = 1; s < C; s *= 2) {
+                    const float a = __shfl_up(up, s), e = __shfl_down(down, s);
+                    if (u >= s) up += a;
+                    if (u + s < C) down += e;
+                }
+                const double wt = d.total < 0x1p-24f ? 0.0 : R - wave_total((double)z);
+                R = wt + wave_total(u < C ? (double)y : 0.0);
+                const float dg = down + (up - z) + (float)wt;
+                if (u < n) {
+                    if (p.g_per_head) sum_dg += dg; else b.dg[(size_t)(row + u) * p.H + h] = dg;
+                }
+            }
+        } else {
+            GK::intra(OK, sP + C * LP, sQ, wv);
+            if (p.wide)
+                GK::store((float *)b.dk + ((size_t)row * p.H + h) * DK, (size_t)p.H * DK, n, OK, wv);
+            else
+                GK::store((T *)b.dk + ((size_t)row * Hk + hk) * DK, sk, n, OK, wv);
+            st.k.update(sO, sQ, d, wv);
+        }
+    }
+    if (w.part == 0 && b.dh0 && !keys)
+        st.v.template put<false>(deferred(p, w, 0) ? p.part + ((size_t)w.slot * p.H + h) * part_size
+                                                   : b.dh0 + pair * part_size, wv);
+    if (DG && p.g_per_head && wave == 3) {
+        sum_dg = wave_total(sum_dg);
+        if (t % 64 == 0) b.dg_part[(size_t)id * p.H + h] = sum_dg;
+    }
+}
+
+// dg of constant decays: the segments' sums in order.  One wave per head.
+__global__ __launch_bounds__(64) void linear_dg_heads_kernel(const LinearBwdParams b, int cap)
+{
+    const LinearChunkParams &p = b.c;
+    const int h = (int)blockIdx.x;
+    Piece w;
+    int lo = 0, hi = cap;                 // segments there are: the first id that is none
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (find_piece(p, mid, w)) lo = mid + 1; else hi = mid;
+    }
+    double s = 0.0;
+    for (int i = lane_id(); i < lo; i += 64) s += b.dg_part[(size_t)i * p.H + h];
+    s = wave_total(s);
+    if (lane_id() == 0) b.dg[h] = (float)s;
+}
+
+// Gradients of shared query / key heads: the sum over their value heads, for the rows that sequences cover.
+template <typename T>
+__global__ __launch_bounds__(256) void linear_share_kernel(const LinearChunkParams p, const float *dq, const float *dk, T *oq, T *ok, int DK)
+{
+    int lo = 0, hi = p.rows;
+    if (p.cu) {
+        lo = min(max(p.cu[0], 0), p.T);
+        hi = min(max(p.cu[p.N], lo), p.T);
+    }
+    const int Hk = p.H / p.group, per = DK / 4;
+    const size_t n = (size_t)(hi - lo) * Hk * per;
+    const float *src = blockIdx.y ? dk : dq;
+    T *dst = blockIdx.y ? ok : oq;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+        const size_t head = (size_t)lo * Hk + i / per;         // (row, query / key head)
+        const float *s = src + head * p.group * DK + (i % per) * 4;
+        f32x4 a = *reinterpret_cast<const f32x4 *>(s);
+        for (int j = 1; j < p.group; ++j) a += *reinterpret_cast<const f32x4 *>(s + (size_t)j * DK);
+        *reinterpret_cast<quad_t<T> *>(dst + head * DK + (i % per) * 4) = make_quad<T>(a);
+    }
+}
+
+// ---- launches ----------------------------------------------------------------------------------------------------------
+
+template <typename T, int DK, int DV> static hipError_t fwd_t(const LinearChunkParams &p, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((size_t)p.n_seg * p.H)), block(256);
+    if (p.part) {
+        hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE>), grid, block, 0, stream, p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_OUT>), grid, block, 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !p.defer) return e;
+    hipLaunchKernelGGL(linear_deferred_kernel, grid, block, 0, stream, p, p.hT, 0, DK * DV);
+    return hipGetLastError();
+}
+
+template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdParams &b, hipStream_t stream)
+{
+    const LinearChunkParams &c = b.c;
+    const dim3 grid((unsigned)((size_t)c.n_seg * c.H)), block(256);
+    hipError_t e;
+    LinearChunkParams dq = c;
+    if (c.part) {
+        LinearChunkParams s = c;
+        s.part = b.part_fwd; s.dec = b.dec_fwd;
+        hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE>), grid, block, 0, stream, s);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        s = c;
+        s.k = c.q; s.v = b.d_o;
+        hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE_REV>), grid, block, 0, stream, s);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        dq.part = b.part_fwd; dq.dec = b.dec_fwd;
+    }
+    dq.q = b.d_o; dq.k = c.v; dq.v = c.k; dq.q_rows = c.q; dq.o = b.dq;
+    hipLaunchKernelGGL((linear_walk_kernel<T, DV, DK, WALK_DQ>), grid, block, 0, stream, dq);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    constexpr int C = chunk_of<T>;
+    constexpr size_t lds = sizeof(T) * C * (2 * ld_of<T>(DK) + 2 * ld_of<T>(DV) + 2 * ldp_of<T>) + 2 * sizeof(Decay<C>)
+                           + 12 * C * sizeof(float) + 4 * sizeof(double);
+    static_assert(lds <= 160 * 1024, "one compute unit's LDS");
+    const auto kernel = b.dg ? linear_dkdv_kernel<T, DK, DV, true> : linear_dkdv_kernel<T, DK, DV, false>;
+    // above 64 KiB a kernel asks for its dynamic LDS; per device, so with every launch
+    e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, grid, dim3(512), lds, stream, b);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (c.defer) {
+        hipLaunchKernelGGL(linear_deferred_kernel, grid, block, 0, stream, c, b.dh0, 1, DK * DV);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (b.dg && c.g_per_head) {
+        hipLaunchKernelGGL(linear_dg_heads_kernel, dim3((unsigned)c.H), dim3(64), 0, stream, b, c.n_seg);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (c.wide) {
+        hipLaunchKernelGGL((linear_share_kernel<T>), dim3(2048, 2), dim3(256), 0, stream, c, (const float *)b.dq,
+                           (const float *)b.dk, (T *)b.dq_out, (T *)b.dk_out, DK);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+#define KDA_LINEAR_DISPATCH(FN, ARG)                                              \
+    if (dtype_bf16) {                                                             \
+        if (Dk == 64 && Dv == 64) return FN<bf16, 64, 64>(ARG, stream);           \
+        if (Dk == 64 && Dv == 128) return FN<bf16, 64, 128>(ARG, stream);         \
+        if (Dk == 128 && Dv == 64) return FN<bf16, 128, 64>(ARG, stream);         \
+        if (Dk == 128 && Dv == 128) return FN<bf16, 128, 128>(ARG, stream);       \
+    } else {                                                                      \
+        if (Dk == 64 && Dv == 64) return FN<float, 64, 64>(ARG, stream);          \
+        if (Dk == 64 && Dv == 128) return FN<float, 64, 128>(ARG, stream);        \
+        if (Dk == 128 && Dv == 64) return FN<float, 128, 64>(ARG, stream);        \
+        if (Dk == 128 && Dv == 128) return FN<float, 128, 128>(ARG, stream);      \
+    }                                                                             \
+    return hipErrorInvalidValue;
+
+hipError_t launch_linear_fwd(int dtype_bf16, int Dk, int Dv, const LinearChunkParams &p, hipStream_t stream)
+{
+    KDA_LINEAR_DISPATCH(fwd_t, p)
+}
+
+hipError_t launch_linear_bwd(int dtype_bf16, int Dk, int Dv, const LinearBwdParams &p, hipStream_t stream)
+{
+    KDA_LINEAR_DISPATCH(bwd_t, p)
+}
+
+}  // namespace kda

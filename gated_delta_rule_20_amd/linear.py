@@ -9,7 +9,7 @@ import ctypes
 
 import torch
 
-from . import _DTYPES, LinearStepArgs, _check, _dev, _ptr, _stream, load_library
+from . import _DTYPES, LinearBwdArgs, LinearFwdArgs, LinearStepArgs, _check, _dev, _ptr, _stream, load_library
 
 
 def _on_device(device, **tensors):
@@ -49,6 +49,146 @@ def _heads(q, k, v, g):
     if not (tuple(g.shape) == (H,) if per_head else g.shape == v.shape[:-1]):
         raise ValueError(f"g must be [H] = [{H}] or {tuple(v.shape[:-1])}, got {tuple(g.shape)}")
     return H, Hk, q.shape[-1], v.shape[-1], per_head
+
+
+def _sequences(q, v, cu_seqlens):
+    """(B, T, N) of q [B, T, Hk, Dk], or with cu_seqlens of [T, Hk, Dk] (a leading 1 allowed)."""
+    if cu_seqlens is None:
+        if q.dim() != 4:
+            raise ValueError(f"q must be [B, T, Hk, Dk], got {tuple(q.shape)}")
+        return q.shape[0], q.shape[1], q.shape[0]
+    _dev(cu_seqlens, "cu_seqlens", torch.int32)
+    _on_device(q.device, cu_seqlens=cu_seqlens)
+    if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[0] != 1):
+        raise ValueError(f"with cu_seqlens q must be [T, Hk, Dk], got {tuple(q.shape)}")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError(f"cu_seqlens must be [N + 1] with N >= 1, got {tuple(cu_seqlens.shape)}")
+    return 1, q.shape[-3], cu_seqlens.shape[0] - 1
+
+
+def _state(t, name, shape, device):
+    if t is not None:
+        _dev(t, name, torch.float32)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be [N, H, Dk, Dv] = {shape}, got {tuple(t.shape)}")
+        _on_device(device, **{name: t})
+    return t
+
+
+def _like(t, name, ref, dtype=None):
+    """An output: allocated like ref when not given, checked when given."""
+    if t is None:
+        return torch.empty(ref.shape, dtype=dtype or ref.dtype, device=ref.device)
+    _dev(t, name, dtype or ref.dtype)
+    if t.shape != ref.shape:
+        raise ValueError(f"{name} must have shape {tuple(ref.shape)}, got {tuple(t.shape)}")
+    _on_device(ref.device, **{name: t})
+    return t
+
+
+def _workspace(fn, a, workspace, device):
+    """Sets the workspace the call needs (allocated when not given); returns it so that it outlives the call."""
+    need = _need(fn, a)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        _on_device(device, workspace=workspace)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def linear_chunk_fwd(q, k, v, g, *, scale: float = 1.0, cu_seqlens=None, initial_state=None,
+                     output_final_state: bool = True, out=None, final_state=None, workspace=None, stream=None,
+                     checkpoints=None, checkpoint_every: int = 0):
+    """Forward over whole sequences (``kda_linear_chunk_fwd``).
+
+    q, k: [B, T, Hk, Dk]; v: [B, T, H, Dv] (bf16 or fp32; H a multiple of Hk: value head h reads query / key head
+    h // (H // Hk)); g: log-decays [B, T, H] or [H] fp32.  With cu_seqlens ([N+1] int32 on the device) the token axis is
+    packed: [T, H, D].  initial_state / final_state: [N, H, Dk, Dv] fp32 (may be one tensor).  checkpoints /
+    checkpoint_every as for :func:`chunk_fwd`.  Returns (o, final_state or None)."""
+    H, Hk, Dk, Dv, per_head = _heads(q, k, v, g)
+    B, T, N = _sequences(q, v, cu_seqlens)
+    dev, shape = q.device, (N, H, Dk, Dv)
+    out = _like(out, "out", v)
+    _state(initial_state, "initial_state", shape, dev)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(shape, dtype=torch.float32, device=dev)
+    _state(final_state, "final_state", shape, dev)
+    slots = 0
+    if checkpoints is not None:
+        _dev(checkpoints, "checkpoints", torch.float32)
+        _on_device(dev, checkpoints=checkpoints)
+        if (checkpoints.dim() != 5 or checkpoints.shape[0] != N or checkpoints.shape[1] < 1
+                or tuple(checkpoints.shape[2:]) != shape[1:] or checkpoint_every < 1):
+            raise ValueError(f"checkpoints must be [N, slots >= 1, H, Dk, Dv] with N, H, Dk, Dv = {shape} and "
+                             f"checkpoint_every >= 1; got {tuple(checkpoints.shape)}, every={checkpoint_every}")
+        slots = checkpoints.shape[1]
+    a = LinearFwdArgs(B, T, H, Hk, Dk, Dv, _DTYPES[q.dtype], _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_head, scale,
+                      _ptr(cu_seqlens), N, _ptr(initial_state), _ptr(out), _ptr(final_state), None, 0,
+                      _ptr(checkpoints), checkpoint_every if slots else 0, slots)
+    workspace = _workspace("kda_linear_chunk_fwd_workspace_size", a, workspace, dev)
+    _call("kda_linear_chunk_fwd", (ctypes.byref(a),), stream, dev)
+    return out, final_state
+
+
+def linear_chunk_bwd(q, k, v, g, d_o, *, scale: float = 1.0, cu_seqlens=None, initial_state=None, dfinal_state=None,
+                     need_dg: bool = True, dq=None, dk=None, dv=None, dg=None, dinitial_state=None, workspace=None,
+                     stream=None):
+    """Gradients of :func:`linear_chunk_fwd` (``kda_linear_chunk_bwd``) for the same arguments, given ``d_o`` (shaped
+    like o, in its dtype) and ``dfinal_state`` ([N, H, Dk, Dv] fp32, None: zeros).  Returns (dq, dk, dv, dg, dinitial_state):
+    the first three shaped and typed like q, k, v; dg fp32 shaped like g (None without ``need_dg``)."""
+    H, Hk, Dk, Dv, per_head = _heads(q, k, v, g)
+    B, T, N = _sequences(q, v, cu_seqlens)
+    dev, shape = q.device, (N, H, Dk, Dv)
+    _dev(d_o, "d_o", q.dtype)
+    if d_o.shape != v.shape:
+        raise ValueError(f"d_o must have v's shape {tuple(v.shape)}, got {tuple(d_o.shape)}")
+    _on_device(dev, d_o=d_o)
+    _state(initial_state, "initial_state", shape, dev)
+    _state(dfinal_state, "dfinal_state", shape, dev)
+    dq, dk, dv = _like(dq, "dq", q), _like(dk, "dk", k), _like(dv, "dv", v)
+    dg = _like(dg, "dg", g) if need_dg else None
+    if dinitial_state is None:
+        dinitial_state = torch.empty(shape, dtype=torch.float32, device=dev)
+    _state(dinitial_state, "dinitial_state", shape, dev)
+    a = LinearBwdArgs(B, T, H, Hk, Dk, Dv, _DTYPES[q.dtype], _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_head, scale,
+                      _ptr(cu_seqlens), N, _ptr(initial_state), _ptr(d_o), _ptr(dfinal_state), _ptr(dq), _ptr(dk),
+                      _ptr(dv), _ptr(dg), _ptr(dinitial_state), None, 0)
+    workspace = _workspace("kda_linear_chunk_bwd_workspace_size", a, workspace, dev)
+    _call("kda_linear_chunk_bwd", (ctypes.byref(a),), stream, dev)
+    return dq, dk, dv, dg, dinitial_state
+
+
+def linear_chunk_fwd_workspace_size(q, v, *, cu_seqlens=None) -> int:
+    """Workspace bytes :func:`linear_chunk_fwd` needs for q [B, T, Hk, Dk] (or [T, Hk, Dk] with cu_seqlens) and v."""
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    B, T, N = _sequences(q, v, cu_seqlens)
+    a = LinearFwdArgs(B, T, v.shape[-2], q.shape[-2], q.shape[-1], v.shape[-1], _DTYPES[q.dtype], scale=1.0,
+                      cu_seqlens=_ptr(cu_seqlens), N=N)
+    return _need("kda_linear_chunk_fwd_workspace_size", a)
+
+
+def linear_chunk_bwd_workspace_size(q, v, *, cu_seqlens=None, g_per_head: bool = False, need_dg: bool = True,
+                                    dfinal_state: bool = False) -> int:
+    """Workspace bytes :func:`linear_chunk_bwd` needs; the flags say whether g is [H], whether dg is wanted and whether
+    dfinal_state is given."""
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    B, T, N = _sequences(q, v, cu_seqlens)
+    a = LinearBwdArgs(B, T, v.shape[-2], q.shape[-2], q.shape[-1], v.shape[-1], _DTYPES[q.dtype], scale=1.0,
+                      cu_seqlens=_ptr(cu_seqlens), N=N, g_per_head=g_per_head)
+    a.dg = 16 if need_dg else None             # only whether they are given is read
+    a.d_final_state = 16 if dfinal_state else None
+    return _need("kda_linear_chunk_bwd_workspace_size", a)
+
+
+def _need(fn, a) -> int:
+    lib = load_library()
+    need = ctypes.c_size_t(0)
+    _check(lib, fn, getattr(lib, fn)(ctypes.byref(a), ctypes.byref(need)))
+    return need.value
 
 
 def linear_recurrent_step(q, k, v, g, state, *, scale: float = 1.0, slots=None, new_state=None, out=None, stream=None):

@@ -307,8 +307,77 @@ KDA_API kda_status_t kda_recurrent_replay(const kda_replay_args_t *args, void *s
  *   - Hk query / key heads serve H value heads (H a multiple of Hk): value head
  *     h reads query / key head h / (H / Hk).  Hk = H is the plain layout.
  *   - q and k need no norm bound.
- * Sums, states and decays are held in float32 or more.
+ * Sums, states and decays are held in float32 or more; float32 results
+ * (states, their gradients, dg) are accurate to float32 also for bf16 inputs.
+ * A NaN or infinity among a sequence's tokens can reach the outputs of the
+ * KDA_CHUNK tokens around it, not only those behind it, and no other sequence.
  */
+
+/*
+ * Forward over whole sequences (chunkwise-parallel form):
+ *   q, k : [B, T, Hk, Dk]   v, o : [B, T, H, Dv]   g : [B, T, H] or [H]
+ * cu_seqlens / N, initial_state, final_state and checkpoints exactly as for
+ * kda_chunk_fwd (states [N, H, Dk, Dv] float32; final_state may alias
+ * initial_state).  Rows of o outside every sequence are left as they were.
+ * The workspace (>= kda_linear_chunk_fwd_workspace_size bytes, 256-byte aligned)
+ * holds partial states of sequences that are split over workgroups; its
+ * contents on entry are ignored.
+ */
+typedef struct {
+    int32_t B, T, H, Hk, Dk, Dv;
+    int32_t dtype;                 /* kda_dtype_t */
+    const void *q, *k, *v;
+    const float *g;
+    int32_t g_per_head;            /* 1: g is [H] */
+    float scale;
+    const int32_t *cu_seqlens;
+    int32_t N;
+    const float *initial_state;
+    void *o;
+    float *final_state;
+    void *workspace;
+    size_t workspace_bytes;
+    float *checkpoints;
+    int32_t checkpoint_every;
+    int32_t checkpoint_slots;
+} kda_linear_fwd_args_t;
+
+KDA_API kda_status_t kda_linear_chunk_fwd_workspace_size(const kda_linear_fwd_args_t *args, size_t *bytes);
+KDA_API kda_status_t kda_linear_chunk_fwd(const kda_linear_fwd_args_t *args, void *stream);
+
+/*
+ * Gradients of kda_linear_chunk_fwd for the same q, k, v, g, scale, sequences
+ * and initial_state, given d_o (gradient of o, shaped like it, in the call's
+ * dtype) and d_final_state (gradient of final_state, or NULL for zeros):
+ *   dq, dk : [B, T, Hk, Dk]   dv : [B, T, H, Dv]   (call's dtype, required)
+ *   dg : float32 shaped like g, or NULL if not wanted.  The gradient of a g
+ *        outside its range is that of the value it counts as.
+ *   d_initial_state : [N, H, Dk, Dv] float32, or NULL if not wanted; it may
+ *        alias d_final_state.
+ * Rows of dq, dk, dv and dg outside every sequence are left as they were.
+ * Results do not depend on the order in which workgroups run.
+ */
+typedef struct {
+    int32_t B, T, H, Hk, Dk, Dv;
+    int32_t dtype;                 /* kda_dtype_t */
+    const void *q, *k, *v;
+    const float *g;
+    int32_t g_per_head;
+    float scale;
+    const int32_t *cu_seqlens;
+    int32_t N;
+    const float *initial_state;
+    const void *d_o;
+    const float *d_final_state;
+    void *dq, *dk, *dv;
+    float *dg;
+    float *d_initial_state;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_linear_bwd_args_t;
+
+KDA_API kda_status_t kda_linear_chunk_bwd_workspace_size(const kda_linear_bwd_args_t *args, size_t *bytes);
+KDA_API kda_status_t kda_linear_chunk_bwd(const kda_linear_bwd_args_t *args, void *stream);
 
 /*
  * One token for each of N sequences:

@@ -63,7 +63,7 @@ def backward(q, k, v, g, do, scale, cu, h0=None, dhT=None):
             dg[t] = a[t] * np.einsum("hkv,hkv->h", S[i - 1], dS)
             dS = a[t][:, None, None] * dS
         dh0[s] = dS
-    share = lambda x: x.reshape(R, Hk, H // Hk, -1).sum(2)  # noqa: E731
+    share = lambda x: x.reshape(R, Hk, H // Hk, Dk).sum(2)  # noqa: E731
     return share(dq), share(dk), dv, (dg.sum(0) if np.ndim(g) == 1 else dg), dh0
 
 
@@ -130,3 +130,30 @@ def pages_compact(pools, table, count):
         p = table[j]
         table[j] = moved[p] if 0 <= p < n_pages else -1
     return moved, n
+
+
+# ---- bounds for the chunked form -------------------------------------------------------------------------------------
+#
+# Every result is a sum of products of inputs and decays, so running the same formulas on absolute
+# values bounds the sum of its terms' magnitudes ("mags").  With u = 2^-24:
+#  * float32 arithmetic: a term passes through a sum over the contracted width, one over the chunk and one product and
+#    addition per chunk it is carried (its decay shrinks the error it carries with it); each rounds by u.  The decay of
+#    a token pair is the exponential of a difference of float64 sums held in two floats (2^-22 relative for |G| below
+#    the underflow, with the hardware exponential's error).  ACC counts them: 128 + 64 + 64 plus three a chunk.
+#  * bf16 operands: the decayed score or the state's operand of an output term is rounded once (2^-8).
+#  * the output's own rounding, to its type.
+
+def acc(tokens):
+    return (256 + 16 + 3 * (tokens // 32 + 1)) * 2.0 ** -24
+
+
+def bound(ref, mags, dtype, tokens):
+    """Largest |error| of an output of type dtype, of value ref and term magnitudes mags."""
+    t = mags * (acc(tokens) + (2.0 ** -8 if dtype == torch.bfloat16 else 0.0))
+    return 1.02 * (t + HALF[dtype] * (np.abs(ref) + t)) + 1e-35
+
+
+def rel2(got, ref):
+    """Difference over result in the 2-norm."""
+    n = np.linalg.norm(ref)
+    return float(np.linalg.norm(got - ref) / n) if n else float(np.linalg.norm(got))

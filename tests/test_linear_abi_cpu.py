@@ -153,3 +153,101 @@ def test_binding_requires_device_tensors(lib):
         kda.cache_copy([], None, i, i)
     with pytest.raises(ValueError, match="device tensor"):
         kda.cache_free(i.view(1, 3), i, i)
+
+
+def _fwd_args(**over):
+    a = kda.LinearFwdArgs(B=1, T=1000, H=4, Hk=2, Dk=128, Dv=64, dtype=kda.KDA_BF16, scale=1.0)
+    for f in ("q", "k", "v", "g", "o"):
+        setattr(a, f, 0x10000)
+    a.workspace, a.workspace_bytes = 0x100000, 1 << 40
+    for key, val in over.items():
+        setattr(a, key, val)
+    return a
+
+
+def _bwd_args(**over):
+    a = kda.LinearBwdArgs(B=1, T=1000, H=4, Hk=2, Dk=128, Dv=64, dtype=kda.KDA_BF16, scale=1.0)
+    for f in ("q", "k", "v", "g", "d_o", "dq", "dk", "dv", "dg"):
+        setattr(a, f, 0x10000)
+    a.workspace, a.workspace_bytes = 0x100000, 1 << 40
+    for key, val in over.items():
+        setattr(a, key, val)
+    return a
+
+
+SHAPE_REFUSALS = [
+    (dict(Dk=32), 2, "head dims"),
+    (dict(Dv=100), 2, "head dims"),
+    (dict(dtype=-1), 1, "dtype"),
+    (dict(H=5), 1, "multiple"),
+    (dict(Hk=0), 1, "multiple"),
+    (dict(B=0), 1, "B >= 1"),
+    (dict(T=-1), 1, "T >= 0"),
+    (dict(scale=float("inf")), 1, "scale"),
+    (dict(cu_seqlens=0x20000, B=2, N=1), 1, "B == 1"),
+    (dict(cu_seqlens=0x20000, N=0), 1, "N >= 1"),
+    (dict(cu_seqlens=0x20002, N=1), 1, "cu_seqlens"),
+    (dict(B=1 << 16, T=1 << 16), 2, "too large"),
+    (dict(cu_seqlens=0x20000, N=1 << 28), 2, "too large"),
+]
+
+
+@pytest.mark.parametrize("over,status,msg", SHAPE_REFUSALS + [
+    (dict(q=None), 1, "q is NULL"),
+    (dict(k=0x10008), 1, "k is not 16-byte"),
+    (dict(o=None), 1, "o is NULL"),
+    (dict(g=None), 1, "g is NULL"),
+    (dict(g=0x10002), 1, "g is not 4-byte"),
+    (dict(initial_state=0x10004), 1, "initial_state"),
+    (dict(final_state=0x10004), 1, "final_state"),
+    (dict(checkpoints=0x10004, checkpoint_every=1, checkpoint_slots=1), 1, "checkpoints is not"),
+    (dict(checkpoints=0x10000, checkpoint_every=0, checkpoint_slots=1), 1, "checkpoint_every"),
+    (dict(checkpoints=0x10000, checkpoint_every=1, checkpoint_slots=0), 1, "checkpoint_slots"),
+    (dict(workspace=None), 3, "workspace is NULL"),
+    (dict(workspace_bytes=1024), 3, "needs"),
+    (dict(workspace=0x100010), 3, "256-byte"),
+])
+def test_forward_rejects(lib, over, status, msg):
+    assert lib.kda_linear_chunk_fwd(ctypes.byref(_fwd_args(**over)), None) == status
+    assert msg in _message(lib)
+
+
+@pytest.mark.parametrize("over,status,msg", SHAPE_REFUSALS + [
+    (dict(d_o=None), 1, "d_o is NULL"),
+    (dict(dq=None), 1, "dq is NULL"),
+    (dict(dv=0x10008), 1, "dv is not 16-byte"),
+    (dict(dg=0x10002), 1, "dg is not"),
+    (dict(d_final_state=0x10004), 1, "d_final_state"),
+    (dict(d_initial_state=0x10004), 1, "d_initial_state"),
+    (dict(workspace=None), 3, "workspace is NULL"),
+    (dict(workspace_bytes=1 << 16), 3, "needs"),
+])
+def test_backward_rejects(lib, over, status, msg):
+    assert lib.kda_linear_chunk_bwd(ctypes.byref(_bwd_args(**over)), None) == status
+    assert msg in _message(lib)
+
+
+def test_chunk_null_and_empty(lib):
+    n = ctypes.c_size_t(0)
+    assert lib.kda_linear_chunk_fwd(None, None) == 1 and lib.kda_linear_chunk_bwd(None, None) == 1
+    assert lib.kda_linear_chunk_fwd_workspace_size(None, ctypes.byref(n)) == 1
+    assert lib.kda_linear_chunk_bwd_workspace_size(ctypes.byref(_bwd_args()), None) == 1
+    assert lib.kda_linear_chunk_fwd(ctypes.byref(_fwd_args(T=0, q=None, g=None, o=None, workspace=None)), None) == 0
+
+
+def test_workspace_sizes(lib):
+    """No workspace for sequences that stay whole; otherwise one state per head for every segment that another follows,
+    so that many short sequences need none per sequence."""
+    def size(fn, a):
+        n = ctypes.c_size_t(0)
+        assert getattr(lib, fn)(ctypes.byref(a), ctypes.byref(n)) == 0, _message(lib)
+        return n.value
+    fwd, bwd = "kda_linear_chunk_fwd_workspace_size", "kda_linear_chunk_bwd_workspace_size"
+    assert size(fwd, _fwd_args(T=200)) == 0
+    one = 4 * 4 * 128 * 64                              # a state of every head
+    assert size(fwd, _fwd_args(T=1000)) >= one
+    packed = _fwd_args(T=1 << 20, cu_seqlens=0x20000, N=1 << 16)
+    assert size(fwd, packed) <= ((1 << 20) // 256 + 1) * (one + 4096)
+    assert size(bwd, _bwd_args(T=64, Hk=4, dg=None)) == 0
+    assert size(bwd, _bwd_args(T=64, dg=None)) == 2 * 64 * 4 * 128 * 4    # shared heads: dq, dk per value head
+    assert size(bwd, _bwd_args(T=64, Hk=4)) == 1024                       # y [64, 4]
