@@ -136,7 +136,7 @@ kda_status_t plan_linear(const LinearShape &a, LinearPlan *pl)
     }
     const long long rows = (long long)a.B * a.T;
     pl->N = a.cu ? a.N : a.B;
-    if (rows > 0x7fffffffLL || (long long)pl->N * a.H > 0x0fffffffLL || (long long)a.H * a.Dk > 0x7fffffLL)
+    if (rows > 0x7fffffffLL || (long long)pl->N * a.H > 0x0fffffffLL || a.H > (1 << 15))
         return fail(KDA_ERROR_NOT_SUPPORTED, "problem too large for 32-bit token/pair indices");
     pl->rows = (int)rows;
     long long seg = rows * a.H / SEGMENTS;

@@ -31,6 +31,8 @@
 // (decayed V) enters as three bf16 terms, which together hold all 24 bits, so states are exact to
 // float32 over any length; the decayed scores and the state as an operand of the outputs are rounded
 // once to bf16, as the output is.  The state as an operand of dg's terms keeps three terms too.
+#include <type_traits>
+
 #include "kda_common.h"
 #include "kda_linear.h"
 
@@ -91,28 +93,68 @@ template <int NS> __device__ __forceinline__ void split(const float *x, f32x8 *f
     for (int e = 0; e < 8; ++e) f[0][e] = x[e];
 }
 
+// Global memory is reached through buffer descriptors over uniform bases: a lane
+// then holds one 32-bit offset instead of 64-bit addresses (which were spilled, and a reload
+// from scratch waits for every load in flight), and rows behind a chunk's last are read as zero
+// and not written by the descriptor's bound.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void *base, unsigned bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, bytes, 0x00020000);
+}
+// n >= 1 rows of `width` bytes, `stride` bytes apart
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_window(const void *base, int n, unsigned stride, unsigned width)
+{
+    return window(base, (unsigned)(n - 1) * stride + width);
+}
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f32x4 load16(__amdgpu_buffer_rsrc_t rs, int voff, int soff = 0)
+{
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, voff, soff, 0));
+}
+__device__ __forceinline__ bf16x4 load_quad(const bf16 *, __amdgpu_buffer_rsrc_t rs, int voff)
+{
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(rs, voff, 0, 0));
+}
+__device__ __forceinline__ f32x4 load_quad(const float *, __amdgpu_buffer_rsrc_t rs, int voff) { return load16(rs, voff); }
+__device__ __forceinline__ void store_quad(__amdgpu_buffer_rsrc_t rs, int voff, bf16x4 v)
+{
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), rs, voff, 0, 0);
+}
+__device__ __forceinline__ void store_quad(__amdgpu_buffer_rsrc_t rs, int voff, f32x4 v, int soff = 0)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, voff, soff, 0);
+}
+__device__ __forceinline__ void store_oct(__amdgpu_buffer_rsrc_t rs, int voff, bf16x8 v)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, voff, 0, 0);
+}
+__device__ __forceinline__ void store_oct(__amdgpu_buffer_rsrc_t rs, int voff, f32x8 v)
+{
+    store_quad(rs, voff, f32x4{v[0], v[1], v[2], v[3]});
+    store_quad(rs, voff + 16, f32x4{v[4], v[5], v[6], v[7]});
+}
+
 // One chunk tile [C][D] on its way from global memory to LDS, NT threads.
 template <typename T, int D, int NT> struct Stage {
-    static constexpr int C = chunk_of<T>, PER = 16 / sizeof(T), ROW = D / PER, N = C * ROW / NT;
-    static_assert(N * NT == C * ROW, "tile divides evenly");
+    static constexpr int C = chunk_of<T>, ROW = D * (int)sizeof(T) / 16, N = C * ROW / NT;
+    static_assert(N * NT == C * ROW && NT % ROW == 0, "tile divides evenly");
     f32x4 r[N];
-    // rows [0, n) of base, `stride` elements apart; the others are zero
+    // rows [0, n) of base (n >= 1), `stride` elements apart; the others are zero
     __device__ __forceinline__ void load(const T *base, size_t stride, int n, int t)
     {
+        const unsigned sb = (unsigned)(stride * sizeof(T));
+        const __amdgpu_buffer_rsrc_t rs = rows_window(base, n, sb, D * sizeof(T));
+        const unsigned at = (unsigned)(t / ROW) * sb + (unsigned)(t % ROW) * 16;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = t + i * NT, row = e / ROW;
-            r[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (row < n) r[i] = *reinterpret_cast<const f32x4 *>(base + (size_t)row * stride + (e % ROW) * PER);
-        }
+        for (int i = 0; i < N; ++i) r[i] = load16(rs, (int)(at + (unsigned)(i * (NT / ROW)) * sb));
     }
     __device__ __forceinline__ void store(T *tile, int t) const
     {
+        char *p = (char *)tile + (t / ROW) * (ld_of<T>(D) * (int)sizeof(T)) + (t % ROW) * 16;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = t + i * NT;
-            *reinterpret_cast<f32x4 *>(tile + (e / ROW) * ld_of<T>(D) + (e % ROW) * PER) = r[i];
-        }
+        for (int i = 0; i < N; ++i)
+            *reinterpret_cast<f32x4 *>(p + i * (NT / ROW) * (ld_of<T>(D) * (int)sizeof(T))) = r[i];
     }
 };
 
@@ -173,47 +215,66 @@ template <typename T, int DK, int DV, bool REV> struct Group {
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    // S = f * S + m, m in memory as [DK][DV], or [DV][DK] when TR
-    template <bool TR> __device__ __forceinline__ f32x4 fetch(const float *m, int w, int rt, int ct) const
+    // m in memory as [DK][DV], or [DV][DK] when TR: this lane's offset, and tile (rt, ct)'s row i from there
+    template <bool TR> static __device__ __forceinline__ int state_lane(int w)
     {
-        const int l = lane_id(), x = l & 15, g = l >> 4;
-        const int col = col0(w, ct) + STEP * (x >> 2) + (x & 3), row = 16 * rt + 4 * g;
-        if (TR) return *reinterpret_cast<const f32x4 *>(m + (size_t)col * DK + row);
+        const int l = lane_id(), x = l & 15, g = l >> 4, col = col0(w, 0) + STEP * (x >> 2) + (x & 3);
+        return 4 * (TR ? col * DK + 4 * g : 4 * g * DV + col);
+    }
+    template <bool TR> static constexpr __device__ int state_at(int rt, int ct, int i)
+    {
+        return 4 * (TR ? 4 * ct * DK + 16 * rt : (16 * rt + i) * DV + 4 * ct);
+    }
+    template <bool TR> static __device__ __forceinline__ f32x4 fetch(__amdgpu_buffer_rsrc_t m, int at, int rt, int ct)
+    {
+        if (TR) return load16(m, at, state_at<TR>(rt, ct, 0));
         f32x4 v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = m[(size_t)(row + i) * DV + col];
+        for (int i = 0; i < 4; ++i)
+            v[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(m, at, state_at<TR>(rt, ct, i), 0));
         return v;
     }
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t state_window(const float *m) { return window(m, DK * DV * 4); }
+
+    // S = f * S + m
     template <bool TR> __device__ __forceinline__ void add(const float *m, float f, int w)
     {
+        const __amdgpu_buffer_rsrc_t rs = state_window(m);
+        const int at = state_lane<TR>(w);
 #pragma unroll
         for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = S[rt][ct] * f + fetch<TR>(m, w, rt, ct);
+            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = S[rt][ct] * f + fetch<TR>(rs, at, rt, ct);
     }
     template <bool TR> __device__ __forceinline__ void put(float *m, int w) const
     {
-        const int l = lane_id(), x = l & 15, g = l >> 4;
+        const __amdgpu_buffer_rsrc_t rs = state_window(m);
+        const int at = state_lane<TR>(w);
 #pragma unroll
         for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
-                const int col = col0(w, ct) + STEP * (x >> 2) + (x & 3), row = 16 * rt + 4 * g;
                 if (TR)
-                    *reinterpret_cast<f32x4 *>(m + (size_t)col * DK + row) = S[rt][ct];
+                    store_quad(rs, at, S[rt][ct], state_at<TR>(rt, ct, 0));
                 else
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) m[(size_t)(row + i) * DV + col] = S[rt][ct][i];
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = S[rt][ct][i];          // (a vector's element cannot be bit-cast in place)
+                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), rs, at,
+                                                              state_at<TR>(rt, ct, i), 0);
+                    }
             }
     }
     template <bool TR> __device__ __forceinline__ double dot(const float *m, int w) const
     {
+        const __amdgpu_buffer_rsrc_t rs = state_window(m);
+        const int at = state_lane<TR>(w);
         double s = 0.0;
 #pragma unroll
         for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
-                const f32x4 y = fetch<TR>(m, w, rt, ct);
+                const f32x4 y = fetch<TR>(rs, at, rt, ct);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s += (double)S[rt][ct][i] * (double)y[i];
             }
@@ -250,6 +311,7 @@ template <typename T, int DK, int DV, bool REV> struct Group {
                 for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                     for (int n = 0; n < NS; ++n) S[rt][ct] = mma(kf, vf[ct][n], S[rt][ct]);
+                if (rt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
@@ -297,6 +359,7 @@ template <typename T, int DK, int DV, bool REV> struct Group {
                 for (int e = 0; e < 4; ++e) p[e] = c[e] != 0.f ? p[e] * c[e] : 0.f;
             }
             *reinterpret_cast<quad_t<T> *>(P + (16 * rt + x) * LDP + 16 * st + 4 * g) = make_quad<T>(p);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 
@@ -326,6 +389,7 @@ template <typename T, int DK, int DV, bool REV> struct Group {
 #pragma unroll
                     for (int n = 0; n < NS; ++n) O[it][ct] = mma(sf[ct][n], qf, O[it][ct]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
@@ -351,6 +415,7 @@ template <typename T, int DK, int DV, bool REV> struct Group {
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct) O[it][ct] = mma(vf[ct], pf, O[it][ct]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 
@@ -364,34 +429,35 @@ template <typename T, int DK, int DV, bool REV> struct Group {
     static __device__ __forceinline__ void store(U *o, size_t stride, int n, const f32x4 (&O)[NT][NCT], int w)
     {
         const int x = lane_id() & 15;
+        const unsigned sb = (unsigned)(stride * sizeof(U));
+        const __amdgpu_buffer_rsrc_t rs = rows_window(o, n, sb, DV * sizeof(U));
+        const unsigned at = (unsigned)x * sb + first_col(w) * (unsigned)sizeof(U);
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
-            if (16 * it + x >= n) continue;
-            U *p = o + (size_t)(16 * it + x) * stride + first_col(w);
+            const int p = (int)(at + 16u * it * sb);
             if constexpr (NCT == 2) {
                 const float y[8] = {O[it][0][0], O[it][0][1], O[it][0][2], O[it][0][3],
                                     O[it][1][0], O[it][1][1], O[it][1][2], O[it][1][3]};
-                store8(p, make_frag<U>(y));
+                store_oct(rs, p, make_frag<U>(y));
             } else {
-                *reinterpret_cast<quad_t<U> *>(p) = make_quad<U>(O[it][0]);
+                store_quad(rs, p, make_quad<U>(O[it][0]));
             }
         }
     }
-    // For each row 16 it + x: the sum over this wave's columns of O times m's row (element type T).
-    static __device__ __forceinline__ void row_dots(float *out, const T *m, size_t stride, int n, const f32x4 (&O)[NT][NCT], int w)
+    // For each row 16 it + x: the sum over this wave's columns of O times m's row; m in LDS, or in global memory
+    // (n rows, `stride` elements apart) through `quads`.
+    template <typename F>
+    static __device__ __forceinline__ void row_dots(float *out, F quads, const f32x4 (&O)[NT][NCT])
     {
         const int l = lane_id(), x = l & 15, g = l >> 4;
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
             float s = 0.f;
-            if (16 * it + x < n) {
-                const T *p = m + (size_t)(16 * it + x) * stride + first_col(w);
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    const f32x4 y = quad_to_f<T>(*reinterpret_cast<const quad_t<T> *>(p + 4 * ct));
+            for (int ct = 0; ct < NCT; ++ct) {
+                const f32x4 y = quad_to_f<T>(quads(it, ct));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s += O[it][ct][i] * y[i];
-                }
+                for (int i = 0; i < 4; ++i) s += O[it][ct][i] * y[i];
             }
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
@@ -572,7 +638,13 @@ __global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkPa
             if constexpr (MODE == WALK_DQ) {
                 if (p.y) {
                     grp.template inter<split_of<T>>(O, sQ, d);
-                    G::row_dots(sY[wv], (const T *)p.q_rows + (size_t)row * Hk * DV + (size_t)hk * DV, (size_t)Hk * DV, n, O, wv);
+                    const T *q0 = (const T *)p.q_rows + ((size_t)row * Hk + hk) * DV;
+                    const unsigned sb = (unsigned)(Hk * DV * sizeof(T));
+                    const __amdgpu_buffer_rsrc_t rs = rows_window(q0, n, sb, DV * sizeof(T));
+                    const unsigned at = (unsigned)(t & 15) * sb + G::first_col(wv) * (unsigned)sizeof(T);
+                    G::row_dots(sY[wv], [&](int it, int ct) {
+                        return load_quad(q0, rs, (int)(at + 16u * it * sb + 4u * ct * sizeof(T)));
+                    }, O);
                 } else {
                     grp.template inter<1>(O, sQ, d);
                 }
@@ -640,25 +712,28 @@ __global__ __launch_bounds__(256) void linear_deferred_kernel(const LinearChunkP
 // w = R - sum z, and R at the chunk's start is w + sum y, both in float64; R is formed anew
 // from the state that WALK_DQ left at every anchor, and w is 0 where e^{G_end} < 2^-24 (then w is below the rounding
 // of R), so the roundings of y and z do not pile up.
-template <typename T, int DK, int DV, bool DG>
-__global__ __launch_bounds__(512, 2) void linear_dkdv_kernel(const LinearBwdParams b)
+template <typename T, int DK, int DV> struct DkdvLds {
+    static constexpr int C = chunk_of<T>, LK = ld_of<T>(DK), LV = ld_of<T>(DV), LP = ldp_of<T>;
+    T q[C * LK], k[C * LK], v[C * LV], d_o[C * LV];
+    T p[2][C * LP];           // decayed scores of dV and of dK
+    Decay<C> decay[2];
+    float z[4][C];            // by wave: sums over its columns
+    float x_t[4][C], x_s[4][C];   // by wave: x summed over the earlier rows (token as t), over the later ones (as s)
+    double r[4];              // by wave: <state, gradient> at an anchor
+};
+
+// The walk of one kind of waves; both kinds pass the same barriers.
+template <typename T, int DK, int DV, bool DG, bool KEYS>
+__device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, DK, DV> &s, const Piece &w, int id, int h)
 {
     const LinearChunkParams &p = b.c;
     using GV = Group<T, DK, DV, true>;    // rows k, sources q, values dO, state dS
     using GK = Group<T, DV, DK, true>;    // rows v, sources dO, values q, state dS^T
-    constexpr int C = GV::C, NT = GV::NT, LK = ld_of<T>(DK), LV = ld_of<T>(DV), LP = ldp_of<T>;
-    extern __shared__ __align__(16) char smem[];
-    T *sQ = (T *)smem, *sK = sQ + C * LK, *sV = sK + C * LK, *sO = sV + C * LV, *sP = sO + C * LV;  // sP: two of them
-    Decay<C> *sD = (Decay<C> *)(sP + 2 * C * LP);
-    float *sZ = (float *)(sD + 2);        // [4][C]
-    float *sX = sZ + 4 * C;               // [4][C] sums over s of x, and [4][C] sums over t
-    double *sR = (double *)(sX + 8 * C);  // [4]
-
-    const int h = (int)(blockIdx.x % (unsigned)p.H), id = (int)(blockIdx.x / (unsigned)p.H);
-    Piece w;
-    if (!find_piece(p, id, w)) return;
-    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), wv = wave & 3;
-    const bool keys = wave >= 4;
+    using G = typename std::conditional<KEYS, GK, GV>::type;
+    using L = DkdvLds<T, DK, DV>;
+    constexpr int C = G::C, NT = G::NT;
+    const int t = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(t >> 6) & 3;
+    const bool scribe = !KEYS && wv == 3;                      // forms the decays and dg: wave 3 has the fewest scores
     const int first = w.part * p.seg, toks = min(p.seg, w.len - first);
     const int nc = (max(toks, 0) + C - 1) / C;
     const int row0 = w.begin + first;
@@ -666,20 +741,13 @@ __global__ __launch_bounds__(512, 2) void linear_dkdv_kernel(const LinearBwdPara
     const size_t sk = (size_t)Hk * DK, sv = (size_t)p.H * DV;
     const size_t pair = (size_t)w.seq * p.H + h, part_size = (size_t)DK * DV;
 
-    union States {                        // a wave is of one kind for good
-        GV v;
-        GK k;
-        __device__ States() {}
-    } st;
-    if (keys) st.k.clear(); else st.v.clear();
-    auto add = [&](const float *m, float f) {
-        if (keys) st.k.template add<true>(m, f, wv); else st.v.template add<false>(m, f, wv);
-    };
-    if (b.dhT) add(b.dhT + pair * part_size, 0.f);
+    G grp;
+    grp.clear();
+    if (b.dhT) grp.template add<KEYS>(b.dhT + pair * part_size, 0.f, wv);
     for (int i = w.parts - 1; i > w.part; --i) {
         if (w.slot + i - 1 >= p.n_part) continue;
         const size_t at = (size_t)(w.slot + i - 1) * p.H + h;
-        add(p.part + at * part_size, p.dec[at]);
+        grp.template add<KEYS>(p.part + at * part_size, p.dec[at], wv);
     }
     Stage<T, DK, 512> rq, rk;
     Stage<T, DV, 512> rv, ro;
@@ -690,105 +758,101 @@ __global__ __launch_bounds__(512, 2) void linear_dkdv_kernel(const LinearBwdPara
         rk.load((const T *)p.k + (size_t)row * sk + (size_t)hk * DK, sk, n, t);
         rv.load((const T *)p.v + (size_t)row * sv + (size_t)h * DV, sv, n, t);
         ro.load((const T *)b.d_o + (size_t)row * sv + (size_t)h * DV, sv, n, t);
-        rg = fetch_decay(p, row, h, n);
-        if (DG) ry = lane_id() < n ? p.y[(size_t)(row + lane_id()) * p.H + h] : 0.f;
+        if (scribe) {
+            rg = fetch_decay(p, row, h, n);
+            if (DG) ry = lane_id() < n ? p.y[(size_t)(row + lane_id()) * p.H + h] : 0.f;
+        }
     };
     if (nc > 0) {
         fetch(nc - 1);
-        if (wave == 3) make_decay<C, true>(&sD[0], rg, p.scale);
+        if (scribe) make_decay<C, true>(&s.decay[0], rg, p.scale);
     }
     double R = 0.0, sum_dg = 0.0;
     for (int i = 0; i < nc; ++i) {
         const int c = nc - 1 - i, n = min(C, toks - c * C), row = row0 + c * C;
         const int pos = first + c * C + n;
-        const Decay<C> &d = sD[i & 1];
+        const Decay<C> &d = s.decay[i & 1];
         const long anchor = DG ? anchor_at(p, w, pos) : -1;
-        lds_barrier();
-        rq.store(sQ, t);
-        rk.store(sK, t);
-        rv.store(sV, t);
-        ro.store(sO, t);
+        lds_barrier();                                         // the last chunk has been read
+        rq.store(s.q, t);
+        rk.store(s.k, t);
+        rv.store(s.v, t);
+        ro.store(s.d_o, t);
         const float y = ry;
         lds_barrier();
         if (i + 1 < nc) fetch(c - 1);
-        f32x4 OV[NT][GV::NCT], OK[NT][GK::NCT];
-        if (!keys) {
-            GV::make_scores(sP, sK, sQ, d, p.scale, wv);
-            st.v.template inter<1>(OV, sK, d);
-            if (wave == 3 && i + 1 < nc) make_decay<C, true>(&sD[(i + 1) & 1], rg, p.scale);
-        } else {
-            if constexpr (DG) {
-                // as make_scores, with the pair terms x summed along both axes
-                const int l = lane_id(), x = l & 15, g = l >> 4;
-                T *P = sP + C * LP;
-                float over_t = 0.f;
+        f32x4 O[NT][G::NCT];
+        if constexpr (!KEYS) {
+            G::make_scores(s.p[0], s.k, s.q, d, p.scale, wv);
+            grp.template inter<1>(O, s.k, d);
+            if (scribe && i + 1 < nc) make_decay<C, true>(&s.decay[(i + 1) & 1], rg, p.scale);
+        } else if constexpr (DG) {
+            // as make_scores, with the pair terms x summed along both axes
+            const int l = lane_id(), x = l & 15, g = l >> 4;
+            float over_t = 0.f;
 #pragma unroll
-                for (int j = 0; j < NT * NT / 4; ++j) {
-                    const int tile = wv + 4 * j, rt = tile % NT, s_t = tile / NT;
-                    f32x4 a = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
-                    if (GK::reached(rt, s_t)) {
-                        a = GK::scores(sV, sO, rt, s_t);
-                        const f32x4 qk = GV::scores(sK, sQ, rt, s_t);
-                        const f32x4 cw = GK::weights(d, p.scale, rt, s_t);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            a[e] = cw[e] != 0.f ? a[e] * cw[e] : 0.f;
-                            xs[e] = 16 * s_t + 4 * g + e > 16 * rt + x ? a[e] * qk[e] : 0.f;
-                            over_t += xs[e];
-                        }
-                    }
-                    *reinterpret_cast<quad_t<T> *>(P + (16 * rt + x) * LP + 16 * s_t + 4 * g) = make_quad<T>(a);
-                    // sum over the tile's 16 rows s = this lane group's x
+            for (int j = 0; j < NT * NT / 4; ++j) {
+                const int tile = wv + 4 * j, rt = tile % NT, s_t = tile / NT;
+                f32x4 a = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
+                if (G::reached(rt, s_t)) {
+                    a = G::scores(s.v, s.d_o, rt, s_t);
+                    const f32x4 qk = GV::scores(s.k, s.q, rt, s_t);
+                    const f32x4 cw = G::weights(d, p.scale, rt, s_t);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                        for (int m = 1; m < 16; m *= 2) xs[e] += __shfl_xor(xs[e], m);
+                        a[e] = cw[e] != 0.f ? a[e] * cw[e] : 0.f;
+                        xs[e] = 16 * s_t + 4 * g + e > 16 * rt + x ? a[e] * qk[e] : 0.f;
+                        over_t += xs[e];
                     }
-                    if (x == 0) *reinterpret_cast<f32x4 *>(sX + wv * C + 16 * s_t + 4 * g) = xs;
                 }
-                over_t += __shfl_xor(over_t, 16);
-                over_t += __shfl_xor(over_t, 32);
-                if (g == 0) sX[4 * C + wv * C + 16 * (wv % NT) + x] = over_t;
-                st.k.template inter<split_of<T>>(OK, sV, d);
-                GK::row_dots(sZ + wv * C, sK, LK, C, OK, wv);
-                if (anchor >= 0) {
-                    const float *m = p.anchors + ((size_t)anchor * p.H + h) * part_size;
-                    const double r = st.k.template dot<true>(m, wv);
-                    if (l == 0) sR[wv] = r;
+                *reinterpret_cast<quad_t<T> *>(s.p[1] + (16 * rt + x) * L::LP + 16 * s_t + 4 * g) = make_quad<T>(a);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                    for (int m = 1; m < 16; m *= 2) xs[e] += __shfl_xor(xs[e], m);
                 }
-            } else {
-                GK::make_scores(sP + C * LP, sV, sO, d, p.scale, wv);
-                st.k.template inter<1>(OK, sV, d);
+                if (x == 0) *reinterpret_cast<f32x4 *>(&s.x_t[wv][16 * s_t + 4 * g]) = xs;
+                __builtin_amdgcn_sched_barrier(0);
             }
+            over_t += __shfl_xor(over_t, 16);
+            over_t += __shfl_xor(over_t, 32);
+            if (g == 0) s.x_s[wv][16 * (wv % NT) + x] = over_t;
+            grp.template inter<split_of<T>>(O, s.v, d);
+            G::row_dots(s.z[wv], [&](int it, int ct) {
+                return *reinterpret_cast<const quad_t<T> *>(s.k + (16 * it + x) * L::LK + G::first_col(wv) + 4 * ct);
+            }, O);
+            if (anchor >= 0) {
+                const double r = grp.template dot<true>(p.anchors + ((size_t)anchor * p.H + h) * part_size, wv);
+                if (l == 0) s.r[wv] = r;
+            }
+        } else {
+            G::make_scores(s.p[1], s.v, s.d_o, d, p.scale, wv);
+            grp.template inter<1>(O, s.v, d);
         }
-        lds_barrier();
-        if (!keys) {
-            GV::intra(OV, sP, sO, wv);
-            GV::store((T *)b.dv + ((size_t)row * p.H + h) * DV, sv, n, OV, wv);
-            st.v.update(sQ, sO, d, wv);
-            if (DG && wave == 3) {
+        lds_barrier();                                         // scores and sums are whole
+        if constexpr (!KEYS) {
+            G::intra(O, s.p[0], s.d_o, wv);
+            G::store((T *)b.dv + ((size_t)row * p.H + h) * DV, sv, n, O, wv);
+            grp.update(s.q, s.d_o, d, wv);
+            if (DG && scribe) {
                 const int u = lane_id();
                 float z = 0.f, cx = 0.f;
                 if (u < C) {
-                    z = (sZ[u] + sZ[C + u]) + (sZ[2 * C + u] + sZ[3 * C + u]);
-                    float xt = 0.f, xo;   // x summed over the earlier rows (this token as t), over the later ones (as s)
-                    if (NT == 4) {
-                        xt = (sX[u] + sX[C + u]) + (sX[2 * C + u] + sX[3 * C + u]);
-                        xo = sX[4 * C + (u / 16) * C + u];
-                    } else {
-                        const int q = u / 16;
-                        xt = sX[2 * q * C + u] + sX[(2 * q + 1) * C + u];
-                        xo = sX[4 * C + q * C + u] + sX[4 * C + (q + 2) * C + u];
-                    }
-                    cx = y + xt - xo;
+                    const int tile = u / 16;
+                    z = (s.z[0][u] + s.z[1][u]) + (s.z[2][u] + s.z[3][u]);
+                    // the waves that held tiles of this token's row
+                    const float xt = NT == 4 ? (s.x_t[0][u] + s.x_t[1][u]) + (s.x_t[2][u] + s.x_t[3][u])
+                                             : s.x_t[(2 * tile) & 3][u] + s.x_t[(2 * tile + 1) & 3][u];
+                    const float xs = NT == 4 ? s.x_s[tile][u] : s.x_s[tile][u] + s.x_s[(tile + 2) & 3][u];
+                    cx = y + xt - xs;
                 }
-                if (anchor >= 0) R = (sR[0] + sR[1]) + (sR[2] + sR[3]);
+                if (anchor >= 0) R = (s.r[0] + s.r[1]) + (s.r[2] + s.r[3]);
                 float up = z, down = cx;                       // inclusive sums from below, from above
 #pragma unroll
-                for (int s = 1; s < C; s *= 2) {
-                    const float a = __shfl_up(up, s), e = __shfl_down(down, s);
-                    if (u >= s) up += a;
-                    if (u + s < C) down += e;
+                for (int m = 1; m < C; m *= 2) {
+                    const float a = __shfl_up(up, m), e = __shfl_down(down, m);
+                    if (u >= m) up += a;
+                    if (u + m < C) down += e;
                 }
                 const double wt = d.total < 0x1p-24f ? 0.0 : R - wave_total((double)z);
                 R = wt + wave_total(u < C ? (double)y : 0.0);
@@ -798,21 +862,37 @@ __global__ __launch_bounds__(512, 2) void linear_dkdv_kernel(const LinearBwdPara
                 }
             }
         } else {
-            GK::intra(OK, sP + C * LP, sQ, wv);
+            G::intra(O, s.p[1], s.q, wv);
             if (p.wide)
-                GK::store((float *)b.dk + ((size_t)row * p.H + h) * DK, (size_t)p.H * DK, n, OK, wv);
+                G::store((float *)b.dk + ((size_t)row * p.H + h) * DK, (size_t)p.H * DK, n, O, wv);
             else
-                GK::store((T *)b.dk + ((size_t)row * Hk + hk) * DK, sk, n, OK, wv);
-            st.k.update(sO, sQ, d, wv);
+                G::store((T *)b.dk + ((size_t)row * Hk + hk) * DK, sk, n, O, wv);
+            grp.update(s.d_o, s.q, d, wv);
         }
     }
-    if (w.part == 0 && b.dh0 && !keys)
-        st.v.template put<false>(deferred(p, w, 0) ? p.part + ((size_t)w.slot * p.H + h) * part_size
-                                                   : b.dh0 + pair * part_size, wv);
-    if (DG && p.g_per_head && wave == 3) {
-        sum_dg = wave_total(sum_dg);
-        if (t % 64 == 0) b.dg_part[(size_t)id * p.H + h] = sum_dg;
+    if constexpr (!KEYS) {
+        if (w.part == 0 && b.dh0)
+            grp.template put<false>(deferred(p, w, 0) ? p.part + ((size_t)w.slot * p.H + h) * part_size
+                                                      : b.dh0 + pair * part_size, wv);
+        if (DG && p.g_per_head && scribe) {
+            sum_dg = wave_total(sum_dg);
+            if (lane_id() == 0) b.dg_part[(size_t)id * p.H + h] = sum_dg;
+        }
     }
+}
+
+template <typename T, int DK, int DV, bool DG>
+__global__ __launch_bounds__(512, 2) void linear_dkdv_kernel(const LinearBwdParams b)
+{
+    extern __shared__ __align__(16) char smem[];
+    DkdvLds<T, DK, DV> &s = *reinterpret_cast<DkdvLds<T, DK, DV> *>(smem);
+    const int h = (int)(blockIdx.x % (unsigned)b.c.H), id = (int)(blockIdx.x / (unsigned)b.c.H);
+    Piece w;
+    if (!find_piece(b.c, id, w)) return;
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 8))
+        dkdv_walk<T, DK, DV, DG, true>(b, s, w, id, h);
+    else
+        dkdv_walk<T, DK, DV, DG, false>(b, s, w, id, h);
 }
 
 // dg of constant decays: the segments' sums in order.  One wave per head.
@@ -891,9 +971,7 @@ template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdPar
     dq.q = b.d_o; dq.k = c.v; dq.v = c.k; dq.q_rows = c.q; dq.o = b.dq;
     hipLaunchKernelGGL((linear_walk_kernel<T, DV, DK, WALK_DQ>), grid, block, 0, stream, dq);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    constexpr int C = chunk_of<T>;
-    constexpr size_t lds = sizeof(T) * C * (2 * ld_of<T>(DK) + 2 * ld_of<T>(DV) + 2 * ldp_of<T>) + 2 * sizeof(Decay<C>)
-                           + 12 * C * sizeof(float) + 4 * sizeof(double);
+    constexpr size_t lds = sizeof(DkdvLds<T, DK, DV>);
     static_assert(lds <= 160 * 1024, "one compute unit's LDS");
     const auto kernel = b.dg ? linear_dkdv_kernel<T, DK, DV, true> : linear_dkdv_kernel<T, DK, DV, false>;
     // above 64 KiB a kernel asks for its dynamic LDS; per device, so with every launch
