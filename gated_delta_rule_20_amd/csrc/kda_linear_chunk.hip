@@ -42,7 +42,7 @@ template <typename T> constexpr int chunk_of = sizeof(T) == 2 ? 64 : 32;  // tok
 // LDS row lengths: 32 bytes (bf16) or 16 bytes (fp32) of padding keep the transposing and the row reads off
 // one another's banks.
 template <typename T> __host__ __device__ constexpr int ld_of(int d) { return d + (sizeof(T) == 2 ? 16 : 4); }
-template <typename T> constexpr int ldp_of = chunk_of<T> + (sizeof(T) == 2 ? 8 : 4);
+template <typename T> constexpr int ldp_of = chunk_of<T> + 4;
 template <typename T> constexpr int split_of = sizeof(T) == 2 ? 3 : 1;    // operand terms that hold a float32
 
 typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
@@ -205,7 +205,11 @@ template <typename T, int DK, int DV, bool REV> struct Group {
     static __device__ __forceinline__ int col0(int w, int ct) { return NCT == 2 ? 32 * w + 4 * ct : 16 * w; }
     static constexpr int STEP = NCT == 2 ? 8 : 4;
 
-    // ---- state, accumulator layout: value i of lane (x, g) in tile [rt][ct] is S[16 rt + 4 g + i][column x of ct]
+    // ---- state, accumulator layout: value i of lane (x, g) in tile [rt][ct] is S[row(rt) + 8 g + i][column x of ct].
+    // Rows are dealt so that the tiles 2 ks and 2 ks + 1 hold, in one lane, the rows 32 ks + 8 g .. + 7: as an
+    // operand of the outputs they meet 8 neighbouring elements of a row of Q, one 16-byte read free of bank
+    // conflicts (two 8-byte reads of the common deal were four-way conflicts).
+    static constexpr __device__ int row(int rt) { return 32 * (rt >> 1) + 4 * (rt & 1); }
     f32x4 S[NRT][NCT];
 
     __device__ __forceinline__ void clear()
@@ -219,11 +223,11 @@ template <typename T, int DK, int DV, bool REV> struct Group {
     template <bool TR> static __device__ __forceinline__ int state_lane(int w)
     {
         const int l = lane_id(), x = l & 15, g = l >> 4, col = col0(w, 0) + STEP * (x >> 2) + (x & 3);
-        return 4 * (TR ? col * DK + 4 * g : 4 * g * DV + col);
+        return 4 * (TR ? col * DK + 8 * g : 8 * g * DV + col);
     }
     template <bool TR> static constexpr __device__ int state_at(int rt, int ct, int i)
     {
-        return 4 * (TR ? 4 * ct * DK + 16 * rt : (16 * rt + i) * DV + 4 * ct);
+        return 4 * (TR ? 4 * ct * DK + row(rt) : (row(rt) + i) * DV + 4 * ct);
     }
     template <bool TR> static __device__ __forceinline__ f32x4 fetch(__amdgpu_buffer_rsrc_t m, int at, int rt, int ct)
     {
@@ -306,7 +310,7 @@ template <typename T, int DK, int DV, bool REV> struct Group {
             }
 #pragma unroll
             for (int rt = 0; rt < NRT; ++rt) {
-                const frag_t<T> kf = col_frag(K, LDK, 32 * ks, 16 * rt, 4);
+                const frag_t<T> kf = col_frag(K, LDK, 32 * ks, row(rt), 8);
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
@@ -323,8 +327,8 @@ template <typename T, int DK, int DV, bool REV> struct Group {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-            acc = mma(load_frag_kmap<T>(K + (16 * st + x) * LDK + 32 * ks, g),
-                      load_frag_kmap<T>(Q + (16 * rt + x) * LDK + 32 * ks, g), acc);
+            acc = mma(load_frag_lin<T>(K + (16 * st + x) * LDK + 32 * ks, g),
+                      load_frag_lin<T>(Q + (16 * rt + x) * LDK + 32 * ks, g), acc);
         return acc;
     }
     // scale * D of the same tile, 0 where s is not a source of r.
@@ -383,7 +387,7 @@ template <typename T, int DK, int DV, bool REV> struct Group {
             }
 #pragma unroll
             for (int it = 0; it < NT; ++it) {
-                const frag_t<T> qf = load_frag_kmap<T>(Q + (16 * it + x) * LDK + 32 * ks, g);
+                const frag_t<T> qf = load_frag_lin<T>(Q + (16 * it + x) * LDK + 32 * ks, g);
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
