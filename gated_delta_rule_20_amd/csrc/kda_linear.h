@@ -35,7 +35,8 @@ struct LinearChunkParams {
     const float *h0;                  // [N, H, Dk, Dv] or null
     float *hT;                        // [N, H, Dk, Dv] or null
     void *o;
-    float *part, *dec;                // [n_part, H, Dk, Dv] and [n_part, H] of the first pass, or null: no pass
+    float *part, *dec;                // [n_part, H, Dk * Dv] and [n_part, H] of the first pass, or null: no pass
+    float *part_tr;                   // backward: part once more, as [Dk][Dv]
     int n_part;
     int defer;                        // entering and resulting states share memory, and there is a first pass
     float *ckpt;                      // [N, ckpt_slots, H, Dk, Dv] or null

@@ -234,6 +234,7 @@ size_t plan_bwd(const kda_linear_bwd_args_t *a, const LinearPlan &pl, void *ws, 
         take_parts(c, pl, a->H, state, &b->c.part, &b->c.dec);
         b->c.defer = overlap(a->d_final_state, a->d_initial_state, state * pl.N);
         take_parts(c, pl, a->H, state, &b->part_fwd, &b->dec_fwd);
+        b->c.part_tr = (float *)c.take(state * pl.n_part);
     }
     if (a->dg) {
         b->c.y = (float *)c.take(sizeof(float) * (size_t)a->H * pl.rows);

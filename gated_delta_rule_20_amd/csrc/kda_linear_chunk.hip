@@ -250,6 +250,26 @@ template <typename T, int DK, int DV, bool REV> struct Group {
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = S[rt][ct] * f + fetch<TR>(rs, at, rt, ct);
     }
+    // The same for a state kept in the order of the registers (parts, read by workgroups of the same geometry):
+    // a wave's access is 1 KiB in a row.
+    __device__ __forceinline__ void add_part(const float *m, float f, int w)
+    {
+        const __amdgpu_buffer_rsrc_t rs = state_window(m);
+        const int at = 16 * (64 * w + lane_id());
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = S[rt][ct] * f + load16(rs, at, 4096 * (rt * NCT + ct));
+    }
+    __device__ __forceinline__ void put_part(float *m, int w) const
+    {
+        const __amdgpu_buffer_rsrc_t rs = state_window(m);
+        const int at = 16 * (64 * w + lane_id());
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) store_quad(rs, at, S[rt][ct], 4096 * (rt * NCT + ct));
+    }
     template <bool TR> __device__ __forceinline__ void put(float *m, int w) const
     {
         const __amdgpu_buffer_rsrc_t rs = state_window(m);
@@ -559,12 +579,13 @@ __device__ __forceinline__ float fetch_decay(const LinearChunkParams &p, int row
     return log2_decay(p.g_per_head ? p.g[h] : p.g[(size_t)(row + u) * p.H + h]);
 }
 
-enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ };
+enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ, WALK_STATE_DQ };
 
 // One workgroup walks one segment for one value head (head fastest, so that
 // workgroups that run together read neighbouring rows).
 //   WALK_STATE      q, k, v roles: -, k, v;  writes the segment's part and decay
-//   WALK_STATE_REV  -, q, do, backwards
+//   WALK_STATE_REV  -, q, do, backwards; writes its part in both orders that linear_dkdv_kernel reads
+//   WALK_STATE_DQ   -, v, k: as WALK_STATE, transposed (DK = the problem's Dv, DV = its Dk)
 //   WALK_OUT        q, k, v;  writes o, final state, checkpoints
 //   WALK_DQ         do, v, k (DK = the problem's Dv, DV = its Dk);  writes dq, y, anchors
 // 66 KiB of LDS and up to 256 registers a lane: two workgroups share a compute
@@ -585,7 +606,7 @@ __global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkPa
     const int h = (int)(blockIdx.x % (unsigned)p.H), id = (int)(blockIdx.x / (unsigned)p.H);
     Piece w;
     if (!find_piece(p, id, w)) return;
-    if (MODE == WALK_STATE && w.part == w.parts - 1) return;   // nothing comes after it
+    if ((MODE == WALK_STATE || MODE == WALK_STATE_DQ) && w.part == w.parts - 1) return;   // nothing comes after it
     if (MODE == WALK_STATE_REV && w.part == 0) return;
     const int slot = w.slot + (MODE == WALK_STATE_REV ? w.part - 1 : w.part);
     if (!OUT && slot >= p.n_part) return;                      // only with offsets that break the rules
@@ -595,7 +616,7 @@ __global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkPa
     const int row0 = w.begin + first;
     const int hk = h / p.group, Hk = p.H / p.group;
     // strides and heads of the three roles
-    constexpr bool QK_SHARED = MODE != WALK_DQ;                // role q / k carry the query / key heads
+    constexpr bool QK_SHARED = MODE != WALK_DQ && MODE != WALK_STATE_DQ;                // role q / k carry the query / key heads
     const size_t sq = (size_t)(QK_SHARED ? Hk : p.H) * DK;
     const size_t sv = (size_t)(QK_SHARED ? p.H : Hk) * DV;
     const T *gq = (const T *)p.q + (size_t)(QK_SHARED ? hk : h) * DK;
@@ -610,7 +631,7 @@ __global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkPa
         for (int i = 0; i < w.part; ++i) {
             if (w.slot + i >= p.n_part) break;
             const size_t at = (size_t)(w.slot + i) * p.H + h;
-            grp.template add<TR>(p.part + at * part_size, p.dec[at], wv);
+            grp.add_part(p.part + at * part_size, p.dec[at], wv);
         }
     }
     Stage<T, DK, 256> rq, rk;
@@ -684,7 +705,8 @@ __global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkPa
     }
     if (!OUT) {
         const size_t at = (size_t)slot * p.H + h;
-        grp.template put<TR>(p.part + at * part_size, wv);
+        grp.put_part(p.part + at * part_size, wv);
+        if (MODE == WALK_STATE_REV) grp.template put<false>(p.part_tr + at * part_size, wv);
         if (t == 0) p.dec[at] = dec;
     }
     if (MODE == WALK_OUT && p.hT && w.part == w.parts - 1)
@@ -751,7 +773,10 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
     for (int i = w.parts - 1; i > w.part; --i) {
         if (w.slot + i - 1 >= p.n_part) continue;
         const size_t at = (size_t)(w.slot + i - 1) * p.H + h;
-        grp.template add<KEYS>(p.part + at * part_size, p.dec[at], wv);
+        if constexpr (KEYS)
+            grp.template add<true>(p.part_tr + at * part_size, p.dec[at], wv);
+        else
+            grp.add_part(p.part + at * part_size, p.dec[at], wv);
     }
     Stage<T, DK, 512> rq, rk;
     Stage<T, DV, 512> rv, ro;
@@ -964,7 +989,8 @@ template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdPar
     if (c.part) {
         LinearChunkParams s = c;
         s.part = b.part_fwd; s.dec = b.dec_fwd;
-        hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE>), grid, block, 0, stream, s);
+        s.k = c.v; s.v = c.k;
+        hipLaunchKernelGGL((linear_walk_kernel<T, DV, DK, WALK_STATE_DQ>), grid, block, 0, stream, s);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         s = c;
         s.k = c.q; s.v = b.d_o;
