@@ -45,7 +45,8 @@ template <typename T> __host__ __device__ constexpr int ld_of(int d) { return d 
 template <typename T> constexpr int ldp_of = chunk_of<T> + 4;
 template <typename T> constexpr int split_of = sizeof(T) == 2 ? 3 : 1;    // operand terms that hold a float32
 
-typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 // Fragment whose k-axis is the rows of a row-major LDS tile: value e of lane
 // (x, g) is tile[k0 + kmap(g, e)][base + step * (x / 4) + x % 4].  bf16 uses the
@@ -54,10 +55,10 @@ typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ bf16x8 col_frag(const bf16 *tile, int ld, int k0, int base, int step)
 {
     const int l = lane_id(), x = l & 15, g = l >> 4;
-    typedef __attribute__((address_space(3))) bf16x4v *lds_ptr;
+    typedef __attribute__((address_space(3))) bf16x4 *lds_ptr;
     const bf16 *p = tile + (k0 + 4 * g + (x >> 2)) * ld + base + step * (x & 3);
-    const bf16x4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)p);
-    const bf16x4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)(p + 16 * ld));
+    const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)p);
+    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_ptr)(p + 16 * ld));
     bf16x8 f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) { f[i] = lo[i]; f[4 + i] = hi[i]; }
@@ -72,19 +73,28 @@ __device__ __forceinline__ f32x8 col_frag(const float *tile, int ld, int k0, int
     return f;
 }
 
-// x as a sum of NS operand fragments.
+// x as a sum of NS operand fragments.  Two values at a time: one conversion, then
+// their bf16 bits, moved up, are the floats to take off.
 template <int NS> __device__ __forceinline__ void split(const float *x, bf16x8 *f)
 {
-    float r[8];
+    typedef __bf16 pair __attribute__((ext_vector_type(2)));
+    typedef float fpair __attribute__((ext_vector_type(2)));
+    u32x4 u[NS];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = x[e];
+    for (int j = 0; j < 4; ++j) {
+        float a = x[2 * j], b = x[2 * j + 1];
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            f[n][e] = (bf16)r[e];
-            r[e] -= (float)f[n][e];
+        for (int n = 0; n < NS; ++n) {
+            const unsigned w = __builtin_bit_cast(unsigned, __builtin_convertvector((fpair{a, b}), pair));
+            u[n][j] = w;
+            if (n + 1 < NS) {
+                a -= __builtin_bit_cast(float, w << 16);
+                b -= __builtin_bit_cast(float, w & 0xffff0000u);
+            }
         }
+    }
+#pragma unroll
+    for (int n = 0; n < NS; ++n) f[n] = __builtin_bit_cast(bf16x8, u[n]);
 }
 template <int NS> __device__ __forceinline__ void split(const float *x, f32x8 *f)
 {
@@ -106,8 +116,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_window(const void *base, 
 {
     return window(base, (unsigned)(n - 1) * stride + width);
 }
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ f32x4 load16(__amdgpu_buffer_rsrc_t rs, int voff, int soff = 0)
 {
     return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, voff, soff, 0));
@@ -351,38 +359,56 @@ template <typename T, int DK, int DV, bool REV> struct Group {
                       load_frag_lin<T>(Q + (16 * rt + x) * LDK + 32 * ks, g), acc);
         return acc;
     }
-    // scale * D of the same tile, 0 where s is not a source of r.
-    static __device__ __forceinline__ f32x4 weights(const Decay<C> &d, float scale, int rt, int st)
+    // Those scores with their decays, 0 where s is not a source of r (on the diagonal tile).
+    static __device__ __forceinline__ f32x4 decayed(f32x4 p, const Decay<C> &d, float scale, int rt, int st)
     {
         const int l = lane_id(), x = l & 15, g = l >> 4;
         const int r = 16 * rt + x, s = 16 * st + 4 * g;
         const float rh = d.hi[r], rl = d.lo[r];
         const f32x4 sh = *reinterpret_cast<const f32x4 *>(&d.hi[s]), sl = *reinterpret_cast<const f32x4 *>(&d.lo[s]);
-        f32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float y = REV ? (sh[i] - rh) + (sl[i] - rl) : (rh - sh[i]) + (rl - sl[i]);
-            o[i] = (REV ? s + i >= r : s + i <= r) ? scale * __builtin_amdgcn_exp2f(y) : 0.f;
+            p[i] *= scale * __builtin_amdgcn_exp2f(y);
         }
-        return o;
+        if (rt == st) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = (REV ? 4 * g + i >= x : 4 * g + i <= x) ? p[i] : 0.f;
+        }
+        return p;
     }
-    static __device__ __forceinline__ bool reached(int rt, int st) { return REV ? st >= rt : st <= rt; }
-
-    // Decayed scores into P[r][s] (rounded to T), tiles dealt to the four waves.
-    static __device__ __forceinline__ void make_scores(T *P, const T *Q, const T *K, const Decay<C> &d, float scale, int w)
+    static __device__ __forceinline__ void put_scores(T *P, f32x4 p, int rt, int st)
     {
         const int l = lane_id(), x = l & 15, g = l >> 4;
+        *reinterpret_cast<quad_t<T> *>(P + (16 * rt + x) * LDP + 16 * st + 4 * g) = make_quad<T>(p);
+    }
+    static constexpr __device__ bool reached(int rt, int st) { return REV ? st >= rt : st <= rt; }
+
+    // P's tiles that no source reaches but that a product takes in with its 32 source rows: zero, once.
+    static __device__ __forceinline__ void clear_scores(T *P, int w)
+    {
+        if (w < NT / 2) put_scores(P, f32x4{0.f, 0.f, 0.f, 0.f}, REV ? 2 * w + 1 : 2 * w, REV ? 2 * w : 2 * w + 1);
+    }
+
+    // Decayed scores into P[r][s] (rounded to T).  Of the ten tiles of a 64-token chunk each of three waves takes three:
+    // (0,0) (3,0) (3,1), (1,0) (1,1) (3,2) and (2,0) (2,1) (2,2), and the fourth takes (3,3) and the next chunk's
+    // decays; backwards all is mirrored.  Of a 32-token chunk's three tiles each wave takes one.
+    static __device__ __forceinline__ void make_scores(T *P, const T *Q, const T *K, const Decay<C> &d, float scale, int w)
+    {
 #pragma unroll
-        for (int i = 0; i < NT * NT / 4; ++i) {
-            const int tile = w + 4 * i, rt = tile % NT, st = tile / NT;
-            f32x4 p = {0.f, 0.f, 0.f, 0.f};
-            if (reached(rt, st)) {
-                p = scores(Q, K, rt, st);
-                const f32x4 c = weights(d, scale, rt, st);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = c[e] != 0.f ? p[e] * c[e] : 0.f;
+        for (int i = 0; i < (NT == 4 ? 3 : 1); ++i) {
+            int rt, st;
+            if (NT == 4) {
+                if (w == 3 && i > 0) break;
+                rt = w == 3 ? 3 : w == 2 ? 2 : w == 1 ? (i < 2 ? 1 : 3) : (i < 1 ? 0 : 3);
+                st = w == 3 ? 3 : w == 2 ? i : w == 1 ? i : (i < 1 ? 0 : i - 1);
+            } else {
+                if (w == 3) break;
+                rt = w > 0;
+                st = w > 1;
             }
-            *reinterpret_cast<quad_t<T> *>(P + (16 * rt + x) * LDP + 16 * st + 4 * g) = make_quad<T>(p);
+            if (REV) { rt = NT - 1 - rt; st = NT - 1 - st; }
+            put_scores(P, decayed(scores(Q, K, rt, st), d, scale, rt, st), rt, st);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -644,9 +670,10 @@ __global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkPa
         rv.load(gv + (size_t)row * sv, sv, n, t);
         rg = fetch_decay(p, row, h, n);
     };
+    if (OUT) G::clear_scores(sP, wv);
     if (nc > 0) {
         fetch(REV ? nc - 1 : 0);
-        if (wv == 0) make_decay<C, REV>(&sD[0], rg, p.scale);
+        if (wv == 3) make_decay<C, REV>(&sD[0], rg, p.scale);
     }
     for (int i = 0; i < nc; ++i) {
         const int c = REV ? nc - 1 - i : i, n = min(C, toks - c * C), row = row0 + c * C;
@@ -676,7 +703,7 @@ __global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkPa
             } else {
                 grp.template inter<1>(O, sQ, d);
             }
-            if (wv == 0 && i + 1 < nc) make_decay<C, REV>(&sD[(i + 1) & 1], rg, p.scale);
+            if (wv == 3 && i + 1 < nc) make_decay<C, REV>(&sD[(i + 1) & 1], rg, p.scale);
             lds_barrier();                                     // P (and y) are whole
             G::intra(O, sP, sV, wv);
             if (MODE == WALK_DQ && p.wide)
@@ -688,7 +715,7 @@ __global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkPa
             if (MODE == WALK_DQ && p.y && t < n)
                 p.y[(size_t)(row + t) * p.H + h] = (sY[0][t] + sY[1 % 4][t]) + (sY[2 % 4][t] + sY[3 % 4][t]);
         } else {
-            if (wv == 0 && i + 1 < nc) make_decay<C, REV>(&sD[(i + 1) & 1], rg, p.scale);
+            if (wv == 3 && i + 1 < nc) make_decay<C, REV>(&sD[(i + 1) & 1], rg, p.scale);
             dec *= d.total;
         }
         grp.update(sK, sV, d, wv);
@@ -780,6 +807,7 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
     }
     Stage<T, DK, 512> rq, rk;
     Stage<T, DV, 512> rv, ro;
+    G::clear_scores(s.p[KEYS], wv);
     float rg = 0.f, ry = 0.f;
     auto fetch = [&](int c) {
         const int row = row0 + c * C, n = min(C, toks - c * C);
@@ -824,17 +852,15 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
                 const int tile = wv + 4 * j, rt = tile % NT, s_t = tile / NT;
                 f32x4 a = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
                 if (G::reached(rt, s_t)) {
-                    a = G::scores(s.v, s.d_o, rt, s_t);
+                    a = G::decayed(G::scores(s.v, s.d_o, rt, s_t), d, p.scale, rt, s_t);
                     const f32x4 qk = GV::scores(s.k, s.q, rt, s_t);
-                    const f32x4 cw = G::weights(d, p.scale, rt, s_t);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        a[e] = cw[e] != 0.f ? a[e] * cw[e] : 0.f;
                         xs[e] = 16 * s_t + 4 * g + e > 16 * rt + x ? a[e] * qk[e] : 0.f;
                         over_t += xs[e];
                     }
+                    G::put_scores(s.p[1], a, rt, s_t);
                 }
-                *reinterpret_cast<quad_t<T> *>(s.p[1] + (16 * rt + x) * L::LP + 16 * s_t + 4 * g) = make_quad<T>(a);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
 #pragma unroll
