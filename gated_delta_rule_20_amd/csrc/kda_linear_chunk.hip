@@ -196,6 +196,15 @@ template <int C, bool REV> __device__ __forceinline__ void make_decay(Decay<C> *
     if (u == C - 1) d->total = in;
 }
 
+// The sum over the 16 lanes of a row, in each of them.
+__device__ __forceinline__ float row_total(float v)
+{
+    v = dpp_add<0xB1, 0xF>(v);   // quad_perm [1, 0, 3, 2]
+    v = dpp_add<0x4E, 0xF>(v);   // quad_perm [2, 3, 0, 1]
+    v = dpp_add<0x141, 0xF>(v);  // row_half_mirror
+    return dpp_add<0x140, 0xF>(v);  // row_mirror
+}
+
 __device__ __forceinline__ double wave_total(double v)
 {
 #pragma unroll
@@ -395,6 +404,10 @@ template <typename T, int DK, int DV, bool REV> struct Group {
     // decays; backwards all is mirrored.  Of a 32-token chunk's three tiles each wave takes one.
     static __device__ __forceinline__ void make_scores(T *P, const T *Q, const T *K, const Decay<C> &d, float scale, int w)
     {
+        for_tiles(w, [&](int rt, int st) { put_scores(P, decayed(scores(Q, K, rt, st), d, scale, rt, st), rt, st); });
+    }
+    template <typename F> static __device__ __forceinline__ void for_tiles(int w, F f)
+    {
 #pragma unroll
         for (int i = 0; i < (NT == 4 ? 3 : 1); ++i) {
             int rt, st;
@@ -408,7 +421,7 @@ template <typename T, int DK, int DV, bool REV> struct Group {
                 st = w > 1;
             }
             if (REV) { rt = NT - 1 - rt; st = NT - 1 - st; }
-            put_scores(P, decayed(scores(Q, K, rt, st), d, scale, rt, st), rt, st);
+            f(rt, st);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -663,12 +676,21 @@ __global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkPa
     Stage<T, DK, 256> rq, rk;
     Stage<T, DV, 256> rv;
     float rg = 0.f, dec = 1.f;
+    // the next chunk's rows
+    const int chunk0 = row0 + (REV ? max(nc - 1, 0) : 0) * C;
+    gq += (size_t)chunk0 * sq;
+    gk += (size_t)chunk0 * sq;
+    gv += (size_t)chunk0 * sv;
+    const long step_q = (REV ? -C : C) * (long)sq, step_v = (REV ? -C : C) * (long)sv;
     auto fetch = [&](int c) {
-        const int row = row0 + c * C, n = min(C, toks - c * C);
-        if (OUT) rq.load(gq + (size_t)row * sq, sq, n, t);
-        rk.load(gk + (size_t)row * sq, sq, n, t);
-        rv.load(gv + (size_t)row * sv, sv, n, t);
-        rg = fetch_decay(p, row, h, n);
+        const int n = min(C, toks - c * C);
+        if (OUT) rq.load(gq, sq, n, t);
+        rk.load(gk, sq, n, t);
+        rv.load(gv, sv, n, t);
+        gq += step_q;
+        gk += step_q;
+        gv += step_v;
+        if (wv == 3) rg = fetch_decay(p, row0 + c * C, h, n);
     };
     if (OUT) G::clear_scores(sP, wv);
     if (nc > 0) {
@@ -771,7 +793,9 @@ template <typename T, int DK, int DV> struct DkdvLds {
     T p[2][C * LP];           // decayed scores of dV and of dK
     Decay<C> decay[2];
     float z[4][C];            // by wave: sums over its columns
-    float x_t[4][C], x_s[4][C];   // by wave: x summed over the earlier rows (token as t), over the later ones (as s)
+    // x summed over the 16 s of a tile (for each t, by the tile's s), over its 16 t (for each s, by its t); 0 where no
+    // tile is
+    float x_t[C / 16][C], x_s[C / 16][C];
     double r[4];              // by wave: <state, gradient> at an anchor
 };
 
@@ -808,13 +832,19 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
     Stage<T, DK, 512> rq, rk;
     Stage<T, DV, 512> rv, ro;
     G::clear_scores(s.p[KEYS], wv);
+    if (DG && KEYS)
+        for (int e = t - 256; e < NT * C; e += 256) s.x_t[e / C][e % C] = s.x_s[e / C][e % C] = 0.f;
     float rg = 0.f, ry = 0.f;
+    size_t at_k = (size_t)(row0 + max(nc - 1, 0) * C) * sk + (size_t)hk * DK;   // the next chunk's rows
+    size_t at_v = (size_t)(row0 + max(nc - 1, 0) * C) * sv + (size_t)h * DV;
     auto fetch = [&](int c) {
         const int row = row0 + c * C, n = min(C, toks - c * C);
-        rq.load((const T *)p.q + (size_t)row * sk + (size_t)hk * DK, sk, n, t);
-        rk.load((const T *)p.k + (size_t)row * sk + (size_t)hk * DK, sk, n, t);
-        rv.load((const T *)p.v + (size_t)row * sv + (size_t)h * DV, sv, n, t);
-        ro.load((const T *)b.d_o + (size_t)row * sv + (size_t)h * DV, sv, n, t);
+        rq.load((const T *)p.q + at_k, sk, n, t);
+        rk.load((const T *)p.k + at_k, sk, n, t);
+        rv.load((const T *)p.v + at_v, sv, n, t);
+        ro.load((const T *)b.d_o + at_v, sv, n, t);
+        at_k -= C * sk;
+        at_v -= C * sv;
         if (scribe) {
             rg = fetch_decay(p, row, h, n);
             if (DG) ry = lane_id() < n ? p.y[(size_t)(row + lane_id()) * p.H + h] : 0.f;
@@ -840,49 +870,44 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
         if (i + 1 < nc) fetch(c - 1);
         f32x4 O[NT][G::NCT];
         if constexpr (!KEYS) {
-            G::make_scores(s.p[0], s.k, s.q, d, p.scale, wv);
+            if constexpr (DG) {
+                // the pair terms x of each tile too, summed along both axes
+                const int l = lane_id(), x = l & 15, g = l >> 4;
+                G::for_tiles(wv, [&](int rt, int st) {
+                    const f32x4 a = G::decayed(G::scores(s.k, s.q, rt, st), d, p.scale, rt, st);
+                    const f32x4 dov = GK::scores(s.v, s.d_o, rt, st);
+                    G::put_scores(s.p[0], a, rt, st);
+                    f32x4 xs;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) xs[e] = rt == st && 4 * g + e <= x ? 0.f : a[e] * dov[e];
+                    float over = (xs[0] + xs[1]) + (xs[2] + xs[3]);
+                    over += __shfl_xor(over, 16);
+                    over += __shfl_xor(over, 32);
+                    if (g == 0) s.x_s[st][16 * rt + x] = over;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) xs[e] = row_total(xs[e]);
+                    if (x == 0) *reinterpret_cast<f32x4 *>(&s.x_t[rt][16 * st + 4 * g]) = xs;
+                });
+            } else {
+                G::make_scores(s.p[0], s.k, s.q, d, p.scale, wv);
+            }
             grp.template inter<1>(O, s.k, d);
             if (scribe && i + 1 < nc) make_decay<C, true>(&s.decay[(i + 1) & 1], rg, p.scale);
-        } else if constexpr (DG) {
-            // as make_scores, with the pair terms x summed along both axes
-            const int l = lane_id(), x = l & 15, g = l >> 4;
-            float over_t = 0.f;
-#pragma unroll
-            for (int j = 0; j < NT * NT / 4; ++j) {
-                const int tile = wv + 4 * j, rt = tile % NT, s_t = tile / NT;
-                f32x4 a = {0.f, 0.f, 0.f, 0.f}, xs = {0.f, 0.f, 0.f, 0.f};
-                if (G::reached(rt, s_t)) {
-                    a = G::decayed(G::scores(s.v, s.d_o, rt, s_t), d, p.scale, rt, s_t);
-                    const f32x4 qk = GV::scores(s.k, s.q, rt, s_t);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        xs[e] = 16 * s_t + 4 * g + e > 16 * rt + x ? a[e] * qk[e] : 0.f;
-                        over_t += xs[e];
-                    }
-                    G::put_scores(s.p[1], a, rt, s_t);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                    for (int m = 1; m < 16; m *= 2) xs[e] += __shfl_xor(xs[e], m);
-                }
-                if (x == 0) *reinterpret_cast<f32x4 *>(&s.x_t[wv][16 * s_t + 4 * g]) = xs;
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            over_t += __shfl_xor(over_t, 16);
-            over_t += __shfl_xor(over_t, 32);
-            if (g == 0) s.x_s[wv][16 * (wv % NT) + x] = over_t;
-            grp.template inter<split_of<T>>(O, s.v, d);
-            G::row_dots(s.z[wv], [&](int it, int ct) {
-                return *reinterpret_cast<const quad_t<T> *>(s.k + (16 * it + x) * L::LK + G::first_col(wv) + 4 * ct);
-            }, O);
-            if (anchor >= 0) {
-                const double r = grp.template dot<true>(p.anchors + ((size_t)anchor * p.H + h) * part_size, wv);
-                if (l == 0) s.r[wv] = r;
-            }
         } else {
             G::make_scores(s.p[1], s.v, s.d_o, d, p.scale, wv);
-            grp.template inter<1>(O, s.v, d);
+            if constexpr (DG) {
+                const int l = lane_id(), x = l & 15;
+                grp.template inter<split_of<T>>(O, s.v, d);
+                G::row_dots(s.z[wv], [&](int it, int ct) {
+                    return *reinterpret_cast<const quad_t<T> *>(s.k + (16 * it + x) * L::LK + G::first_col(wv) + 4 * ct);
+                }, O);
+                if (anchor >= 0) {
+                    const double r = grp.template dot<true>(p.anchors + ((size_t)anchor * p.H + h) * part_size, wv);
+                    if (l == 0) s.r[wv] = r;
+                }
+            } else {
+                grp.template inter<1>(O, s.v, d);
+            }
         }
         lds_barrier();                                         // scores and sums are whole
         if constexpr (!KEYS) {
@@ -893,13 +918,10 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
                 const int u = lane_id();
                 float z = 0.f, cx = 0.f;
                 if (u < C) {
-                    const int tile = u / 16;
                     z = (s.z[0][u] + s.z[1][u]) + (s.z[2][u] + s.z[3][u]);
-                    // the waves that held tiles of this token's row
-                    const float xt = NT == 4 ? (s.x_t[0][u] + s.x_t[1][u]) + (s.x_t[2][u] + s.x_t[3][u])
-                                             : s.x_t[(2 * tile) & 3][u] + s.x_t[(2 * tile + 1) & 3][u];
-                    const float xs = NT == 4 ? s.x_s[tile][u] : s.x_s[tile][u] + s.x_s[(tile + 2) & 3][u];
-                    cx = y + xt - xs;
+                    cx = y;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) cx += s.x_t[j][u] - s.x_s[j][u];
                 }
                 if (anchor >= 0) R = (s.r[0] + s.r[1]) + (s.r[2] + s.r[3]);
                 float up = z, down = cx;                       // inclusive sums from below, from above
