@@ -212,10 +212,11 @@ __device__ __forceinline__ double wave_total(double v)
     return v;
 }
 
-// The work of four waves on one chunk: output columns (and state columns) are
+// The work of NW waves on one chunk: output columns (and state columns) are
 // dealt 16 * NCT to a wave.  DK: contracted width, DV: output width.
-template <typename T, int DK, int DV, bool REV> struct Group {
-    static constexpr int C = chunk_of<T>, NT = C / 16, NRT = DK / 16, NCT = DV / 64, KS = DK / 32, CK = C / 32;
+template <typename T, int DK, int DV, bool REV, int NW> struct Group {
+    static constexpr int C = chunk_of<T>, NT = C / 16, NRT = DK / 16, NCT = DV / 16 / NW, KS = DK / 32, CK = C / 32;
+    static_assert(NCT == 1 || NCT == 2, "one or two column tiles a wave");
     static constexpr int LDK = ld_of<T>(DK), LDV = ld_of<T>(DV), LDP = ldp_of<T>;
 
     // With two column tiles a lane's rows of both tiles are made neighbours (8 columns: one wide access).
@@ -276,7 +277,7 @@ template <typename T, int DK, int DV, bool REV> struct Group {
 #pragma unroll
         for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = S[rt][ct] * f + load16(rs, at, 4096 * (rt * NCT + ct));
+            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = S[rt][ct] * f + load16(rs, at, 1024 * NW * (rt * NCT + ct));
     }
     __device__ __forceinline__ void put_part(float *m, int w) const
     {
@@ -285,7 +286,7 @@ template <typename T, int DK, int DV, bool REV> struct Group {
 #pragma unroll
         for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) store_quad(rs, at, S[rt][ct], 4096 * (rt * NCT + ct));
+            for (int ct = 0; ct < NCT; ++ct) store_quad(rs, at, S[rt][ct], 1024 * NW * (rt * NCT + ct));
     }
     template <bool TR> __device__ __forceinline__ void put(float *m, int w) const
     {
@@ -409,14 +410,18 @@ template <typename T, int DK, int DV, bool REV> struct Group {
     template <typename F> static __device__ __forceinline__ void for_tiles(int w, F f)
     {
 #pragma unroll
-        for (int i = 0; i < (NT == 4 ? 3 : 1); ++i) {
+        for (int i = 0; i < (NT == 4 && NW == 4 ? 3 : NT == 4 ? 2 : 1); ++i) {
             int rt, st;
-            if (NT == 4) {
+            if (NT == 4 && NW == 4) {
                 if (w == 3 && i > 0) break;
                 rt = w == 3 ? 3 : w == 2 ? 2 : w == 1 ? (i < 2 ? 1 : 3) : (i < 1 ? 0 : 3);
                 st = w == 3 ? 3 : w == 2 ? i : w == 1 ? i : (i < 1 ? 0 : i - 1);
+            } else if (NT == 4) {
+                if (w > 5 || (w > 3 && i > 0)) break;         // rows 3, 2, (2, 1), (1, 0)
+                rt = w < 2 ? 3 : w == 2 ? 2 : w == 3 ? 2 - i : 1 - (w - 4);
+                st = w < 2 ? 2 * w + i : w == 2 ? i : w == 3 ? 2 - i : 0;
             } else {
-                if (w == 3) break;
+                if (w >= 3) break;
                 rt = w > 0;
                 st = w > 1;
             }
@@ -618,6 +623,9 @@ __device__ __forceinline__ float fetch_decay(const LinearChunkParams &p, int row
     return log2_decay(p.g_per_head ? p.g[h] : p.g[(size_t)(row + u) * p.H + h]);
 }
 
+// Waves of each kind in linear_dkdv_kernel.
+template <int DK, int DV> constexpr int pair_waves = DK == 128 && DV == 128 ? 8 : 4;
+
 enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ, WALK_STATE_DQ };
 
 // One workgroup walks one segment for one value head (head fastest, so that
@@ -629,11 +637,14 @@ enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ, WALK_STATE_DQ };
 //   WALK_DQ         do, v, k (DK = the problem's Dv, DV = its Dk);  writes dq, y, anchors
 // 66 KiB of LDS and up to 256 registers a lane: two workgroups share a compute
 // unit, and one computes while the other waits for memory.
+template <int DK, int DV, int MODE> constexpr int walk_waves = MODE == WALK_STATE_REV ? pair_waves<DK, DV> : 4;
+
 template <typename T, int DK, int DV, int MODE>
-__global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkParams p)
+__global__ __launch_bounds__((64 * walk_waves<DK, DV, MODE>), (walk_waves<DK, DV, MODE> / 2)) void linear_walk_kernel(const LinearChunkParams p)
 {
+    constexpr int NW = walk_waves<DK, DV, MODE>, THREADS = 64 * NW;
     constexpr bool REV = MODE == WALK_STATE_REV, OUT = MODE == WALK_OUT || MODE == WALK_DQ, TR = MODE == WALK_DQ;
-    using G = Group<T, DK, DV, REV>;
+    using G = Group<T, DK, DV, REV, NW>;
     constexpr int C = G::C;
     __shared__ __align__(16) T sQ[OUT ? C * G::LDK : 8];
     __shared__ __align__(16) T sK[C * G::LDK];
@@ -673,8 +684,8 @@ __global__ __launch_bounds__(256, 2) void linear_walk_kernel(const LinearChunkPa
             grp.add_part(p.part + at * part_size, p.dec[at], wv);
         }
     }
-    Stage<T, DK, 256> rq, rk;
-    Stage<T, DV, 256> rv;
+    Stage<T, DK, THREADS> rq, rk;
+    Stage<T, DV, THREADS> rv;
     float rg = 0.f, dec = 1.f;
     // the next chunk's rows
     const int chunk0 = row0 + (REV ? max(nc - 1, 0) : 0) * C;
@@ -788,15 +799,16 @@ __global__ __launch_bounds__(256) void linear_deferred_kernel(const LinearChunkP
 // from the state that WALK_DQ left at every anchor, and w is 0 where e^{G_end} < 2^-24 (then w is below the rounding
 // of R), so the roundings of y and z do not pile up.
 template <typename T, int DK, int DV> struct DkdvLds {
+    static constexpr int NW = pair_waves<DK, DV>;
     static constexpr int C = chunk_of<T>, LK = ld_of<T>(DK), LV = ld_of<T>(DV), LP = ldp_of<T>;
     T q[C * LK], k[C * LK], v[C * LV], d_o[C * LV];
     T p[2][C * LP];           // decayed scores of dV and of dK
     Decay<C> decay[2];
-    float z[4][C];            // by wave: sums over its columns
+    float z[NW][C];           // by wave: sums over its columns
     // x summed over the 16 s of a tile (for each t, by the tile's s), over its 16 t (for each s, by its t); 0 where no
     // tile is
     float x_t[C / 16][C], x_s[C / 16][C];
-    double r[4];              // by wave: <state, gradient> at an anchor
+    double r[NW];             // by wave: <state, gradient> at an anchor
 };
 
 // The walk of one kind of waves; both kinds pass the same barriers.
@@ -804,13 +816,14 @@ template <typename T, int DK, int DV, bool DG, bool KEYS>
 __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, DK, DV> &s, const Piece &w, int id, int h)
 {
     const LinearChunkParams &p = b.c;
-    using GV = Group<T, DK, DV, true>;    // rows k, sources q, values dO, state dS
-    using GK = Group<T, DV, DK, true>;    // rows v, sources dO, values q, state dS^T
-    using G = typename std::conditional<KEYS, GK, GV>::type;
     using L = DkdvLds<T, DK, DV>;
+    constexpr int NW = L::NW, THREADS = 128 * NW;
+    using GV = Group<T, DK, DV, true, NW>;    // rows k, sources q, values dO, state dS
+    using GK = Group<T, DV, DK, true, NW>;    // rows v, sources dO, values q, state dS^T
+    using G = typename std::conditional<KEYS, GK, GV>::type;
     constexpr int C = G::C, NT = G::NT;
-    const int t = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(t >> 6) & 3;
-    const bool scribe = !KEYS && wv == 3;                      // forms the decays and dg: wave 3 has the fewest scores
+    const int t = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(t >> 6) & (NW - 1);
+    const bool scribe = !KEYS && wv == NW - 1;                 // forms the decays and dg: the wave with the fewest scores
     const int first = w.part * p.seg, toks = min(p.seg, w.len - first);
     const int nc = (max(toks, 0) + C - 1) / C;
     const int row0 = w.begin + first;
@@ -829,11 +842,11 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
         else
             grp.add_part(p.part + at * part_size, p.dec[at], wv);
     }
-    Stage<T, DK, 512> rq, rk;
-    Stage<T, DV, 512> rv, ro;
+    Stage<T, DK, THREADS> rq, rk;
+    Stage<T, DV, THREADS> rv, ro;
     G::clear_scores(s.p[KEYS], wv);
     if (DG && KEYS)
-        for (int e = t - 256; e < NT * C; e += 256) s.x_t[e / C][e % C] = s.x_s[e / C][e % C] = 0.f;
+        for (int e = t - 64 * NW; e < NT * C; e += 64 * NW) s.x_t[e / C][e % C] = s.x_s[e / C][e % C] = 0.f;
     float rg = 0.f, ry = 0.f;
     size_t at_k = (size_t)(row0 + max(nc - 1, 0) * C) * sk + (size_t)hk * DK;   // the next chunk's rows
     size_t at_v = (size_t)(row0 + max(nc - 1, 0) * C) * sv + (size_t)h * DV;
@@ -918,12 +931,17 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
                 const int u = lane_id();
                 float z = 0.f, cx = 0.f;
                 if (u < C) {
-                    z = (s.z[0][u] + s.z[1][u]) + (s.z[2][u] + s.z[3][u]);
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) z += s.z[j][u];
                     cx = y;
 #pragma unroll
                     for (int j = 0; j < NT; ++j) cx += s.x_t[j][u] - s.x_s[j][u];
                 }
-                if (anchor >= 0) R = (s.r[0] + s.r[1]) + (s.r[2] + s.r[3]);
+                if (anchor >= 0) {
+                    R = 0.0;
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) R += s.r[j];
+                }
                 float up = z, down = cx;                       // inclusive sums from below, from above
 #pragma unroll
                 for (int m = 1; m < C; m *= 2) {
@@ -959,14 +977,14 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
 }
 
 template <typename T, int DK, int DV, bool DG>
-__global__ __launch_bounds__(512, 2) void linear_dkdv_kernel(const LinearBwdParams b)
+__global__ __launch_bounds__((128 * pair_waves<DK, DV>), (pair_waves<DK, DV> / 2)) void linear_dkdv_kernel(const LinearBwdParams b)
 {
     extern __shared__ __align__(16) char smem[];
     DkdvLds<T, DK, DV> &s = *reinterpret_cast<DkdvLds<T, DK, DV> *>(smem);
     const int h = (int)(blockIdx.x % (unsigned)b.c.H), id = (int)(blockIdx.x / (unsigned)b.c.H);
     Piece w;
     if (!find_piece(b.c, id, w)) return;
-    if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 8))
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x) >= 64 * pair_waves<DK, DV>)
         dkdv_walk<T, DK, DV, DG, true>(b, s, w, id, h);
     else
         dkdv_walk<T, DK, DV, DG, false>(b, s, w, id, h);
@@ -1042,7 +1060,7 @@ template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdPar
         if ((e = hipGetLastError()) != hipSuccess) return e;
         s = c;
         s.k = c.q; s.v = b.d_o;
-        hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE_REV>), grid, block, 0, stream, s);
+        hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE_REV>), grid, dim3(64 * pair_waves<DK, DV>), 0, stream, s);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         dq.part = b.part_fwd; dq.dec = b.dec_fwd;
     }
@@ -1055,7 +1073,7 @@ template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdPar
     // above 64 KiB a kernel asks for its dynamic LDS; per device, so with every launch
     e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, grid, dim3(512), lds, stream, b);
+    hipLaunchKernelGGL(kernel, grid, dim3(128 * pair_waves<DK, DV>), lds, stream, b);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (c.defer) {
         hipLaunchKernelGGL(linear_deferred_kernel, grid, block, 0, stream, c, b.dh0, 1, DK * DV);
