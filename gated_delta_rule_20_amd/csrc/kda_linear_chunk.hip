@@ -167,18 +167,18 @@ template <typename T, int D, int NT> struct Stage {
 };
 
 // Decay vectors of one chunk.
-template <int C> struct Decay {
+template <int C> struct alignas(16) Decay {
     float hi[C], lo[C];      // G in units of log 2, as hi + lo
     float inter[C];          // factor of the state's part of output row r
     float state[C];          // factor of source row s in the state
     float total;             // e^{G_end}
 };
 
-// One wave: lane u holds the log-decay x of token u (0 behind the chunk's last).
+// One wave: lane u holds the log-decay of token u (0 behind the chunk's last).
 template <int C, bool REV> __device__ __forceinline__ void make_decay(Decay<C> *d, float x, float scale)
 {
     const int u = lane_id();
-    double G = u < C ? (double)x : 0.0;
+    double G = u < C ? (double)log2_decay(x) : 0.0;
 #pragma unroll
     for (int s = 1; s < C; s *= 2) {
         const double y = __shfl_up(G, s);
@@ -362,11 +362,16 @@ template <typename T, int DK, int DV, bool REV, int NW> struct Group {
     static __device__ __forceinline__ f32x4 scores(const T *Q, const T *K, int rt, int st)
     {
         const int l = lane_id(), x = l & 15, g = l >> 4;
+        frag_t<T> k[KS], q[KS];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            k[ks] = load_frag_lin<T>(K + (16 * st + x) * LDK + 32 * ks, g);
+            q[ks] = load_frag_lin<T>(Q + (16 * rt + x) * LDK + 32 * ks, g);
+        }
+        __builtin_amdgcn_sched_barrier(0);                     // all reads in flight before the first product
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-            acc = mma(load_frag_lin<T>(K + (16 * st + x) * LDK + 32 * ks, g),
-                      load_frag_lin<T>(Q + (16 * rt + x) * LDK + 32 * ks, g), acc);
+        for (int ks = 0; ks < KS; ++ks) acc = mma(k[ks], q[ks], acc);
         return acc;
     }
     // Those scores with their decays, 0 where s is not a source of r (on the diagonal tile).
@@ -615,12 +620,15 @@ __device__ __forceinline__ bool deferred(const LinearChunkParams &p, const Piece
     return p.defer && w.parts > 1 && w.slot + i < p.n_part;
 }
 
-// The log-decay of a chunk's token u for this lane (log 2 units), 0 behind the last.
+// The log-decay of a chunk's token u for this lane, 0 behind the last; as it is in memory, so that nothing waits
+// for it here.  n >= 1.
 __device__ __forceinline__ float fetch_decay(const LinearChunkParams &p, int row, int h, int n)
 {
     const int u = lane_id();
-    if (u >= n) return 0.f;
-    return log2_decay(p.g_per_head ? p.g[h] : p.g[(size_t)(row + u) * p.H + h]);
+    const unsigned step = 4u * (unsigned)p.H;
+    const __amdgpu_buffer_rsrc_t rs = p.g_per_head ? window(p.g + h, 4) : rows_window(p.g + (size_t)row * p.H + h, n, step, 4);
+    const unsigned at = !p.g_per_head ? u * step : u < n ? 0u : 4u;
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (int)at, 0, 0));
 }
 
 // Waves of each kind in linear_dkdv_kernel.
@@ -701,12 +709,19 @@ __global__ __launch_bounds__((64 * walk_waves<DK, DV, MODE>), (walk_waves<DK, DV
         gq += step_q;
         gk += step_q;
         gv += step_v;
-        if (wv == 3) rg = fetch_decay(p, row0 + c * C, h, n);
+    };
+    // decays are fetched two chunks ahead: they are summed while the tiles of the chunk between are in flight
+    auto decays_of = [&](int i) {
+        const int c = REV ? nc - 1 - i : i;
+        return fetch_decay(p, row0 + c * C, h, min(C, toks - c * C));
     };
     if (OUT) G::clear_scores(sP, wv);
     if (nc > 0) {
         fetch(REV ? nc - 1 : 0);
-        if (wv == 3) make_decay<C, REV>(&sD[0], rg, p.scale);
+        if (wv == NW - 1) {
+            make_decay<C, REV>(&sD[0], decays_of(0), p.scale);
+            if (nc > 1) rg = decays_of(1);
+        }
     }
     for (int i = 0; i < nc; ++i) {
         const int c = REV ? nc - 1 - i : i, n = min(C, toks - c * C), row = row0 + c * C;
@@ -717,6 +732,12 @@ __global__ __launch_bounds__((64 * walk_waves<DK, DV, MODE>), (walk_waves<DK, DV
         rv.store(sV, t);
         lds_barrier();
         if (i + 1 < nc) fetch(REV ? c - 1 : c + 1);
+        auto next_decay = [&]() {
+            if (wv != NW - 1 || i + 1 >= nc) return;
+            const float x = rg;
+            if (i + 2 < nc) rg = decays_of(i + 2);
+            make_decay<C, REV>(&sD[(i + 1) & 1], x, p.scale);
+        };
         if constexpr (OUT) {
             f32x4 O[G::NT][G::NCT];
             G::make_scores(sP, sQ, sK, d, p.scale, wv);
@@ -736,7 +757,7 @@ __global__ __launch_bounds__((64 * walk_waves<DK, DV, MODE>), (walk_waves<DK, DV
             } else {
                 grp.template inter<1>(O, sQ, d);
             }
-            if (wv == 3 && i + 1 < nc) make_decay<C, REV>(&sD[(i + 1) & 1], rg, p.scale);
+            next_decay();
             lds_barrier();                                     // P (and y) are whole
             G::intra(O, sP, sV, wv);
             if (MODE == WALK_DQ && p.wide)
@@ -748,7 +769,7 @@ __global__ __launch_bounds__((64 * walk_waves<DK, DV, MODE>), (walk_waves<DK, DV
             if (MODE == WALK_DQ && p.y && t < n)
                 p.y[(size_t)(row + t) * p.H + h] = (sY[0][t] + sY[1 % 4][t]) + (sY[2 % 4][t] + sY[3 % 4][t]);
         } else {
-            if (wv == 3 && i + 1 < nc) make_decay<C, REV>(&sD[(i + 1) & 1], rg, p.scale);
+            next_decay();
             dec *= d.total;
         }
         grp.update(sK, sV, d, wv);
@@ -859,13 +880,16 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
         at_k -= C * sk;
         at_v -= C * sv;
         if (scribe) {
-            rg = fetch_decay(p, row, h, n);
             if (DG) ry = lane_id() < n ? p.y[(size_t)(row + lane_id()) * p.H + h] : 0.f;
         }
     };
+    auto decays_of = [&](int c) { return fetch_decay(p, row0 + c * C, h, min(C, toks - c * C)); };
     if (nc > 0) {
         fetch(nc - 1);
-        if (scribe) make_decay<C, true>(&s.decay[0], rg, p.scale);
+        if (scribe) {
+            make_decay<C, true>(&s.decay[0], decays_of(nc - 1), p.scale);
+            if (nc > 1) rg = decays_of(nc - 2);
+        }
     }
     double R = 0.0, sum_dg = 0.0;
     for (int i = 0; i < nc; ++i) {
@@ -905,7 +929,11 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
                 G::make_scores(s.p[0], s.k, s.q, d, p.scale, wv);
             }
             grp.template inter<1>(O, s.k, d);
-            if (scribe && i + 1 < nc) make_decay<C, true>(&s.decay[(i + 1) & 1], rg, p.scale);
+            if (scribe && i + 1 < nc) {
+                const float x = rg;
+                if (i + 2 < nc) rg = decays_of(c - 2);
+                make_decay<C, true>(&s.decay[(i + 1) & 1], x, p.scale);
+            }
         } else {
             G::make_scores(s.p[1], s.v, s.d_o, d, p.scale, wv);
             if constexpr (DG) {
