@@ -35,8 +35,8 @@ __device__ __forceinline__ void copy_slice(const CachePools &pools, int slice, i
     int i = 0;
     while (slice >= pools.pool[i].slices) slice -= pools.pool[i++].slices;
     const CachePool &p = pools.pool[i];
-    const size_t begin = (size_t)slice * CACHE_SLICE;
-    const size_t end = min(begin + CACHE_SLICE, p.page_bytes);
+    const size_t begin = (size_t)slice * pools.slice;
+    const size_t end = min(begin + pools.slice, p.page_bytes);
     char *dst = p.dst + (size_t)to * p.page_bytes;
     const char *src = p.src + (size_t)from * p.page_bytes;
     switch (p.unit) {

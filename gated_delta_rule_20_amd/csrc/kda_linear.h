@@ -76,12 +76,12 @@ struct CachePool {
 };
 
 constexpr int CACHE_MAX_POOLS = 8;
-constexpr size_t CACHE_SLICE = 32768; // bytes one workgroup copies
 
 struct CachePools {
     CachePool pool[CACHE_MAX_POOLS];
     int n;
-    int slices;                       // over all pools
+    size_t slice;                     // bytes one workgroup copies
+    int slices;                       // of a page, over all pools
 };
 
 hipError_t launch_cache_copy(const CachePools &pools, int n_dst, int n_src, const int32_t *dst_pages,

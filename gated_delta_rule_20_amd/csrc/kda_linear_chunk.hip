@@ -212,11 +212,11 @@ __device__ __forceinline__ double wave_total(double v)
     return v;
 }
 
-// The work of NW waves on one chunk: output columns (and state columns) are
+// The work of NW = 4 waves on one chunk: output columns (and state columns) are
 // dealt 16 * NCT to a wave.  DK: contracted width, DV: output width.
-template <typename T, int DK, int DV, bool REV, int NW> struct Group {
+constexpr int NW = 4;
+template <typename T, int DK, int DV, bool REV> struct Group {
     static constexpr int C = chunk_of<T>, NT = C / 16, NRT = DK / 16, NCT = DV / 16 / NW, KS = DK / 32, CK = C / 32;
-    static_assert(NCT == 1 || NCT == 2, "one or two column tiles a wave");
     static constexpr int LDK = ld_of<T>(DK), LDV = ld_of<T>(DV), LDP = ldp_of<T>;
 
     // With two column tiles a lane's rows of both tiles are made neighbours (8 columns: one wide access).
@@ -311,15 +311,19 @@ template <typename T, int DK, int DV, bool REV, int NW> struct Group {
     {
         const __amdgpu_buffer_rsrc_t rs = state_window(m);
         const int at = state_lane<TR>(w);
+        f32x4 y[NRT][NCT];
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) y[rt][ct] = fetch<TR>(rs, at, rt, ct);
+        __builtin_amdgcn_sched_barrier(0);                     // one wait for all of it
         double s = 0.0;
 #pragma unroll
         for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                const f32x4 y = fetch<TR>(rs, at, rt, ct);
+            for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s += (double)S[rt][ct][i] * (double)y[i];
-            }
+                for (int i = 0; i < 4; ++i) s += (double)S[rt][ct][i] * (double)y[rt][ct][i];
         return wave_total(s);
     }
 
@@ -415,16 +419,12 @@ template <typename T, int DK, int DV, bool REV, int NW> struct Group {
     template <typename F> static __device__ __forceinline__ void for_tiles(int w, F f)
     {
 #pragma unroll
-        for (int i = 0; i < (NT == 4 && NW == 4 ? 3 : NT == 4 ? 2 : 1); ++i) {
+        for (int i = 0; i < (NT == 4 ? 3 : 1); ++i) {
             int rt, st;
-            if (NT == 4 && NW == 4) {
+            if (NT == 4) {
                 if (w == 3 && i > 0) break;
                 rt = w == 3 ? 3 : w == 2 ? 2 : w == 1 ? (i < 2 ? 1 : 3) : (i < 1 ? 0 : 3);
                 st = w == 3 ? 3 : w == 2 ? i : w == 1 ? i : (i < 1 ? 0 : i - 1);
-            } else if (NT == 4) {
-                if (w > 5 || (w > 3 && i > 0)) break;         // rows 3, 2, (2, 1), (1, 0)
-                rt = w < 2 ? 3 : w == 2 ? 2 : w == 3 ? 2 - i : 1 - (w - 4);
-                st = w < 2 ? 2 * w + i : w == 2 ? i : w == 3 ? 2 - i : 0;
             } else {
                 if (w >= 3) break;
                 rt = w > 0;
@@ -631,9 +631,6 @@ __device__ __forceinline__ float fetch_decay(const LinearChunkParams &p, int row
     return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (int)at, 0, 0));
 }
 
-// Waves of each kind in linear_dkdv_kernel.
-template <int DK, int DV> constexpr int pair_waves = DK == 128 && DV == 128 ? 8 : 4;
-
 enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ, WALK_STATE_DQ };
 
 // One workgroup walks one segment for one value head (head fastest, so that
@@ -645,14 +642,12 @@ enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ, WALK_STATE_DQ };
 //   WALK_DQ         do, v, k (DK = the problem's Dv, DV = its Dk);  writes dq, y, anchors
 // 66 KiB of LDS and up to 256 registers a lane: two workgroups share a compute
 // unit, and one computes while the other waits for memory.
-template <int DK, int DV, int MODE> constexpr int walk_waves = MODE == WALK_STATE_REV ? pair_waves<DK, DV> : 4;
-
 template <typename T, int DK, int DV, int MODE>
-__global__ __launch_bounds__((64 * walk_waves<DK, DV, MODE>), (walk_waves<DK, DV, MODE> / 2)) void linear_walk_kernel(const LinearChunkParams p)
+__global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChunkParams p)
 {
-    constexpr int NW = walk_waves<DK, DV, MODE>, THREADS = 64 * NW;
+    constexpr int THREADS = 64 * NW;
     constexpr bool REV = MODE == WALK_STATE_REV, OUT = MODE == WALK_OUT || MODE == WALK_DQ, TR = MODE == WALK_DQ;
-    using G = Group<T, DK, DV, REV, NW>;
+    using G = Group<T, DK, DV, REV>;
     constexpr int C = G::C;
     __shared__ __align__(16) T sQ[OUT ? C * G::LDK : 8];
     __shared__ __align__(16) T sK[C * G::LDK];
@@ -731,6 +726,20 @@ __global__ __launch_bounds__((64 * walk_waves<DK, DV, MODE>), (walk_waves<DK, DV
         rk.store(sK, t);
         rv.store(sV, t);
         lds_barrier();
+        // q's rows for y, before the next tiles: what is loaded later is waited for later
+        quad_t<T> yq[MODE == WALK_DQ ? G::NT : 1][G::NCT];
+        if constexpr (MODE == WALK_DQ)
+            if (p.y) {
+                const T *q0 = (const T *)p.q_rows + ((size_t)row * Hk + hk) * DV;
+                const unsigned sb = (unsigned)(Hk * DV * sizeof(T));
+                const __amdgpu_buffer_rsrc_t rs = rows_window(q0, n, sb, DV * sizeof(T));
+                const unsigned at = (unsigned)(t & 15) * sb + G::first_col(wv) * (unsigned)sizeof(T);
+#pragma unroll
+                for (int it = 0; it < G::NT; ++it)
+#pragma unroll
+                    for (int ct = 0; ct < G::NCT; ++ct)
+                        yq[it][ct] = load_quad(q0, rs, (int)(at + 16u * it * sb + 4u * ct * sizeof(T)));
+            }
         if (i + 1 < nc) fetch(REV ? c - 1 : c + 1);
         auto next_decay = [&]() {
             if (wv != NW - 1 || i + 1 >= nc) return;
@@ -744,13 +753,7 @@ __global__ __launch_bounds__((64 * walk_waves<DK, DV, MODE>), (walk_waves<DK, DV
             if constexpr (MODE == WALK_DQ) {
                 if (p.y) {
                     grp.template inter<split_of<T>>(O, sQ, d);
-                    const T *q0 = (const T *)p.q_rows + ((size_t)row * Hk + hk) * DV;
-                    const unsigned sb = (unsigned)(Hk * DV * sizeof(T));
-                    const __amdgpu_buffer_rsrc_t rs = rows_window(q0, n, sb, DV * sizeof(T));
-                    const unsigned at = (unsigned)(t & 15) * sb + G::first_col(wv) * (unsigned)sizeof(T);
-                    G::row_dots(sY[wv], [&](int it, int ct) {
-                        return load_quad(q0, rs, (int)(at + 16u * it * sb + 4u * ct * sizeof(T)));
-                    }, O);
+                    G::row_dots(sY[wv], [&](int it, int ct) { return yq[it][ct]; }, O);
                 } else {
                     grp.template inter<1>(O, sQ, d);
                 }
@@ -820,7 +823,6 @@ __global__ __launch_bounds__(256) void linear_deferred_kernel(const LinearChunkP
 // from the state that WALK_DQ left at every anchor, and w is 0 where e^{G_end} < 2^-24 (then w is below the rounding
 // of R), so the roundings of y and z do not pile up.
 template <typename T, int DK, int DV> struct DkdvLds {
-    static constexpr int NW = pair_waves<DK, DV>;
     static constexpr int C = chunk_of<T>, LK = ld_of<T>(DK), LV = ld_of<T>(DV), LP = ldp_of<T>;
     T q[C * LK], k[C * LK], v[C * LV], d_o[C * LV];
     T p[2][C * LP];           // decayed scores of dV and of dK
@@ -838,9 +840,9 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
 {
     const LinearChunkParams &p = b.c;
     using L = DkdvLds<T, DK, DV>;
-    constexpr int NW = L::NW, THREADS = 128 * NW;
-    using GV = Group<T, DK, DV, true, NW>;    // rows k, sources q, values dO, state dS
-    using GK = Group<T, DV, DK, true, NW>;    // rows v, sources dO, values q, state dS^T
+    constexpr int THREADS = 128 * NW;
+    using GV = Group<T, DK, DV, true>;    // rows k, sources q, values dO, state dS
+    using GK = Group<T, DV, DK, true>;    // rows v, sources dO, values q, state dS^T
     using G = typename std::conditional<KEYS, GK, GV>::type;
     constexpr int C = G::C, NT = G::NT;
     const int t = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(t >> 6) & (NW - 1);
@@ -904,6 +906,11 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
         ro.store(s.d_o, t);
         const float y = ry;
         lds_barrier();
+        if constexpr (DG && KEYS)                              // before the next loads: they would be waited for with it
+            if (anchor >= 0) {
+                const double r = grp.template dot<true>(p.anchors + ((size_t)anchor * p.H + h) * part_size, wv);
+                if (lane_id() == 0) s.r[wv] = r;
+            }
         if (i + 1 < nc) fetch(c - 1);
         f32x4 O[NT][G::NCT];
         if constexpr (!KEYS) {
@@ -937,15 +944,11 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
         } else {
             G::make_scores(s.p[1], s.v, s.d_o, d, p.scale, wv);
             if constexpr (DG) {
-                const int l = lane_id(), x = l & 15;
+                const int x = lane_id() & 15;
                 grp.template inter<split_of<T>>(O, s.v, d);
                 G::row_dots(s.z[wv], [&](int it, int ct) {
                     return *reinterpret_cast<const quad_t<T> *>(s.k + (16 * it + x) * L::LK + G::first_col(wv) + 4 * ct);
                 }, O);
-                if (anchor >= 0) {
-                    const double r = grp.template dot<true>(p.anchors + ((size_t)anchor * p.H + h) * part_size, wv);
-                    if (l == 0) s.r[wv] = r;
-                }
             } else {
                 grp.template inter<1>(O, s.v, d);
             }
@@ -1005,14 +1008,14 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
 }
 
 template <typename T, int DK, int DV, bool DG>
-__global__ __launch_bounds__((128 * pair_waves<DK, DV>), (pair_waves<DK, DV> / 2)) void linear_dkdv_kernel(const LinearBwdParams b)
+__global__ __launch_bounds__(128 * NW, 2) void linear_dkdv_kernel(const LinearBwdParams b)
 {
     extern __shared__ __align__(16) char smem[];
     DkdvLds<T, DK, DV> &s = *reinterpret_cast<DkdvLds<T, DK, DV> *>(smem);
     const int h = (int)(blockIdx.x % (unsigned)b.c.H), id = (int)(blockIdx.x / (unsigned)b.c.H);
     Piece w;
     if (!find_piece(b.c, id, w)) return;
-    if (__builtin_amdgcn_readfirstlane(threadIdx.x) >= 64 * pair_waves<DK, DV>)
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x) >= 64 * NW)
         dkdv_walk<T, DK, DV, DG, true>(b, s, w, id, h);
     else
         dkdv_walk<T, DK, DV, DG, false>(b, s, w, id, h);
@@ -1061,7 +1064,7 @@ __global__ __launch_bounds__(256) void linear_share_kernel(const LinearChunkPara
 
 template <typename T, int DK, int DV> static hipError_t fwd_t(const LinearChunkParams &p, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((size_t)p.n_seg * p.H)), block(256);
+    const dim3 grid((unsigned)((size_t)p.n_seg * p.H)), block(64 * NW);
     if (p.part) {
         hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE>), grid, block, 0, stream, p);
         const hipError_t e = hipGetLastError();
@@ -1077,7 +1080,7 @@ template <typename T, int DK, int DV> static hipError_t fwd_t(const LinearChunkP
 template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdParams &b, hipStream_t stream)
 {
     const LinearChunkParams &c = b.c;
-    const dim3 grid((unsigned)((size_t)c.n_seg * c.H)), block(256);
+    const dim3 grid((unsigned)((size_t)c.n_seg * c.H)), block(64 * NW);
     hipError_t e;
     LinearChunkParams dq = c;
     if (c.part) {
@@ -1088,7 +1091,7 @@ template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdPar
         if ((e = hipGetLastError()) != hipSuccess) return e;
         s = c;
         s.k = c.q; s.v = b.d_o;
-        hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE_REV>), grid, dim3(64 * pair_waves<DK, DV>), 0, stream, s);
+        hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE_REV>), grid, block, 0, stream, s);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         dq.part = b.part_fwd; dq.dec = b.dec_fwd;
     }
@@ -1101,7 +1104,7 @@ template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdPar
     // above 64 KiB a kernel asks for its dynamic LDS; per device, so with every launch
     e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, grid, dim3(128 * pair_waves<DK, DV>), lds, stream, b);
+    hipLaunchKernelGGL(kernel, grid, dim3(128 * NW), lds, stream, b);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (c.defer) {
         hipLaunchKernelGGL(linear_deferred_kernel, grid, block, 0, stream, c, b.dh0, 1, DK * DV);
