@@ -11,8 +11,8 @@ from __future__ import annotations
 
 import torch
 
-from . import CACHE_MAX_POOLS, CachePool, _dev, _ptr
-from .linear import _call, _on_device
+from . import CACHE_MAX_POOLS, CachePool, _dev
+from .linear import _call, _check_tensors
 
 
 def _pools(dst, src=None):
@@ -25,14 +25,14 @@ def _pools(dst, src=None):
     arr = (CachePool * len(dst))()
     for i, (d, s) in enumerate(zip(dst, src)):
         _dev(d, "pool")
+        if d.device != dst[0].device:
+            raise ValueError(f"pool {i} is on another device than the first")
         if s is not d:
-            _dev(s, "source pool", d.dtype)
+            _check_tensors(d.device, d.dtype, source_pool=s)
         if d.dim() < 1 or s.dim() < 1 or d.shape[1:] != s.shape[1:]:
             raise ValueError(f"pool {i}: pages of {tuple(d.shape[1:])} and {tuple(s.shape[1:])}")
         if d.shape[0] != dst[0].shape[0] or s.shape[0] != src[0].shape[0]:
             raise ValueError("all pools of a call must have the same number of pages")
-        if d.device != dst[0].device or s.device != dst[0].device:
-            raise ValueError(f"pool {i} is on another device than the first")
         page = d.element_size()
         for n in d.shape[1:]:
             page *= n
@@ -46,17 +46,14 @@ def _pools(dst, src=None):
 
 
 def _list(t, name, device):
-    _dev(t, name, torch.int32)
+    _check_tensors(device, torch.int32, **{name: t})
     if t is None or t.dim() != 1:
         raise ValueError(f"{name} must be a 1-d int32 tensor")
-    _on_device(device, **{name: t})
     return t.shape[0]
 
 
 def _tables(table, refcount, device, n_pages=None):
-    _dev(table, "table", torch.int32)
-    _dev(refcount, "refcount", torch.int32)
-    _on_device(device, table=table, refcount=refcount)
+    _check_tensors(device, torch.int32, table=table, refcount=refcount)
     if table.dim() != 2:
         raise ValueError(f"table must be [rows, per_row], got {tuple(table.shape)}")
     if refcount.dim() != 1 or (n_pages is not None and refcount.shape[0] != n_pages):
@@ -74,7 +71,7 @@ def cache_copy(pools, src_pools, dst_pages, src_pages, *, stream=None) -> None:
     n = _list(dst_pages, "dst_pages", device)
     if _list(src_pages, "src_pages", device) != n:
         raise ValueError("dst_pages and src_pages must have the same length")
-    _call("kda_cache_copy", (arr, n_pools, n_dst, n_src, _ptr(dst_pages), _ptr(src_pages), n), stream, device)
+    _call("kda_cache_copy", (arr, n_pools, n_dst, n_src, dst_pages.data_ptr(), src_pages.data_ptr(), n), stream, device)
 
 
 def cache_fork(pools, table, refcount, parents, children, *, stream=None):
@@ -90,8 +87,8 @@ def cache_fork(pools, table, refcount, parents, children, *, stream=None):
     if _list(children, "children", device) != n:
         raise ValueError("parents and children must have the same length")
     pages = torch.empty((2, n), dtype=torch.int32, device=device)
-    _call("kda_cache_fork", (arr, n_pools, n_pages, _ptr(table), table.shape[0], table.shape[1], _ptr(refcount),
-                             _ptr(parents), _ptr(children), n, pages.data_ptr(), pages.data_ptr() + 4 * n), stream, device)
+    _call("kda_cache_fork", (arr, n_pools, n_pages, table.data_ptr(), table.shape[0], table.shape[1], refcount.data_ptr(),
+                             parents.data_ptr(), children.data_ptr(), n, pages.data_ptr(), pages.data_ptr() + 4 * n), stream, device)
     return pages[1]
 
 
@@ -100,7 +97,7 @@ def cache_free(table, refcount, rows, *, stream=None) -> None:
     _dev(table, "table", torch.int32)
     _tables(table, refcount, table.device)
     n = _list(rows, "rows", table.device)
-    _call("kda_cache_free", (_ptr(table), table.shape[0], table.shape[1], _ptr(refcount), refcount.shape[0], _ptr(rows),
+    _call("kda_cache_free", (table.data_ptr(), table.shape[0], table.shape[1], refcount.data_ptr(), refcount.shape[0], rows.data_ptr(),
                              n), stream, table.device)
 
 
@@ -114,6 +111,6 @@ def cache_compact(pools, table, refcount, *, stream=None):
     _tables(table, refcount, device, n_pages)
     buf = torch.empty(2 * n_pages + 2, dtype=torch.int32, device=device)
     at = buf.data_ptr()
-    _call("kda_cache_compact", (arr, n_pools, n_pages, _ptr(table), table.shape[0], table.shape[1], _ptr(refcount), at,
+    _call("kda_cache_compact", (arr, n_pools, n_pages, table.data_ptr(), table.shape[0], table.shape[1], refcount.data_ptr(), at,
                                 at + 4 * n_pages, at + 8 * n_pages), stream, device)
     return buf[:n_pages], buf[2 * n_pages:2 * n_pages + 1]

@@ -9,46 +9,58 @@ import ctypes
 
 import torch
 
-from . import _DTYPES, LinearBwdArgs, LinearFwdArgs, LinearStepArgs, _check, _dev, _ptr, _stream, load_library
+from . import _DTYPES, LinearBwdArgs, LinearFwdArgs, LinearStepArgs, _check, _dev, load_library
 
 
-def _on_device(device, **tensors):
-    """Every given tensor lives on ``device``."""
+def _check_tensors(device, dtype, **tensors):
+    """Every given tensor is contiguous, on ``device`` and of ``dtype`` (None: any).  A decode step's time is mostly the
+    host's, so the good case is one line a tensor."""
     for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the call is on {device}")
+        if t is None or (isinstance(t, torch.Tensor) and t.device == device and (dtype is None or t.dtype is dtype)
+                         and t.is_contiguous()):
+            continue
+        _dev(t, name, dtype)
+        raise ValueError(f"{name} is on {t.device}, the call is on {device}")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _call(fn, args, stream, device):
     """The library launches on the current device: make it the tensors' own."""
     lib = load_library()
-    if device.index == torch.cuda.current_device():
-        status = getattr(lib, fn)(*args, _stream(stream, device))
+    index = device.index
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = getattr(lib, fn)(*args, s)
     else:
         with torch.cuda.device(device):
-            status = getattr(lib, fn)(*args, _stream(stream, device))
-    _check(lib, fn, status)
+            status = getattr(lib, fn)(*args, s)
+    if status != 0:
+        _check(lib, fn, status)
 
 
 def _heads(q, k, v, g):
     """Checks q, k [..., Hk, Dk], v [..., H, Dv] and g [..., H] or [H]; returns (H, Hk, Dk, Dv, g_per_head)."""
-    if q.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {q.dtype}")
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _dev(t, name, q.dtype)
-    _dev(g, "g", torch.float32)
-    _on_device(q.device, k=k, v=v, g=g)
-    if k.shape != q.shape:
-        raise ValueError(f"k must have q's shape {tuple(q.shape)}, got {tuple(k.shape)}")
-    if v.dim() != q.dim() or v.shape[:-2] != q.shape[:-2]:
-        raise ValueError(f"v must be [..., H, Dv] over q's leading axes {tuple(q.shape[:-2])}, got {tuple(v.shape)}")
-    H, Hk = v.shape[-2], q.shape[-2]
-    if Hk < 1 or H % Hk != 0:
+    dtype = q.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    _dev(q, "q")
+    _check_tensors(q.device, dtype, k=k, v=v)
+    _check_tensors(q.device, torch.float32, g=g)
+    qs, vs = q.shape, v.shape
+    if k.shape != qs:
+        raise ValueError(f"k must have q's shape {tuple(qs)}, got {tuple(k.shape)}")
+    if len(vs) != len(qs) or len(qs) < 3 or vs[:-2] != qs[:-2]:
+        raise ValueError(f"v must be [..., H, Dv] over q's leading axes {tuple(qs[:-2])}, got {tuple(vs)}")
+    H, Hk = vs[-2], qs[-2]
+    if Hk < 1 or H < 1 or H % Hk != 0:
         raise ValueError(f"v's {H} heads must be a multiple of q's {Hk}")
     per_head = g.dim() == 1
-    if not (tuple(g.shape) == (H,) if per_head else g.shape == v.shape[:-1]):
-        raise ValueError(f"g must be [H] = [{H}] or {tuple(v.shape[:-1])}, got {tuple(g.shape)}")
-    return H, Hk, q.shape[-1], v.shape[-1], per_head
+    if (g.shape[0] != H) if per_head else (g.shape != vs[:-1]):
+        raise ValueError(f"g must be [H] = [{H}] or {tuple(vs[:-1])}, got {tuple(g.shape)}")
+    return H, Hk, qs[-1], vs[-1], per_head
 
 
 def _sequences(q, v, cu_seqlens):
@@ -57,8 +69,7 @@ def _sequences(q, v, cu_seqlens):
         if q.dim() != 4:
             raise ValueError(f"q must be [B, T, Hk, Dk], got {tuple(q.shape)}")
         return q.shape[0], q.shape[1], q.shape[0]
-    _dev(cu_seqlens, "cu_seqlens", torch.int32)
-    _on_device(q.device, cu_seqlens=cu_seqlens)
+    _check_tensors(q.device, torch.int32, cu_seqlens=cu_seqlens)
     if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[0] != 1):
         raise ValueError(f"with cu_seqlens q must be [T, Hk, Dk], got {tuple(q.shape)}")
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
@@ -68,21 +79,18 @@ def _sequences(q, v, cu_seqlens):
 
 def _state(t, name, shape, device):
     if t is not None:
-        _dev(t, name, torch.float32)
-        if tuple(t.shape) != shape:
+        _check_tensors(device, torch.float32, **{name: t})
+        if t.shape != shape:
             raise ValueError(f"{name} must be [N, H, Dk, Dv] = {shape}, got {tuple(t.shape)}")
-        _on_device(device, **{name: t})
-    return t
 
 
-def _like(t, name, ref, dtype=None):
+def _like(t, name, ref):
     """An output: allocated like ref when not given, checked when given."""
     if t is None:
-        return torch.empty(ref.shape, dtype=dtype or ref.dtype, device=ref.device)
-    _dev(t, name, dtype or ref.dtype)
+        return torch.empty_like(ref)
+    _check_tensors(ref.device, ref.dtype, **{name: t})
     if t.shape != ref.shape:
         raise ValueError(f"{name} must have shape {tuple(ref.shape)}, got {tuple(t.shape)}")
-    _on_device(ref.device, **{name: t})
     return t
 
 
@@ -92,8 +100,7 @@ def _workspace(fn, a, workspace, device):
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
     if workspace is not None:
-        _dev(workspace, "workspace")
-        _on_device(device, workspace=workspace)
+        _check_tensors(device, None, workspace=workspace)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     return workspace
 
@@ -117,16 +124,15 @@ def linear_chunk_fwd(q, k, v, g, *, scale: float = 1.0, cu_seqlens=None, initial
     _state(final_state, "final_state", shape, dev)
     slots = 0
     if checkpoints is not None:
-        _dev(checkpoints, "checkpoints", torch.float32)
-        _on_device(dev, checkpoints=checkpoints)
+        _check_tensors(dev, torch.float32, checkpoints=checkpoints)
         if (checkpoints.dim() != 5 or checkpoints.shape[0] != N or checkpoints.shape[1] < 1
                 or tuple(checkpoints.shape[2:]) != shape[1:] or checkpoint_every < 1):
             raise ValueError(f"checkpoints must be [N, slots >= 1, H, Dk, Dv] with N, H, Dk, Dv = {shape} and "
                              f"checkpoint_every >= 1; got {tuple(checkpoints.shape)}, every={checkpoint_every}")
         slots = checkpoints.shape[1]
-    a = LinearFwdArgs(B, T, H, Hk, Dk, Dv, _DTYPES[q.dtype], _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_head, scale,
-                      _ptr(cu_seqlens), N, _ptr(initial_state), _ptr(out), _ptr(final_state), None, 0,
-                      _ptr(checkpoints), checkpoint_every if slots else 0, slots)
+    a = LinearFwdArgs(B, T, H, Hk, Dk, Dv, _DTYPES[q.dtype], _at(q), _at(k), _at(v), _at(g), per_head, scale,
+                      _at(cu_seqlens), N, _at(initial_state), _at(out), _at(final_state), None, 0,
+                      _at(checkpoints), checkpoint_every if slots else 0, slots)
     workspace = _workspace("kda_linear_chunk_fwd_workspace_size", a, workspace, dev)
     _call("kda_linear_chunk_fwd", (ctypes.byref(a),), stream, dev)
     return out, final_state
@@ -141,10 +147,9 @@ def linear_chunk_bwd(q, k, v, g, d_o, *, scale: float = 1.0, cu_seqlens=None, in
     H, Hk, Dk, Dv, per_head = _heads(q, k, v, g)
     B, T, N = _sequences(q, v, cu_seqlens)
     dev, shape = q.device, (N, H, Dk, Dv)
-    _dev(d_o, "d_o", q.dtype)
-    if d_o.shape != v.shape:
-        raise ValueError(f"d_o must have v's shape {tuple(v.shape)}, got {tuple(d_o.shape)}")
-    _on_device(dev, d_o=d_o)
+    if d_o is None or d_o.shape != v.shape:
+        raise ValueError(f"d_o must have v's shape {tuple(v.shape)}, got {None if d_o is None else tuple(d_o.shape)}")
+    _check_tensors(dev, q.dtype, d_o=d_o)
     _state(initial_state, "initial_state", shape, dev)
     _state(dfinal_state, "dfinal_state", shape, dev)
     dq, dk, dv = _like(dq, "dq", q), _like(dk, "dk", k), _like(dv, "dv", v)
@@ -152,9 +157,9 @@ def linear_chunk_bwd(q, k, v, g, d_o, *, scale: float = 1.0, cu_seqlens=None, in
     if dinitial_state is None:
         dinitial_state = torch.empty(shape, dtype=torch.float32, device=dev)
     _state(dinitial_state, "dinitial_state", shape, dev)
-    a = LinearBwdArgs(B, T, H, Hk, Dk, Dv, _DTYPES[q.dtype], _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_head, scale,
-                      _ptr(cu_seqlens), N, _ptr(initial_state), _ptr(d_o), _ptr(dfinal_state), _ptr(dq), _ptr(dk),
-                      _ptr(dv), _ptr(dg), _ptr(dinitial_state), None, 0)
+    a = LinearBwdArgs(B, T, H, Hk, Dk, Dv, _DTYPES[q.dtype], _at(q), _at(k), _at(v), _at(g), per_head, scale,
+                      _at(cu_seqlens), N, _at(initial_state), _at(d_o), _at(dfinal_state), _at(dq), _at(dk),
+                      _at(dv), _at(dg), _at(dinitial_state), None, 0)
     workspace = _workspace("kda_linear_chunk_bwd_workspace_size", a, workspace, dev)
     _call("kda_linear_chunk_bwd", (ctypes.byref(a),), stream, dev)
     return dq, dk, dv, dg, dinitial_state
@@ -166,7 +171,7 @@ def linear_chunk_fwd_workspace_size(q, v, *, cu_seqlens=None) -> int:
         raise ValueError(f"unsupported dtype {q.dtype}")
     B, T, N = _sequences(q, v, cu_seqlens)
     a = LinearFwdArgs(B, T, v.shape[-2], q.shape[-2], q.shape[-1], v.shape[-1], _DTYPES[q.dtype], scale=1.0,
-                      cu_seqlens=_ptr(cu_seqlens), N=N)
+                      cu_seqlens=_at(cu_seqlens), N=N)
     return _need("kda_linear_chunk_fwd_workspace_size", a)
 
 
@@ -178,7 +183,7 @@ def linear_chunk_bwd_workspace_size(q, v, *, cu_seqlens=None, g_per_head: bool =
         raise ValueError(f"unsupported dtype {q.dtype}")
     B, T, N = _sequences(q, v, cu_seqlens)
     a = LinearBwdArgs(B, T, v.shape[-2], q.shape[-2], q.shape[-1], v.shape[-1], _DTYPES[q.dtype], scale=1.0,
-                      cu_seqlens=_ptr(cu_seqlens), N=N, g_per_head=g_per_head)
+                      cu_seqlens=_at(cu_seqlens), N=N, g_per_head=g_per_head)
     a.dg = 16 if need_dg else None             # only whether they are given is read
     a.d_final_state = 16 if dfinal_state else None
     return _need("kda_linear_chunk_bwd_workspace_size", a)
@@ -203,24 +208,20 @@ def linear_recurrent_step(q, k, v, g, state, *, scale: float = 1.0, slots=None, 
     H, Hk, Dk, Dv, per_head = _heads(q, k, v, g)
     if q.dim() != 3:
         raise ValueError(f"q must be [N, Hk, Dk], got {tuple(q.shape)}")
-    N = q.shape[0]
-    _dev(state, "state", torch.float32)
-    if state.dim() != 4 or tuple(state.shape[1:]) != (H, Dk, Dv):
-        raise ValueError(f"state must be [n_slots, H, Dk, Dv] with H, Dk, Dv = {(H, Dk, Dv)}, got {tuple(state.shape)}")
+    N, dev, shape = q.shape[0], q.device, state.shape
+    _check_tensors(dev, torch.float32, state=state, new_state=new_state)
+    if len(shape) != 4 or shape[1] != H or shape[2] != Dk or shape[3] != Dv:
+        raise ValueError(f"state must be [n_slots, H, Dk, Dv] with H, Dk, Dv = {(H, Dk, Dv)}, got {tuple(shape)}")
     if slots is not None:
-        _dev(slots, "slots", torch.int32)
-        if tuple(slots.shape) != (N,):
+        _check_tensors(dev, torch.int32, slots=slots)
+        if slots.dim() != 1 or slots.shape[0] != N:
             raise ValueError(f"slots must be [N] = [{N}], got {tuple(slots.shape)}")
     if new_state is None:
         new_state = state
-    elif _dev(new_state, "new_state", torch.float32).shape != state.shape:
-        raise ValueError(f"new_state must have state's shape {tuple(state.shape)}, got {tuple(new_state.shape)}")
-    if out is None:
-        out = torch.empty(v.shape, dtype=q.dtype, device=q.device)
-    elif _dev(out, "out", q.dtype).shape != v.shape:
-        raise ValueError(f"out must have v's shape {tuple(v.shape)}, got {tuple(out.shape)}")
-    _on_device(q.device, state=state, slots=slots, new_state=new_state, out=out)
-    a = LinearStepArgs(N, H, Hk, Dk, Dv, _DTYPES[q.dtype], _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_head, scale,
-                       _ptr(slots), state.shape[0], _ptr(state), _ptr(new_state), _ptr(out))
-    _call("kda_linear_recurrent_step", (ctypes.byref(a),), stream, q.device)
+    elif new_state.shape != shape:
+        raise ValueError(f"new_state must have state's shape {tuple(shape)}, got {tuple(new_state.shape)}")
+    out = _like(out, "out", v)
+    a = LinearStepArgs(N, H, Hk, Dk, Dv, _DTYPES[q.dtype], q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                       per_head, scale, _at(slots), shape[0], state.data_ptr(), new_state.data_ptr(), out.data_ptr())
+    _call("kda_linear_recurrent_step", (ctypes.byref(a),), stream, dev)
     return out
