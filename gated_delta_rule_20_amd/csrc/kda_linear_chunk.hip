@@ -125,6 +125,22 @@ __device__ __forceinline__ bf16x4 load_quad(const bf16 *, __amdgpu_buffer_rsrc_t
     return __builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(rs, voff, 0, 0));
 }
 __device__ __forceinline__ f32x4 load_quad(const float *, __amdgpu_buffer_rsrc_t rs, int voff) { return load16(rs, voff); }
+// 4 or 8 neighbouring elements
+template <typename T> __device__ __forceinline__ void load_cols(const T *p, __amdgpu_buffer_rsrc_t rs, int voff, quad_t<T> (&v)[1])
+{
+    v[0] = load_quad(p, rs, voff);
+}
+__device__ __forceinline__ void load_cols(const bf16 *, __amdgpu_buffer_rsrc_t rs, int voff, bf16x4 (&v)[2])
+{
+    const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(rs, voff, 0, 0);
+    v[0] = __builtin_bit_cast(bf16x4, u32x2{w[0], w[1]});
+    v[1] = __builtin_bit_cast(bf16x4, u32x2{w[2], w[3]});
+}
+__device__ __forceinline__ void load_cols(const float *, __amdgpu_buffer_rsrc_t rs, int voff, f32x4 (&v)[2])
+{
+    v[0] = load16(rs, voff);
+    v[1] = load16(rs, voff + 16);
+}
 __device__ __forceinline__ void store_quad(__amdgpu_buffer_rsrc_t rs, int voff, bf16x4 v)
 {
     __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), rs, voff, 0, 0);
@@ -735,12 +751,9 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChu
                 const __amdgpu_buffer_rsrc_t rs = rows_window(q0, n, sb, DV * sizeof(T));
                 const unsigned at = (unsigned)(t & 15) * sb + G::first_col(wv) * (unsigned)sizeof(T);
 #pragma unroll
-                for (int it = 0; it < G::NT; ++it)
-#pragma unroll
-                    for (int ct = 0; ct < G::NCT; ++ct)
-                        yq[it][ct] = load_quad(q0, rs, (int)(at + 16u * it * sb + 4u * ct * sizeof(T)));
+                for (int it = 0; it < G::NT; ++it) load_cols(q0, rs, (int)(at + 16u * it * sb), yq[it]);
             }
-        if (i + 1 < nc) fetch(REV ? c - 1 : c + 1);
+        if (MODE != WALK_DQ && i + 1 < nc) fetch(REV ? c - 1 : c + 1);
         auto next_decay = [&]() {
             if (wv != NW - 1 || i + 1 >= nc) return;
             const float x = rg;
@@ -757,6 +770,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChu
                 } else {
                     grp.template inter<1>(O, sQ, d);
                 }
+                if (i + 1 < nc) fetch(c + 1);                  // here, where q's rows have left their registers
             } else {
                 grp.template inter<1>(O, sQ, d);
             }
