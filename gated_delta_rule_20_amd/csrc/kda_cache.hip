@@ -12,40 +12,64 @@ namespace kda {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-// bytes [begin, end) of one page in accesses of U, by 256 threads
-template <typename U> __device__ __forceinline__ void copy_range(char *dst, const char *src, size_t begin, size_t end)
+// bytes [begin, end) of one page in accesses of U, by 256 threads, eight of each
+// in flight; go() is asked once, by every thread, between the first loads and the
+// first stores.
+template <typename U, typename F>
+__device__ __forceinline__ void copy_range(char *dst, const char *src, size_t begin, size_t end, F go)
 {
     const U *s = reinterpret_cast<const U *>(src + begin);
     U *d = reinterpret_cast<U *>(dst + begin);
-    const unsigned n = (unsigned)((end - begin) / sizeof(U));
-    unsigned i = threadIdx.x;
-    for (; i + 7 * 256 < n; i += 8 * 256) {   // eight accesses of each thread in flight
-        U x[8];
+    const unsigned n = (unsigned)((end - begin) / sizeof(U)), t = threadIdx.x;
+    U x[8];
+    const auto load = [&](unsigned base) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __builtin_nontemporal_load(s + i + j * 256);
+        for (unsigned j = 0; j < 8; ++j)
+            if (base + t + j * 256 < n) x[j] = __builtin_nontemporal_load(s + base + t + j * 256);
+    };
+    load(0);
+    if (!go()) return;
+    for (unsigned base = 0;;) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) __builtin_nontemporal_store(x[j], d + i + j * 256);
+        for (unsigned j = 0; j < 8; ++j)
+            if (base + t + j * 256 < n) __builtin_nontemporal_store(x[j], d + base + t + j * 256);
+        base += 8 * 256;
+        if (base >= n) break;
+        load(base);
     }
-    for (; i < n; i += 256) d[i] = s[i];
 }
 
 // One slice (of pools.slices) of page `from` to page `to`.
-__device__ __forceinline__ void copy_slice(const CachePools &pools, int slice, int from, int to)
+template <typename F> __device__ __forceinline__ void copy_slice(const CachePools &pools, int slice, int from, int to, F go)
 {
-    int i = 0;
-    while (slice >= pools.pool[i].slices) slice -= pools.pool[i++].slices;
-    const CachePool &p = pools.pool[i];
-    const size_t begin = (size_t)slice * pools.slice;
-    const size_t end = min(begin + pools.slice, p.page_bytes);
-    char *dst = p.dst + (size_t)to * p.page_bytes;
-    const char *src = p.src + (size_t)from * p.page_bytes;
-    switch (p.unit) {
-    case 16: copy_range<u32x4>(dst, src, begin, end); break;
-    case 4: copy_range<uint32_t>(dst, src, begin, end); break;
-    case 2: copy_range<uint16_t>(dst, src, begin, end); break;
-    default: copy_range<uint8_t>(dst, src, begin, end); break;
+    // Which pool the slice is of.  Field by field, without a variable index: that would put the kernel's arguments into
+    // scratch memory, at every workgroup's start (2000 pages of 17 KiB: 84 us, against 20 us).
+    char *dst = pools.pool[0].dst;
+    const char *src = pools.pool[0].src;
+    size_t bytes = pools.pool[0].page_bytes;
+    int unit = pools.pool[0].unit, slices = pools.pool[0].slices;
+#pragma unroll
+    for (int i = 1; i < CACHE_MAX_POOLS; ++i) {
+        const bool next = slice >= slices;
+        slice -= next ? slices : 0;
+        dst = next ? pools.pool[i].dst : dst;
+        src = next ? pools.pool[i].src : src;
+        bytes = next ? pools.pool[i].page_bytes : bytes;
+        unit = next ? pools.pool[i].unit : unit;
+        slices = next ? pools.pool[i].slices : slices;
+    }
+    const size_t begin = (size_t)slice * CACHE_SLICE;
+    const size_t end = min(begin + CACHE_SLICE, bytes);
+    dst += (size_t)to * bytes;
+    src += (size_t)from * bytes;
+    switch (unit) {
+    case 16: copy_range<u32x4>(dst, src, begin, end, go); break;
+    case 4: copy_range<uint32_t>(dst, src, begin, end, go); break;
+    case 2: copy_range<uint16_t>(dst, src, begin, end, go); break;
+    default: copy_range<uint8_t>(dst, src, begin, end, go); break;
     }
 }
+__device__ __forceinline__ bool always() { return true; }
 
 // One workgroup per (pair, slice).
 __global__ __launch_bounds__(256) void cache_copy_kernel(const CachePools pools, int n_dst, int n_src,
@@ -55,11 +79,12 @@ __global__ __launch_bounds__(256) void cache_copy_kernel(const CachePools pools,
     const int i = (int)(blockIdx.x / (unsigned)pools.slices), slice = (int)(blockIdx.x % (unsigned)pools.slices);
     const int to = dst_pages[i], from = src_pages[i];
     if (to < 0 || to >= n_dst || from < 0 || from >= n_src) return;
-    bool again = false;                       // a later pair has this destination
-    for (int j = i + 1 + (int)threadIdx.x; j < n; j += 256)
-        again |= dst_pages[j] == to && src_pages[j] >= 0 && src_pages[j] < n_src;
-    if (__syncthreads_or(again)) return;
-    copy_slice(pools, slice, from, to);
+    copy_slice(pools, slice, from, to, [&]() {
+        bool again = false;                   // a later pair has this destination
+        for (int j = i + 1 + (int)threadIdx.x; j < n; j += 256)
+            again |= dst_pages[j] == to && src_pages[j] >= 0 && src_pages[j] < n_src;
+        return !__syncthreads_or(again);
+    });
 }
 
 // The copies a fork planned: old_pages[i] to new_pages[i] (-1: none).
@@ -70,7 +95,7 @@ __global__ __launch_bounds__(256) void cache_fork_copy_kernel(const CachePools p
     const int i = (int)(blockIdx.x / (unsigned)pools.slices), slice = (int)(blockIdx.x % (unsigned)pools.slices);
     const int from = old_pages[i], to = new_pages[i];
     if (from < 0 || to < 0) return;
-    copy_slice(pools, slice, from, to);
+    copy_slice(pools, slice, from, to, always);
 }
 
 constexpr int PLAN = 1024;                    // threads of a planning workgroup
@@ -267,7 +292,7 @@ __global__ __launch_bounds__(256) void cache_compact_move_kernel(const CachePool
     const long work = (long)counts[1] * pools.slices;
     for (long i = b - remap; i < work; i += (long)gridDim.x - remap) {
         const int r = (int)(i / pools.slices);
-        copy_slice(pools, (int)(i % pools.slices), moves[2 * r], moves[2 * r + 1]);
+        copy_slice(pools, (int)(i % pools.slices), moves[2 * r], moves[2 * r + 1], always);
     }
 }
 

@@ -52,25 +52,13 @@ bool overlap(const void *a, const void *b, size_t bytes)
     return a && b && x < y + bytes && y < x + bytes;
 }
 
-// A workgroup copies one slice of a page.  Starting it (its pair, the search for
-// a later pair of the same destination) costs microseconds, so slices are large
-// where there are many bytes (256 pages of 2.1 MiB: 32 KiB 327 us, 128 KiB 222 us)
-// and small where few would leave compute units idle.
-constexpr size_t MIN_SLICE = 16384, MAX_SLICE = 131072, SLICES = 4096;
-
-// `pages`: how many pages the call moves.
-kda_status_t plan_pools(const kda_cache_pool_t *pools, int n, long long pages, bool two, kda::CachePools *out)
+kda_status_t plan_pools(const kda_cache_pool_t *pools, int n, bool two, kda::CachePools *out)
 {
-    out->n = 0;
-    out->slices = 0;
+    *out = {};
     if (n < 0 || n > KDA_CACHE_MAX_POOLS)
         return fail(KDA_ERROR_INVALID_VALUE, "n_pools=%d: must be 0..%d", n, KDA_CACHE_MAX_POOLS);
     if (n > 0 && !pools) return fail(KDA_ERROR_INVALID_VALUE, "pools is NULL");
     long long slices = 0;
-    double bytes = 0;
-    for (int i = 0; i < n; ++i) bytes += (double)pools[i].page_bytes * (double)pages;
-    const double share = bytes / SLICES;
-    out->slice = share >= (double)MAX_SLICE ? MAX_SLICE : ((size_t)share + MIN_SLICE) / MIN_SLICE * MIN_SLICE;
     for (int i = 0; i < n; ++i) {
         if (!pools[i].dst) return fail(KDA_ERROR_INVALID_VALUE, "pool %d is NULL", i);
         if (pools[i].page_bytes < 1) return fail(KDA_ERROR_INVALID_VALUE, "pool %d has no page bytes", i);
@@ -81,7 +69,7 @@ kda_status_t plan_pools(const kda_cache_pool_t *pools, int n, long long pages, b
         const uintptr_t low = (uintptr_t)p.dst | (uintptr_t)p.src | (uintptr_t)p.page_bytes;
         p.unit = low % 16 == 0 ? 16 : low % 4 == 0 ? 4 : low % 2 == 0 ? 2 : 1;
         if (p.page_bytes > ((size_t)1 << 40)) return fail(KDA_ERROR_NOT_SUPPORTED, "pool %d: pages above 1 TiB", i);
-        p.slices = (int)((p.page_bytes - 1) / out->slice + 1);
+        p.slices = (int)((p.page_bytes - 1) / kda::CACHE_SLICE + 1);
         slices += p.slices;
     }
     if (slices > 0x7fffffffLL) return fail(KDA_ERROR_NOT_SUPPORTED, "pages too large");
@@ -375,7 +363,7 @@ kda_status_t kda_cache_copy(const kda_cache_pool_t *pools, int32_t n_pools, int3
                             const int32_t *dst_pages, const int32_t *src_pages, int32_t n, void *stream)
 {
     kda::CachePools ps;
-    KDA_TRY(plan_pools(pools, n_pools, n, true, &ps));
+    KDA_TRY(plan_pools(pools, n_pools, true, &ps));
     if (n_dst_pages < 0 || n_src_pages < 0)
         return fail(KDA_ERROR_INVALID_VALUE, "page counts must be >= 0 (got %d, %d)", n_dst_pages, n_src_pages);
     KDA_TRY(check_list(dst_pages, n, "dst_pages"));
@@ -398,7 +386,7 @@ kda_status_t kda_cache_fork(const kda_cache_pool_t *pools, int32_t n_pools, int3
                             int32_t *old_pages, int32_t *new_pages, void *stream)
 {
     kda::CachePools ps;
-    KDA_TRY(plan_pools(pools, n_pools, n, false, &ps));
+    KDA_TRY(plan_pools(pools, n_pools, false, &ps));
     KDA_TRY(check_tables(n_pages, table, rows, per_row, refcount));
     KDA_TRY(check_list(parents, n, "parents"));
     KDA_TRY(check_list(children, n, "children"));
@@ -428,7 +416,7 @@ kda_status_t kda_cache_compact(const kda_cache_pool_t *pools, int32_t n_pools, i
                                void *stream)
 {
     kda::CachePools ps;
-    KDA_TRY(plan_pools(pools, n_pools, n_pages / 4, false, &ps));
+    KDA_TRY(plan_pools(pools, n_pools, false, &ps));
     KDA_TRY(check_tables(n_pages, table, rows, per_row, refcount));
     KDA_TRY(check_list(moved_to, n_pages, "moved_to"));
     KDA_TRY(check_list(moves, n_pages, "moves"));
