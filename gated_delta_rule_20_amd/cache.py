@@ -6,13 +6,15 @@ counts how many page-table entries hold each page (a page is free when it is not
 above 0); ``table`` [rows, per_row] int32 lists each sequence's pages in order, -1
 where there is none.  The last page of a row is the one still being written, those
 before it are read only.
+
+Every call also takes ``stream`` (a torch.cuda.Stream; None: the current one).
 """
 from __future__ import annotations
 
 import torch
 
 from . import CACHE_MAX_POOLS, CachePool, _dev
-from .linear import _call, _check_tensors
+from .linear import _call, _check_tensors, _on_stream
 
 
 def _pools(dst, src=None):
@@ -61,7 +63,8 @@ def _tables(table, refcount, device, n_pages=None):
                          f"got {tuple(refcount.shape)}")
 
 
-def cache_copy(pools, src_pools, dst_pages, src_pages, *, stream=None) -> None:
+@_on_stream
+def cache_copy(pools, src_pools, dst_pages, src_pages) -> None:
     """Copy page src_pages[i] of every source pool to page dst_pages[i] of its pool.
 
     pools / src_pools: a tensor or a list of tensors [n_pages, ...] (src_pools None: within the pools).  Pairs with
@@ -71,10 +74,11 @@ def cache_copy(pools, src_pools, dst_pages, src_pages, *, stream=None) -> None:
     n = _list(dst_pages, "dst_pages", device)
     if _list(src_pages, "src_pages", device) != n:
         raise ValueError("dst_pages and src_pages must have the same length")
-    _call("kda_cache_copy", (arr, n_pools, n_dst, n_src, dst_pages.data_ptr(), src_pages.data_ptr(), n), stream, device)
+    _call("kda_cache_copy", (arr, n_pools, n_dst, n_src, dst_pages.data_ptr(), src_pages.data_ptr(), n), device)
 
 
-def cache_fork(pools, table, refcount, parents, children, *, stream=None):
+@_on_stream
+def cache_fork(pools, table, refcount, parents, children):
     """Make row children[i] of the table a continuation of row parents[i].
 
     The child shares the parent's pages except the last, which is copied to a free page of its own (the i-th fork
@@ -88,20 +92,22 @@ def cache_fork(pools, table, refcount, parents, children, *, stream=None):
         raise ValueError("parents and children must have the same length")
     pages = torch.empty((2, n), dtype=torch.int32, device=device)
     _call("kda_cache_fork", (arr, n_pools, n_pages, table.data_ptr(), table.shape[0], table.shape[1], refcount.data_ptr(),
-                             parents.data_ptr(), children.data_ptr(), n, pages.data_ptr(), pages.data_ptr() + 4 * n), stream, device)
+                             parents.data_ptr(), children.data_ptr(), n, pages.data_ptr(), pages.data_ptr() + 4 * n), device)
     return pages[1]
 
 
-def cache_free(table, refcount, rows, *, stream=None) -> None:
+@_on_stream
+def cache_free(table, refcount, rows) -> None:
     """Give up the pages of the named rows: their counts fall by one (not below 0) and the rows become -1."""
     _dev(table, "table", torch.int32)
     _tables(table, refcount, table.device)
     n = _list(rows, "rows", table.device)
     _call("kda_cache_free", (table.data_ptr(), table.shape[0], table.shape[1], refcount.data_ptr(), refcount.shape[0], rows.data_ptr(),
-                             n), stream, table.device)
+                             n), table.device)
 
 
-def cache_compact(pools, table, refcount, *, stream=None):
+@_on_stream
+def cache_compact(pools, table, refcount):
     """Move the live pages to the front of the pools; table and refcount follow, in place.
 
     Live pages below their number stay, and the i-th live page behind it moves to the i-th free page before it.
@@ -112,5 +118,5 @@ def cache_compact(pools, table, refcount, *, stream=None):
     buf = torch.empty(2 * n_pages + 2, dtype=torch.int32, device=device)
     at = buf.data_ptr()
     _call("kda_cache_compact", (arr, n_pools, n_pages, table.data_ptr(), table.shape[0], table.shape[1], refcount.data_ptr(), at,
-                                at + 4 * n_pages, at + 8 * n_pages), stream, device)
+                                at + 4 * n_pages, at + 8 * n_pages), device)
     return buf[:n_pages], buf[2 * n_pages:2 * n_pages + 1]

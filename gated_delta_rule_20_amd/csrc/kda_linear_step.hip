@@ -36,7 +36,10 @@ __global__ __launch_bounds__(256) void linear_step_kernel(const LinearStepParams
         slot = p.slots[n];
         mine = slot >= 0 && slot < p.n_slots;
         bool seen = false;                // an earlier row of the same slot
-        for (int j = t; j < n; j += 256) seen |= p.slots[j] == slot;
+        for (int j = t; j < n; j += 4 * 256) {             // four reads in flight
+#pragma unroll
+            for (int i = 0; i < 4; ++i) seen |= p.slots[min(j + 256 * i, n - 1)] == slot && j + 256 * i < n;
+        }
         mine = !__syncthreads_or(seen) && mine;
     }
     if (!mine) {                          // an empty place: uniform over the workgroup

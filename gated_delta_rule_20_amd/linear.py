@@ -2,10 +2,14 @@
 
 The recurrence next to KDA's that writes without the delta rule and forgets with
 one scalar per head: S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale * S_t^T q_t.
+
+Every call also takes ``stream`` (a torch.cuda.Stream; None: the current one), on which
+it runs and allocates.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -27,11 +31,27 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(fn, args, stream, device):
-    """The library launches on the current device: make it the tensors' own."""
+def _on_stream(fn):
+    """Adds the keyword ``stream``: the whole call runs on it, what it allocates too, so that memory is not handed to
+    another stream's work while the kernels still use it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        first = args[0] if args else next(iter(kwargs.values()), None)
+        first = first[0] if isinstance(first, (list, tuple)) and first else first
+        if isinstance(first, torch.Tensor) and first.device != stream.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
+
+
+def _call(fn, args, device):
+    """Launches on the tensors' device (the library uses the current one) and its current stream."""
     lib = load_library()
     index = device.index
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    s = torch._C._cuda_getCurrentRawStream(index)
     if index == torch.cuda.current_device():
         status = getattr(lib, fn)(*args, s)
     else:
@@ -105,8 +125,9 @@ def _workspace(fn, a, workspace, device):
     return workspace
 
 
+@_on_stream
 def linear_chunk_fwd(q, k, v, g, *, scale: float = 1.0, cu_seqlens=None, initial_state=None,
-                     output_final_state: bool = True, out=None, final_state=None, workspace=None, stream=None,
+                     output_final_state: bool = True, out=None, final_state=None, workspace=None,
                      checkpoints=None, checkpoint_every: int = 0):
     """Forward over whole sequences (``kda_linear_chunk_fwd``).
 
@@ -134,13 +155,13 @@ def linear_chunk_fwd(q, k, v, g, *, scale: float = 1.0, cu_seqlens=None, initial
                       _at(cu_seqlens), N, _at(initial_state), _at(out), _at(final_state), None, 0,
                       _at(checkpoints), checkpoint_every if slots else 0, slots)
     workspace = _workspace("kda_linear_chunk_fwd_workspace_size", a, workspace, dev)
-    _call("kda_linear_chunk_fwd", (ctypes.byref(a),), stream, dev)
+    _call("kda_linear_chunk_fwd", (ctypes.byref(a),), dev)
     return out, final_state
 
 
+@_on_stream
 def linear_chunk_bwd(q, k, v, g, d_o, *, scale: float = 1.0, cu_seqlens=None, initial_state=None, dfinal_state=None,
-                     need_dg: bool = True, dq=None, dk=None, dv=None, dg=None, dinitial_state=None, workspace=None,
-                     stream=None):
+                     need_dg: bool = True, dq=None, dk=None, dv=None, dg=None, dinitial_state=None, workspace=None):
     """Gradients of :func:`linear_chunk_fwd` (``kda_linear_chunk_bwd``) for the same arguments, given ``d_o`` (shaped
     like o, in its dtype) and ``dfinal_state`` ([N, H, Dk, Dv] fp32, None: zeros).  Returns (dq, dk, dv, dg, dinitial_state):
     the first three shaped and typed like q, k, v; dg fp32 shaped like g (None without ``need_dg``)."""
@@ -161,7 +182,7 @@ def linear_chunk_bwd(q, k, v, g, d_o, *, scale: float = 1.0, cu_seqlens=None, in
                       _at(cu_seqlens), N, _at(initial_state), _at(d_o), _at(dfinal_state), _at(dq), _at(dk),
                       _at(dv), _at(dg), _at(dinitial_state), None, 0)
     workspace = _workspace("kda_linear_chunk_bwd_workspace_size", a, workspace, dev)
-    _call("kda_linear_chunk_bwd", (ctypes.byref(a),), stream, dev)
+    _call("kda_linear_chunk_bwd", (ctypes.byref(a),), dev)
     return dq, dk, dv, dg, dinitial_state
 
 
@@ -196,7 +217,8 @@ def _need(fn, a) -> int:
     return need.value
 
 
-def linear_recurrent_step(q, k, v, g, state, *, scale: float = 1.0, slots=None, new_state=None, out=None, stream=None):
+@_on_stream
+def linear_recurrent_step(q, k, v, g, state, *, scale: float = 1.0, slots=None, new_state=None, out=None):
     """One token for each of N sequences (``kda_linear_recurrent_step``).
 
     q, k: [N, Hk, Dk]; v: [N, H, Dv] (bf16 or fp32; H a multiple of Hk); g: log-decays
@@ -223,5 +245,5 @@ def linear_recurrent_step(q, k, v, g, state, *, scale: float = 1.0, slots=None, 
     out = _like(out, "out", v)
     a = LinearStepArgs(N, H, Hk, Dk, Dv, _DTYPES[q.dtype], q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                        per_head, scale, _at(slots), shape[0], state.data_ptr(), new_state.data_ptr(), out.data_ptr())
-    _call("kda_linear_recurrent_step", (ctypes.byref(a),), stream, dev)
+    _call("kda_linear_recurrent_step", (ctypes.byref(a),), dev)
     return out

@@ -39,7 +39,8 @@
  *     access outside the caller's tensors or the workspace: each sequence is
  *     clamped into tokens [0, T] (a decreasing pair is an empty sequence) and
  *     the chunk count saturates at the workspace's capacity.
- *   - The library is thread-safe; calls that share output buffers race.
+ *   - The library is thread-safe; calls that share output buffers or a workspace
+ *     race (captured graphs that are replayed at once among them).
  */
 #ifndef KDA_H_
 #define KDA_H_
