@@ -107,9 +107,15 @@ kda_status_t check_grid(const kda::CachePools &pools, long long pages)
 
 // Tokens per segment and what the workspace holds.  A sequence is cut only
 // where its (sequence, head) pairs leave compute units idle: about SEGMENTS
-// segments in all keep two workgroups on each of the 256 units, and a segment is at least MIN_SEGMENT
-// tokens, so that the first pass stays cheaper than the walk it shortens.
-constexpr int MIN_SEGMENT = 256, SEGMENTS = 512, ANCHOR = 512;
+// segments in all keep two workgroups on each of the 256 units.  Where even
+// the shortest segments do not fill the chip, a call's time is one workgroup's:
+// about 7 us for every 64 tokens of a segment, over both passes, and 0.8 us for every segment
+// before its own, which is least at sqrt(7.3 * tokens) tokens (T = 1024, H = 4: 256
+// tokens 33 us, 128 tokens 24 us; T = 4096, H = 8, backward: 138 and 152 us).
+// Backwards one workgroup fills a unit, so segments below ANCHOR tokens are made for one
+// workgroup a unit (T = 2048, H = 32: 128 us, with twice the segments 157 us); above, two rounds of shorter
+// segments are better again (T = 8192, H = 32: 512 tokens 460 us, 1024 tokens 499 us).
+constexpr int MIN_SEGMENT = 128, SEGMENTS = 512, ANCHOR = 512;
 
 struct LinearPlan {
     int N, rows, seg, anchor, n_seg, n_part, n_anchors;
@@ -123,7 +129,7 @@ struct LinearShape {
     float scale;
 };
 
-kda_status_t plan_linear(const LinearShape &a, LinearPlan *pl)
+kda_status_t plan_linear(const LinearShape &a, bool backward, LinearPlan *pl)
 {
     const kda_status_t st = check_heads(a.dtype, a.H, a.Hk, a.Dk, a.Dv, a.scale);
     if (st != KDA_SUCCESS) return st;
@@ -139,9 +145,13 @@ kda_status_t plan_linear(const LinearShape &a, LinearPlan *pl)
         return fail(KDA_ERROR_NOT_SUPPORTED, "problem too large for 32-bit token/pair indices");
     pl->rows = (int)rows;
     long long seg = rows * a.H / SEGMENTS;
-    seg = seg < MIN_SEGMENT ? MIN_SEGMENT : (seg + MIN_SEGMENT - 1) / MIN_SEGMENT * MIN_SEGMENT;
+    if (seg > (1 << 28)) seg = 1 << 28;
+    if (backward && seg < ANCHOR) seg = 2 * seg < ANCHOR ? 2 * seg : ANCHOR;
+    // packed: the lengths are on the device; four times their mean stands for the longest
+    const long long longest = a.cu && a.N > 4 ? 4 * rows / a.N : a.cu ? rows : a.T;
+    while (seg < MIN_SEGMENT || seg * seg * 10 < 73 * longest) seg = seg < MIN_SEGMENT ? MIN_SEGMENT : seg + KDA_CHUNK;
+    seg = (seg + KDA_CHUNK - 1) / KDA_CHUNK * KDA_CHUNK;
     if (seg > ANCHOR) seg = (seg + ANCHOR - 1) / ANCHOR * ANCHOR;
-    if (seg > (1 << 30)) seg = 1 << 30;
     pl->seg = (int)seg;
     pl->anchor = seg < ANCHOR ? (int)seg : ANCHOR;
     const auto over = [](int len, int by) { return len <= 0 ? 0 : (len - 1) / by; };  // pieces behind the first
@@ -265,7 +275,7 @@ kda_status_t kda_linear_chunk_fwd_workspace_size(const kda_linear_fwd_args_t *a,
 {
     if (!a || !bytes) return fail(KDA_ERROR_INVALID_VALUE, "args or bytes is NULL");
     LinearPlan pl;
-    KDA_TRY(plan_linear(shape_of(a), &pl));
+    KDA_TRY(plan_linear(shape_of(a), false, &pl));
     kda::LinearChunkParams p;
     *bytes = plan_fwd(a, pl, nullptr, &p);
     return ok();
@@ -275,7 +285,7 @@ kda_status_t kda_linear_chunk_fwd(const kda_linear_fwd_args_t *a, void *stream)
 {
     if (!a) return fail(KDA_ERROR_INVALID_VALUE, "args is NULL");
     LinearPlan pl;
-    KDA_TRY(plan_linear(shape_of(a), &pl));
+    KDA_TRY(plan_linear(shape_of(a), false, &pl));
     if (pl.rows > 0) {
         KDA_TRY(check_decay(a->g));
         const Ptr req[] = {{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->o, "o"}};
@@ -301,7 +311,7 @@ kda_status_t kda_linear_chunk_bwd_workspace_size(const kda_linear_bwd_args_t *a,
 {
     if (!a || !bytes) return fail(KDA_ERROR_INVALID_VALUE, "args or bytes is NULL");
     LinearPlan pl;
-    KDA_TRY(plan_linear(shape_of(a), &pl));
+    KDA_TRY(plan_linear(shape_of(a), true, &pl));
     kda::LinearBwdParams b;
     *bytes = plan_bwd(a, pl, nullptr, &b);
     return ok();
@@ -311,7 +321,7 @@ kda_status_t kda_linear_chunk_bwd(const kda_linear_bwd_args_t *a, void *stream)
 {
     if (!a) return fail(KDA_ERROR_INVALID_VALUE, "args is NULL");
     LinearPlan pl;
-    KDA_TRY(plan_linear(shape_of(a), &pl));
+    KDA_TRY(plan_linear(shape_of(a), true, &pl));
     if (pl.rows > 0) {
         KDA_TRY(check_decay(a->g));
         const Ptr req[] = {{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->d_o, "d_o"}, {a->dq, "dq"}, {a->dk, "dk"}, {a->dv, "dv"}};

@@ -567,7 +567,7 @@ struct Piece {
 // one), sequence by sequence; false when there are fewer.  A sequence of n
 // segments has n - 1 parts in the workspace (nothing is left by its last one, or
 // first one backwards).  Every wave finds the segment by itself: 64
-// sequences at a time, a prefix sum over the lanes.  L and LA are at least 256, so the sums fit 32 bits unsigned.
+// sequences at a time, a prefix sum over the lanes.  L and LA are at least 128, so the sums fit 32 bits unsigned.
 __device__ __forceinline__ int pieces_of(int len, int L) { return len <= 0 ? 1 : (len - 1) / L + 1; }
 
 __device__ __forceinline__ bool find_piece(const LinearChunkParams &p, int id, Piece &w)

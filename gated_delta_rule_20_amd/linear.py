@@ -63,6 +63,9 @@ def _call(fn, args, device):
 
 def _heads(q, k, v, g):
     """Checks q, k [..., Hk, Dk], v [..., H, Dv] and g [..., H] or [H]; returns (H, Hk, Dk, Dv, g_per_head)."""
+    for name, t in (("q", q), ("k", k), ("v", v), ("g", g)):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a device tensor")
     dtype = q.dtype
     if dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {dtype}")
@@ -230,6 +233,8 @@ def linear_recurrent_step(q, k, v, g, state, *, scale: float = 1.0, slots=None, 
     H, Hk, Dk, Dv, per_head = _heads(q, k, v, g)
     if q.dim() != 3:
         raise ValueError(f"q must be [N, Hk, Dk], got {tuple(q.shape)}")
+    if not isinstance(state, torch.Tensor):
+        raise ValueError("state must be a device tensor")
     N, dev, shape = q.shape[0], q.device, state.shape
     _check_tensors(dev, torch.float32, state=state, new_state=new_state)
     if len(shape) != 4 or shape[1] != H or shape[2] != Dk or shape[3] != Dv:

@@ -308,6 +308,7 @@ KDA_API kda_status_t kda_recurrent_replay(const kda_replay_args_t *args, void *s
  *   - Hk query / key heads serve H value heads (H a multiple of Hk): value head
  *     h reads query / key head h / (H / Hk).  Hk = H is the plain layout.
  *   - q and k need no norm bound.
+ *   - Outputs must not overlap inputs or one another, but where it is said.
  * Sums, states and decays are held in float32 or more; float32 results
  * (states, their gradients, dg) are accurate to float32 also for bf16 inputs.
  * A NaN or infinity among a sequence's tokens can reach the outputs of the

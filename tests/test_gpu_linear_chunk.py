@@ -296,3 +296,56 @@ def test_streams_at_once():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_binding_refusals():
+    """Shapes, types, layouts and devices that the binding turns away before the library is called."""
+    import gated_delta_rule_20_amd as kda
+    d, _ = _inputs([64], 4, 2, 64, 64, torch.bfloat16, True, seed=15)
+    q, k, v, g = (d[x][None] if x != "g" else d[x] for x in ("q", "k", "v", "g"))
+    ok = dict(initial_state=d["h0"])
+    kda.linear_chunk_fwd(q, k, v, g, **ok)
+    wide = torch.zeros((1, 64, 2, 128), dtype=torch.bfloat16, device="cuda")
+    bad = [((q.float(), k, v, g), {}, "k must be"), ((q, k[:, :9], v, g), {}, "q's shape"), ((q, k, v[:, :9], g), {}, "leading axes"),
+           ((q, k, v[:, :, :3].contiguous(), g[:3]), {}, "multiple"), ((q, k, v, g[:3]), {}, "g must be"), ((q, k, v, g.cpu()), {}, "device"),
+           ((q, k, v, g.bfloat16()), {}, "g must be"), ((wide[..., :64], k, v, g), {}, "contiguous"),
+           ((q, k, v, g), dict(initial_state=d["h0"][:, :2]), "contiguous|initial_state"),
+           ((q, k, v, g), dict(cu_seqlens=d["cu"].long()), "cu_seqlens"), ((q, k, v, g), dict(cu_seqlens=d["cu"][:1]), "cu_seqlens"),
+           ((q, k, v, g), dict(out=v.float()), "out"), ((q, k, v, g), dict(out=v[:, :9].contiguous()), "out"),
+           ((q, k, v, g), dict(checkpoints=torch.zeros((1, 1, 4, 64, 64), device="cuda")), "checkpoints"),
+           ((q[0], k[0], v[0], g), {}, "q must be")]
+    for args, kw, msg in bad:
+        with pytest.raises(ValueError, match=msg):
+            kda.linear_chunk_fwd(*args, **kw)
+    with pytest.raises(kda.KDAError, match="head dims"):
+        x = torch.zeros((1, 8, 2, 32), dtype=torch.bfloat16, device="cuda")
+        kda.linear_chunk_fwd(x, x, x, g[:2])
+    with pytest.raises(kda.KDAError, match="workspace"):
+        long = torch.zeros((1, 4096, 1, 64), device="cuda")
+        kda.linear_chunk_fwd(long, long, long, g[:1].contiguous(), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="d_o"):
+        kda.linear_chunk_bwd(q, k, v, g, d["do"][None][:, :9])
+    with pytest.raises(ValueError, match="dfinal_state"):
+        kda.linear_chunk_bwd(q, k, v, g, d["do"][None], dfinal_state=d["h0"][0])
+
+
+def test_long_packed_call_beyond_4_gib():
+    """Rows whose byte offset passes 2^32 in q, k, v and o: the last sequence of a long batch equals a call of its own."""
+    import gated_delta_rule_20_amd as kda
+    H, D, T = 64, 128, 270000                          # 64 * 128 * 2 bytes a row: 4.4 GB
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    x = torch.randn((T, H, D), generator=gen, device="cuda", dtype=torch.bfloat16)
+    y = torch.randn((T, H, D), generator=gen, device="cuda", dtype=torch.bfloat16)
+    g = -torch.rand(H, generator=gen, device="cuda") * 0.5
+    cu = torch.tensor([0, T - 200, T], dtype=torch.int32, device="cuda")
+    o, hT = kda.linear_chunk_fwd(x, y, x, g, scale=0.1, cu_seqlens=cu)
+    tail = [t[-200:][None].contiguous() for t in (x, y, x)]
+    o1, h1 = kda.linear_chunk_fwd(*tail, g, scale=0.1)
+    # the calls cut the 200 tokens into segments differently, so states agree to float32 and outputs to a rounding
+    assert ref.rel2(ref.f64(hT[1]), ref.f64(h1[0])) <= 1e-5
+    assert ref.rel2(ref.f64(o[-200:]), ref.f64(o1[0])) <= TOL2[torch.bfloat16]
+    del o, hT
+    got = kda.linear_chunk_bwd(x, y, x, g, y, scale=0.1, cu_seqlens=cu, need_dg=False)
+    one = kda.linear_chunk_bwd(*tail, g, tail[1], scale=0.1, need_dg=False)
+    for a, b in zip(got[:3], one[:3]):
+        assert ref.rel2(ref.f64(a[-200:]), ref.f64(b[0])) <= TOL2[torch.bfloat16]

@@ -145,6 +145,10 @@ def test_binding_requires_device_tensors(lib):
     i = torch.zeros(3, dtype=torch.int32)
     with pytest.raises(ValueError, match="device tensor"):
         kda.linear_recurrent_step(x, x, x, torch.zeros(2), s)
+    with pytest.raises(ValueError, match="g must be"):
+        kda.linear_recurrent_step(x, x, x, None, s)
+    with pytest.raises(ValueError, match="k must be"):
+        kda.linear_chunk_fwd(x, None, x, torch.zeros(2))
     with pytest.raises(ValueError, match="unsupported dtype"):
         kda.linear_recurrent_step(x.half(), x.half(), x.half(), torch.zeros(2), s)
     with pytest.raises(ValueError, match="device tensor"):
@@ -243,7 +247,7 @@ def test_workspace_sizes(lib):
         assert getattr(lib, fn)(ctypes.byref(a), ctypes.byref(n)) == 0, _message(lib)
         return n.value
     fwd, bwd = "kda_linear_chunk_fwd_workspace_size", "kda_linear_chunk_bwd_workspace_size"
-    assert size(fwd, _fwd_args(T=200)) == 0
+    assert size(fwd, _fwd_args(T=128)) == 0
     one = 4 * 4 * 128 * 64                              # a state of every head
     assert size(fwd, _fwd_args(T=1000)) >= one
     packed = _fwd_args(T=1 << 20, cu_seqlens=0x20000, N=1 << 16)
@@ -251,3 +255,14 @@ def test_workspace_sizes(lib):
     assert size(bwd, _bwd_args(T=64, Hk=4, dg=None)) == 0
     assert size(bwd, _bwd_args(T=64, dg=None)) == 2 * 64 * 4 * 128 * 4    # shared heads: dq, dk per value head
     assert size(bwd, _bwd_args(T=64, Hk=4)) == 1024                       # y [64, 4]
+
+
+def test_plans_of_the_largest_calls(lib):
+    """Token and head counts at the limits plan without overflow."""
+    n = ctypes.c_size_t(0)
+    for over in (dict(T=2 ** 31 - 1, H=1 << 15, Hk=1), dict(T=2 ** 31 - 1, H=1, Hk=1), dict(T=1, H=1 << 15, Hk=1 << 15),
+                 dict(T=2 ** 31 - 1, cu_seqlens=0x20000, N=(1 << 13) - 1, H=1 << 15, Hk=1), dict(B=1 << 12, T=1 << 18, H=1 << 12, Hk=1)):
+        for fn, a in (("kda_linear_chunk_fwd_workspace_size", _fwd_args(**over)),
+                      ("kda_linear_chunk_bwd_workspace_size", _bwd_args(dg=None, Hk=over["H"], **{k: v for k, v in over.items() if k != "Hk"}))):
+            assert getattr(lib, fn)(ctypes.byref(a), ctypes.byref(n)) == 0, _message(lib)
+            assert n.value < 1 << 50
