@@ -82,8 +82,17 @@ __global__ __launch_bounds__(256) void cache_copy_kernel(const CachePools pools,
     if (to < 0 || to >= n_dst || from < 0 || from >= n_src) return;
     copy_slice(pools, slice, from, to, [&]() {
         bool again = false;                   // a later pair has this destination
-        for (int j = i + 1 + (int)threadIdx.x; j < n; j += 256)
-            again |= dst_pages[j] == to && src_pages[j] >= 0 && src_pages[j] < n_src;
+        for (long j = i + 1 + (long)threadIdx.x; j < n; j += 8 * 256) {   // eight reads in flight
+            int d[8];
+#pragma unroll
+            for (int m = 0; m < 8; ++m) d[m] = dst_pages[min(j + 256 * m, (long)n - 1)];
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+                if (d[m] == to && j + 256 * m < n) {
+                    const int s = src_pages[j + 256 * m];
+                    again |= s >= 0 && s < n_src;
+                }
+        }
         return !__syncthreads_or(again);
     });
 }

@@ -32,6 +32,9 @@ struct LinearChunkParams {
     int N, T, rows;                   // sequences; tokens per sequence (all rows when cu); rows
     int H, group;                     // value heads; value heads per query / key head
     int seg, n_seg;                   // tokens per segment, segments at most
+    // many packed sequences: the sequence of each segment (-1: none) [n_seg], each sequence's first segment and the
+    // anchor intervals before it [N]; null: searched
+    int32_t *seq_of, *first_seg, *first_anchor;
     const float *h0;                  // [N, H, Dk, Dv] or null
     float *hT;                        // [N, H, Dk, Dv] or null
     void *o;
@@ -61,6 +64,11 @@ struct LinearBwdParams {
     double *dg_part;                  // [n_seg, H] when g_per_head
     float *part_fwd, *dec_fwd;        // the forward states' first pass (c.part, c.dec: the gradients')
 };
+
+// Above this many packed sequences a kernel tabulates their segments first (about 5 us
+// with its launch); up to it every wave searches 64 of them at a time.  300
+// sequences of 64 tokens, H = 8: searched 86 us, tabulated 77 us; 20000 of 16: 54 and 3.4 ms.
+constexpr int TABLE_SEQUENCES = 128;
 
 hipError_t launch_linear_fwd(int bf16, int Dk, int Dv, const LinearChunkParams &p, hipStream_t stream);
 hipError_t launch_linear_bwd(int bf16, int Dk, int Dv, const LinearBwdParams &p, hipStream_t stream);

@@ -207,6 +207,14 @@ template <typename A> kda::LinearChunkParams chunk_params(const A *a, const Line
     return p;
 }
 
+void take_tables(Carver &c, const LinearPlan &pl, kda::LinearChunkParams *p)
+{
+    if (!p->cu || pl.N <= kda::TABLE_SEQUENCES) return;
+    p->seq_of = (int32_t *)c.take(sizeof(int32_t) * (size_t)pl.n_seg);
+    p->first_seg = (int32_t *)c.take(sizeof(int32_t) * (size_t)pl.N);
+    p->first_anchor = (int32_t *)c.take(sizeof(int32_t) * (size_t)pl.N);
+}
+
 // The first pass's buffers.
 void take_parts(Carver &c, const LinearPlan &pl, int H, size_t state, float **part, float **dec)
 {
@@ -223,6 +231,7 @@ size_t plan_fwd(const kda_linear_fwd_args_t *a, const LinearPlan &pl, void *ws, 
     p->ckpt = a->checkpoints;
     p->ckpt_every = a->checkpoint_every;
     p->ckpt_slots = a->checkpoint_slots;
+    take_tables(c, pl, p);
     const size_t state = sizeof(float) * a->H * a->Dk * a->Dv;
     if (pl.first_pass) {
         take_parts(c, pl, a->H, state, &p->part, &p->dec);
@@ -238,6 +247,7 @@ size_t plan_bwd(const kda_linear_bwd_args_t *a, const LinearPlan &pl, void *ws, 
     b->c = chunk_params(a, pl);
     b->d_o = a->d_o; b->dhT = a->d_final_state; b->dh0 = a->d_initial_state;
     b->dq = a->dq; b->dk = a->dk; b->dv = a->dv; b->dg = a->dg;
+    take_tables(c, pl, &b->c);
     const size_t state = sizeof(float) * a->H * a->Dk * a->Dv;
     if (pl.first_pass) {
         take_parts(c, pl, a->H, state, &b->c.part, &b->c.dec);

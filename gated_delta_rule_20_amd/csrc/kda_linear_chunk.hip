@@ -583,6 +583,19 @@ __device__ __forceinline__ bool find_piece(const LinearChunkParams &p, int id, P
         w.anchor = w.seq * (pieces_of(p.T, LA) - 1);
         return w.seq < p.N;
     }
+    if (p.seq_of) {
+        const int s = p.seq_of[id];
+        if (s < 0) return false;
+        const int a = min(max(p.cu[s], 0), p.T);
+        w.seq = s;
+        w.begin = a;
+        w.len = min(max(p.cu[s + 1], a), p.T) - a;
+        w.parts = pieces_of(w.len, L);
+        w.part = id - p.first_seg[s];
+        w.slot = p.first_seg[s] - s;
+        w.anchor = p.first_anchor[s] - s;
+        return true;
+    }
     const int lane = lane_id();
     unsigned before = 0, abefore = 0;
     for (int s0 = 0; s0 < p.N; s0 += 64) {
@@ -616,6 +629,52 @@ __device__ __forceinline__ bool find_piece(const LinearChunkParams &p, int id, P
         abefore += __builtin_amdgcn_readlane(y, 63);
     }
     return false;
+}
+
+// One workgroup: the tables of find_piece for many sequences.  Sums in 64 bits, so
+// that offsets that break the rules cannot wrap; what lies beyond n_seg is cut off.
+__global__ __launch_bounds__(1024) void linear_table_kernel(const LinearChunkParams p)
+{
+    __shared__ unsigned long long s_seg[16], s_anchor[16];
+    const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+    unsigned long long segs = 0, anchors = 0;
+    for (int s0 = 0; s0 < p.N; s0 += 1024) {
+        const int s = s0 + t;
+        int n = 0, na = 0;
+        if (s < p.N) {
+            const int a = min(max(p.cu[s], 0), p.T), b = min(max(p.cu[s + 1], a), p.T);
+            n = pieces_of(b - a, p.seg);
+            na = pieces_of(b - a, p.anchor_tokens);
+        }
+        unsigned long long x = n, y = na;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const unsigned long long u = __shfl_up(x, d), v = __shfl_up(y, d);
+            if (lane >= d) { x += u; y += v; }
+        }
+        if (lane == 63) { s_seg[wv] = x; s_anchor[wv] = y; }
+        __syncthreads();
+        unsigned long long first = segs + x - n, afirst = anchors + y - na;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i < wv) { first += s_seg[i]; afirst += s_anchor[i]; }
+            segs += s_seg[i];
+            anchors += s_anchor[i];
+        }
+        __syncthreads();
+        if (s < p.N) {
+            p.first_seg[s] = (int)min(first, 0x7fffffffull);
+            p.first_anchor[s] = (int)min(afirst, 0x7fffffffull);
+            for (int i = 0; i < n && first + i < (unsigned long long)p.n_seg; ++i) p.seq_of[first + i] = s;
+        }
+    }
+    for (unsigned long long i = segs + t; i < (unsigned long long)p.n_seg; i += 1024) p.seq_of[i] = -1;
+}
+static hipError_t launch_table(const LinearChunkParams &p, hipStream_t stream)
+{
+    if (!p.seq_of) return hipSuccess;
+    hipLaunchKernelGGL(linear_table_kernel, dim3(1), dim3(1024), 0, stream, p);
+    return hipGetLastError();
 }
 
 // Where the state at token `pos` of the sequence is kept for dg, or -1.  Offsets
@@ -1087,13 +1146,15 @@ __global__ __launch_bounds__(256) void linear_share_kernel(const LinearChunkPara
 template <typename T, int DK, int DV> static hipError_t fwd_t(const LinearChunkParams &p, hipStream_t stream)
 {
     const dim3 grid((unsigned)((size_t)p.n_seg * p.H)), block(64 * NW);
+    hipError_t e = launch_table(p, stream);
+    if (e != hipSuccess) return e;
     if (p.part) {
         hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE>), grid, block, 0, stream, p);
-        const hipError_t e = hipGetLastError();
+        e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_OUT>), grid, block, 0, stream, p);
-    const hipError_t e = hipGetLastError();
+    e = hipGetLastError();
     if (e != hipSuccess || !p.defer) return e;
     hipLaunchKernelGGL(linear_deferred_kernel, grid, block, 0, stream, p, p.hT, 0, DK * DV);
     return hipGetLastError();
@@ -1103,7 +1164,8 @@ template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdPar
 {
     const LinearChunkParams &c = b.c;
     const dim3 grid((unsigned)((size_t)c.n_seg * c.H)), block(64 * NW);
-    hipError_t e;
+    hipError_t e = launch_table(c, stream);
+    if (e != hipSuccess) return e;
     LinearChunkParams dq = c;
     if (c.part) {
         LinearChunkParams s = c;

@@ -40,7 +40,7 @@ def _i32(x):
     return torch.tensor(x, dtype=torch.int32).cuda()
 
 
-@pytest.mark.parametrize("n", [0, 1, 7, 300])
+@pytest.mark.parametrize("n", [0, 1, 7, 300, 5000])
 def test_copy_between_pools(n):
     import gated_delta_rule_20_amd as kda
     src, dst = _pools(40, SHAPES, 1), _pools(53, SHAPES, 2)

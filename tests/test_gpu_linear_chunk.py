@@ -142,6 +142,18 @@ def test_decay_range(decay, dtype):
     _backward_check(d, cu, _bwd(d, 1.0), 1.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_sequences(dtype):
+    """More packed sequences than are searched (128): empty and one-token ones and one long enough to be cut."""
+    r = np.random.RandomState(0)
+    lens = r.randint(0, 5, 1300).tolist()
+    lens[700], lens[1299] = 500, 130
+    d, cu = _inputs(lens, 2, 1, 64, 64, dtype, False, seed=17, head=3, tail=5)
+    o, hT = _fwd(d, 1.0)
+    _forward_check(d, cu, o, hT, 1.0)
+    _backward_check(d, cu, _bwd(d, 1.0), 1.0)
+
+
 def test_rows_outside_the_sequences_stay():
     d, cu = _inputs([70, 0, 300], 2, 1, 64, 64, torch.bfloat16, False, seed=4, head=9, tail=77)
     for x in ("q", "k", "v", "do", "g"):        # what is there must not reach the sequences either
@@ -252,6 +264,13 @@ def test_broken_offsets_stay_inside():
         dv = torch.full((900 + 64, 2, 64), 7.0, device="cuda")
         kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["do"], cu_seqlens=cu, initial_state=h, dfinal_state=h, dv=dv[:900])
         assert bool((dv[900:] == 7.0).all())
+    # the same with more sequences than are searched
+    cu = torch.from_numpy(np.random.RandomState(3).randint(-100, 1100, 401).astype(np.int32)).cuda()
+    h = torch.zeros((400, 2, 64, 64), device="cuda")
+    buf, dv = torch.full((900 + 64, 2, 64), 7.0, device="cuda"), torch.full((900 + 64, 2, 64), 7.0, device="cuda")
+    kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], cu_seqlens=cu, initial_state=h, out=buf[:900])
+    kda.linear_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["do"], cu_seqlens=cu, initial_state=h, dfinal_state=h, dv=dv[:900])
+    assert bool((buf[900:] == 7.0).all()) and bool((dv[900:] == 7.0).all())
 
 
 def test_non_finite_stays_in_its_sequence_and_chunk():
