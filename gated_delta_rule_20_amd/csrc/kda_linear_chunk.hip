@@ -706,7 +706,7 @@ __device__ __forceinline__ float fetch_decay(const LinearChunkParams &p, int row
     return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (int)at, 0, 0));
 }
 
-enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ, WALK_STATE_DQ };
+enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ, WALK_STATE_DQ, WALK_DQ_DG };
 
 // One workgroup walks one segment for one value head (head fastest, so that
 // workgroups that run together read neighbouring rows).
@@ -714,7 +714,8 @@ enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ, WALK_STATE_DQ };
 //   WALK_STATE_REV  -, q, do, backwards; writes its part in both orders that linear_dkdv_kernel reads
 //   WALK_STATE_DQ   -, v, k: as WALK_STATE, transposed (DK = the problem's Dv, DV = its Dk)
 //   WALK_OUT        q, k, v;  writes o, final state, checkpoints
-//   WALK_DQ         do, v, k (DK = the problem's Dv, DV = its Dk);  writes dq, y, anchors
+//   WALK_DQ         do, v, k (DK = the problem's Dv, DV = its Dk);  writes dq
+//   WALK_DQ_DG      the same with y and anchors for dg
 // 66 KiB of LDS and up to 256 registers a lane: two workgroups share a compute
 // unit, and one computes while the other waits for memory.  Eight waves of half the
 // columns each hide more latency but read Q and K from LDS twice as often (133 K packed
@@ -726,7 +727,8 @@ template <typename T, int DK, int DV, int MODE>
 __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChunkParams p)
 {
     constexpr int THREADS = 64 * NW;
-    constexpr bool REV = MODE == WALK_STATE_REV, OUT = MODE == WALK_OUT || MODE == WALK_DQ, TR = MODE == WALK_DQ;
+    constexpr bool DG = MODE == WALK_DQ_DG, DQ = MODE == WALK_DQ || DG;
+    constexpr bool REV = MODE == WALK_STATE_REV, OUT = MODE == WALK_OUT || DQ, TR = DQ;
     using G = Group<T, DK, DV, REV>;
     constexpr int C = G::C;
     __shared__ __align__(16) T sQ[OUT ? C * G::LDK : 8];
@@ -734,7 +736,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChu
     __shared__ __align__(16) T sV[C * G::LDV];
     __shared__ __align__(16) T sP[OUT ? C * G::LDP : 8];
     __shared__ __align__(16) Decay<C> sD[2];
-    __shared__ float sY[MODE == WALK_DQ ? 4 : 1][C];
+    __shared__ float sY[DG ? 4 : 1][C];
 
     const int h = (int)(blockIdx.x % (unsigned)p.H), id = (int)(blockIdx.x / (unsigned)p.H);
     Piece w;
@@ -749,7 +751,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChu
     const int row0 = w.begin + first;
     const int hk = h / p.group, Hk = p.H / p.group;
     // strides and heads of the three roles
-    constexpr bool QK_SHARED = MODE != WALK_DQ && MODE != WALK_STATE_DQ;                // role q / k carry the query / key heads
+    constexpr bool QK_SHARED = !DQ && MODE != WALK_STATE_DQ;    // role q / k carry the query / key heads
     const size_t sq = (size_t)(QK_SHARED ? Hk : p.H) * DK;
     const size_t sv = (size_t)(QK_SHARED ? p.H : Hk) * DV;
     const T *gq = (const T *)p.q + (size_t)(QK_SHARED ? hk : h) * DK;
@@ -807,17 +809,16 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChu
         rv.store(sV, t);
         lds_barrier();
         // q's rows for y, before the next tiles: what is loaded later is waited for later
-        quad_t<T> yq[MODE == WALK_DQ ? G::NT : 1][G::NCT];
-        if constexpr (MODE == WALK_DQ)
-            if (p.y) {
-                const T *q0 = (const T *)p.q_rows + ((size_t)row * Hk + hk) * DV;
-                const unsigned sb = (unsigned)(Hk * DV * sizeof(T));
-                const __amdgpu_buffer_rsrc_t rs = rows_window(q0, n, sb, DV * sizeof(T));
-                const unsigned at = (unsigned)(t & 15) * sb + G::first_col(wv) * (unsigned)sizeof(T);
+        quad_t<T> yq[DG ? G::NT : 1][G::NCT];
+        if constexpr (DG) {
+            const T *q0 = (const T *)p.q_rows + ((size_t)row * Hk + hk) * DV;
+            const unsigned sb = (unsigned)(Hk * DV * sizeof(T));
+            const __amdgpu_buffer_rsrc_t rs = rows_window(q0, n, sb, DV * sizeof(T));
+            const unsigned at = (unsigned)(t & 15) * sb + G::first_col(wv) * (unsigned)sizeof(T);
 #pragma unroll
-                for (int it = 0; it < G::NT; ++it) load_cols(q0, rs, (int)(at + 16u * it * sb), yq[it]);
-            }
-        if (MODE != WALK_DQ && i + 1 < nc) fetch(REV ? c - 1 : c + 1);
+            for (int it = 0; it < G::NT; ++it) load_cols(q0, rs, (int)(at + 16u * it * sb), yq[it]);
+        }
+        if (!DG && i + 1 < nc) fetch(REV ? c - 1 : c + 1);
         auto next_decay = [&]() {
             if (wv != NW - 1 || i + 1 >= nc) return;
             const float x = rg;
@@ -827,13 +828,9 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChu
         if constexpr (OUT) {
             f32x4 O[G::NT][G::NCT];
             G::make_scores(sP, sQ, sK, d, p.scale, wv);
-            if constexpr (MODE == WALK_DQ) {
-                if (p.y) {
-                    grp.template inter<split_of<T>>(O, sQ, d);
-                    G::row_dots(sY[wv], [&](int it, int ct) { return yq[it][ct]; }, O);
-                } else {
-                    grp.template inter<1>(O, sQ, d);
-                }
+            if constexpr (DG) {
+                grp.template inter<split_of<T>>(O, sQ, d);
+                G::row_dots(sY[wv], [&](int it, int ct) { return yq[it][ct]; }, O);
                 if (i + 1 < nc) fetch(c + 1);                  // here, where q's rows have left their registers
             } else {
                 grp.template inter<1>(O, sQ, d);
@@ -841,13 +838,13 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChu
             next_decay();
             lds_barrier();                                     // P (and y) are whole
             G::intra(O, sP, sV, wv);
-            if (MODE == WALK_DQ && p.wide)
+            if (DQ && p.wide)
                 G::store((float *)p.o + ((size_t)row * p.H + h) * DV, (size_t)p.H * DV, n, O, wv);
-            else if (MODE == WALK_DQ)
+            else if (DQ)
                 G::store((T *)p.o + ((size_t)row * Hk + hk) * DV, (size_t)Hk * DV, n, O, wv);
             else
                 G::store((T *)p.o + ((size_t)row * p.H + h) * DV, (size_t)p.H * DV, n, O, wv);
-            if (MODE == WALK_DQ && p.y && t < n)
+            if (DG && t < n)
                 p.y[(size_t)(row + t) * p.H + h] = (sY[0][t] + sY[1 % 4][t]) + (sY[2 % 4][t] + sY[3 % 4][t]);
         } else {
             next_decay();
@@ -860,7 +857,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChu
             if (pos % every == 0 && pos / every <= p.ckpt_slots)
                 grp.template put<TR>(p.ckpt + (((size_t)w.seq * p.ckpt_slots + pos / every - 1) * p.H + h) * part_size, wv);
         }
-        if (MODE == WALK_DQ && p.anchors) {
+        if (DG) {
             const long a = anchor_at(p, w, pos);
             if (a >= 0) grp.template put<TR>(p.anchors + ((size_t)a * p.H + h) * part_size, wv);
         }
@@ -891,14 +888,14 @@ __global__ __launch_bounds__(256) void linear_deferred_kernel(const LinearChunkP
 
 // dV (waves 0-3) and dK (waves 4-7) of one segment for one value head, chunks
 // backwards, from one staging of q, k, v and dO; and dg.  With the terms
-//   y_t = q_t . (state part of dq_t)            (from WALK_DQ)
+//   y_t = q_t . (state part of dq_t)            (from WALK_DQ_DG)
 //   z_s = k_s . (state part of dk_s)
 //   x_ts = scale D_ts (q_t . k_s)(dO_t . v_s),  t > s
 //   w = e^{G_end} <S, dS>                       (S enters, dS leaves the chunk)
 //   dg_u = sum_{t >= u} y_t + sum_{s < u} z_s + sum_{s < u <= t} x_ts + w
 // none of which cancel.  w follows from R = <state, its gradient> at the chunk's end:
 // w = R - sum z, and R at the chunk's start is w + sum y, both in float64; R is formed anew
-// from the state that WALK_DQ left at every anchor, and w is 0 where e^{G_end} < 2^-24 (then w is below the rounding
+// from the state that WALK_DQ_DG left at every anchor, and w is 0 where e^{G_end} < 2^-24 (then w is below the rounding
 // of R), so the roundings of y and z do not pile up.
 // One workgroup fills a compute unit (96 KiB of LDS, 8 waves of up to 256 registers); it is bound by
 // latency: the matrix cores are busy 23% of the time, the waves wait for LDS, barriers and one another.
@@ -1180,7 +1177,10 @@ template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdPar
         dq.part = b.part_fwd; dq.dec = b.dec_fwd;
     }
     dq.q = b.d_o; dq.k = c.v; dq.v = c.k; dq.q_rows = c.q; dq.o = b.dq;
-    hipLaunchKernelGGL((linear_walk_kernel<T, DV, DK, WALK_DQ>), grid, block, 0, stream, dq);
+    if (b.dg)
+        hipLaunchKernelGGL((linear_walk_kernel<T, DV, DK, WALK_DQ_DG>), grid, block, 0, stream, dq);
+    else
+        hipLaunchKernelGGL((linear_walk_kernel<T, DV, DK, WALK_DQ>), grid, block, 0, stream, dq);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     constexpr size_t lds = sizeof(DkdvLds<T, DK, DV>);
     static_assert(lds <= 160 * 1024, "one compute unit's LDS");
