@@ -41,6 +41,7 @@ struct LinearChunkParams {
     float *part, *dec;                // [n_part, H, Dk * Dv] and [n_part, H] of the first pass, or null: no pass
     float *part_tr;                   // backward: part once more, as [Dk][Dv]
     int n_part;
+    int summed;                       // backward: the parts have been summed over each sequence
     int defer;                        // entering and resulting states share memory, and there is a first pass
     float *ckpt;                      // [N, ckpt_slots, H, Dk, Dv] or null
     int ckpt_every, ckpt_slots;
@@ -63,6 +64,7 @@ struct LinearBwdParams {
     float *dg;                        // or null
     double *dg_part;                  // [n_seg, H] when g_per_head
     float *part_fwd, *dec_fwd;        // the forward states' first pass (c.part, c.dec: the gradients')
+    float *sum_fwd, *sum_rev;         // products of the decays that belong to the summed parts [n_part, H]
 };
 
 // Above this many packed sequences a kernel tabulates their segments first (about 5 us

@@ -119,7 +119,7 @@ constexpr int MIN_SEGMENT = 128, SEGMENTS = 512, ANCHOR = 512;
 
 struct LinearPlan {
     int N, rows, seg, anchor, n_seg, n_part, n_anchors;
-    bool first_pass;
+    bool first_pass, sum_parts;
 };
 
 struct LinearShape {
@@ -161,6 +161,8 @@ kda_status_t plan_linear(const LinearShape &a, bool backward, LinearPlan *pl)
     pl->n_part = (int)(a.cu ? rows / seg : (long long)a.B * over(a.T, pl->seg));
     pl->n_anchors = (int)(a.cu ? rows / pl->anchor : (long long)a.B * over(a.T, pl->anchor));
     pl->first_pass = over(a.T, pl->seg) > 0;     // packed: some sequence may be that long
+    // where summing them once pays: figures at linear_scan_kernel
+    pl->sum_parts = backward && pl->first_pass && longest > 6 * seg && (long long)pl->N * a.H <= 16;
     return KDA_SUCCESS;
 }
 
@@ -254,6 +256,11 @@ size_t plan_bwd(const kda_linear_bwd_args_t *a, const LinearPlan &pl, void *ws, 
         b->c.defer = overlap(a->d_final_state, a->d_initial_state, state * pl.N);
         take_parts(c, pl, a->H, state, &b->part_fwd, &b->dec_fwd);
         b->c.part_tr = (float *)c.take(state * pl.n_part);
+        if (pl.sum_parts) {
+            b->c.summed = 1;
+            b->sum_fwd = (float *)c.take(sizeof(float) * (size_t)a->H * pl.n_part);
+            b->sum_rev = (float *)c.take(sizeof(float) * (size_t)a->H * pl.n_part);
+        }
     }
     if (a->dg) {
         b->c.y = (float *)c.take(sizeof(float) * (size_t)a->H * pl.rows);

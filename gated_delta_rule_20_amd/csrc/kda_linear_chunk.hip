@@ -631,6 +631,24 @@ __device__ __forceinline__ bool find_piece(const LinearChunkParams &p, int id, P
     return false;
 }
 
+// The parts of sequence s, of a few: the index of the first and their number.
+__device__ __forceinline__ void parts_of(const LinearChunkParams &p, int s, int &slot, int &n)
+{
+    if (!p.cu) {
+        n = pieces_of(p.T, p.seg) - 1;
+        slot = s * n;
+        return;
+    }
+    const auto parts = [&](int i) {
+        const int a = min(max(p.cu[i], 0), p.T), b = min(max(p.cu[i + 1], a), p.T);
+        return pieces_of(b - a, p.seg) - 1;
+    };
+    n = parts(s);
+    long before = 0;
+    for (int i = 0; i < s; ++i) before += parts(i);
+    slot = (int)min(before, 0x7fffffffL);
+}
+
 // One workgroup: the tables of find_piece for many sequences.  Sums in 64 bits, so
 // that offsets that break the rules cannot wrap; what lies beyond n_seg is cut off.
 __global__ __launch_bounds__(1024) void linear_table_kernel(const LinearChunkParams p)
@@ -763,7 +781,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChu
     const size_t pair = (size_t)w.seq * p.H + h, part_size = (size_t)DK * DV;
     if (OUT) {
         if (p.h0) grp.template add<TR>(p.h0 + pair * part_size, 0.f, wv);
-        for (int i = 0; i < w.part; ++i) {
+        for (int i = p.summed ? max(w.part - 1, 0) : 0; i < w.part; ++i) {
             if (w.slot + i >= p.n_part) break;
             const size_t at = (size_t)(w.slot + i) * p.H + h;
             grp.add_part(p.part + at * part_size, p.dec[at], wv);
@@ -886,6 +904,59 @@ __global__ __launch_bounds__(256) void linear_deferred_kernel(const LinearChunkP
     for (int e = threadIdx.x; e < state / 4; e += 256) dst[e] = src[e];
 }
 
+// Sums of the parts in place, so that a segment of the backward walks starts from
+// one state and one decay: part i becomes what all of the sequence's parts up to i
+// (backwards: from i on) leave at its end.  For calls of at most 16 (sequence, head)
+// pairs with more than 6 segments to a sequence, where a segment's own sum of up to n
+// states is the longer path (whole backward, bf16, D = 128): T = 1024, H = 4: 76 -> 66
+// us, T = 4096, H = 8: 137 -> 100, T = 8192, H = 2: 179 -> 110, T = 16384, H = 16:
+// 419 -> 382.  With more pairs the segments' own sums hide behind one another's
+// products, and a launch more costs (H = 32: T = 1024 89 -> 96, T = 4096 194 -> 204).
+// blockIdx.x: the pair; .y: which array; .z: 1024 elements of the state.
+__global__ __launch_bounds__(256) void linear_scan_kernel(const LinearBwdParams b, int state)
+{
+    const LinearChunkParams &p = b.c;
+    const bool forwards = blockIdx.y == 0;
+    float *part = forwards ? b.part_fwd : blockIdx.y == 1 ? p.part : p.part_tr;
+    const float *dec = forwards ? b.dec_fwd : p.dec;
+    float *sum = forwards ? b.sum_fwd : b.sum_rev;
+    const bool scribe = blockIdx.z == 0 && blockIdx.y < 2 && threadIdx.x == 0;
+    const size_t e = (size_t)blockIdx.z * 1024 + threadIdx.x * 4;
+    const int h = (int)(blockIdx.x % p.H);
+    int slot, n;
+    parts_of(p, (int)(blockIdx.x / p.H), slot, n);
+    n = min(n, p.n_part - slot);
+    if (n < 2) {                                           // one part is its own sum
+        if (n == 1 && scribe) sum[(size_t)slot * p.H + h] = dec[(size_t)slot * p.H + h];
+        return;
+    }
+    const long step = forwards ? p.H : -(long)p.H;
+    const size_t at = (size_t)(forwards ? slot : slot + n - 1) * p.H + h;
+    const auto load = [&](int i) {
+        return *reinterpret_cast<const f32x4 *>(part + (at + (long)min(i, n - 1) * step) * state + e);
+    };
+    // eight parts in flight; what is read again behind the last part is not used
+    f32x4 S = {0.f, 0.f, 0.f, 0.f}, y[4] = {load(0), load(1), load(2), load(3)};
+    float d = 1.f;
+    for (int i0 = 0; i0 < n; i0 += 4) {
+        f32x4 z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = load(i0 + 4 + j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i0 + j < n) {
+                const size_t to = at + (i0 + j) * step;
+                const float f = dec[to];
+                S = S * f + y[j];
+                *reinterpret_cast<f32x4 *>(part + to * state + e) = S;
+                d *= f;
+                if (scribe) sum[to] = d;
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = z[j];
+    }
+}
+
 // dV (waves 0-3) and dK (waves 4-7) of one segment for one value head, chunks
 // backwards, from one staging of q, k, v and dO; and dg.  With the terms
 //   y_t = q_t . (state part of dq_t)            (from WALK_DQ_DG)
@@ -935,7 +1006,7 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
     G grp;
     grp.clear();
     if (b.dhT) grp.template add<KEYS>(b.dhT + pair * part_size, 0.f, wv);
-    for (int i = w.parts - 1; i > w.part; --i) {
+    for (int i = p.summed ? min(w.part + 1, w.parts - 1) : w.parts - 1; i > w.part; --i) {
         if (w.slot + i - 1 >= p.n_part) continue;
         const size_t at = (size_t)(w.slot + i - 1) * p.H + h;
         if constexpr (KEYS)
@@ -1175,6 +1246,11 @@ template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdPar
         hipLaunchKernelGGL((linear_walk_kernel<T, DK, DV, WALK_STATE_REV>), grid, block, 0, stream, s);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         dq.part = b.part_fwd; dq.dec = b.dec_fwd;
+        if (c.summed) {
+            hipLaunchKernelGGL(linear_scan_kernel, dim3(c.N * c.H, 3, DK * DV / 1024), dim3(256), 0, stream, b, DK * DV);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            dq.dec = b.sum_fwd;
+        }
     }
     dq.q = b.d_o; dq.k = c.v; dq.v = c.k; dq.q_rows = c.q; dq.o = b.dq;
     if (b.dg)
@@ -1188,7 +1264,9 @@ template <typename T, int DK, int DV> static hipError_t bwd_t(const LinearBwdPar
     // above 64 KiB a kernel asks for its dynamic LDS; per device, so with every launch
     e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, grid, dim3(128 * NW), lds, stream, b);
+    LinearBwdParams kv = b;
+    if (c.summed) kv.c.dec = b.sum_rev;
+    hipLaunchKernelGGL(kernel, grid, dim3(128 * NW), lds, stream, kv);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (c.defer) {
         hipLaunchKernelGGL(linear_deferred_kernel, grid, block, 0, stream, c, b.dh0, 1, DK * DV);

@@ -80,7 +80,7 @@ def _backward_check(d, cu, got, scale):
         assert ref.rel2(y, r) <= TOL2[x.dtype], name
 
 
-LENS = [[1], [63], [64], [65], [130, 0, 1, 31, 32, 33], [0], [300, 257], [1100], [520, 3, 700, 256, 512]]
+LENS = [[1], [63], [64], [65], [130, 0, 1, 31, 32, 33], [0], [300, 257], [1100], [520, 3, 700, 256, 512], [2100]]
 HEADS = [(2, 2, 64, 64), (2, 1, 128, 64), (3, 3, 64, 128), (2, 2, 128, 128)]
 
 
