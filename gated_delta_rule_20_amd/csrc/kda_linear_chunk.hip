@@ -966,8 +966,10 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const LinearBwdParams 
 //   dg_u = sum_{t >= u} y_t + sum_{s < u} z_s + sum_{s < u <= t} x_ts + w
 // none of which cancel.  w follows from R = <state, its gradient> at the chunk's end:
 // w = R - sum z, and R at the chunk's start is w + sum y, both in float64; R is formed anew
-// from the state that WALK_DQ_DG left at every anchor, and w is 0 where e^{G_end} < 2^-24 (then w is below the rounding
-// of R), so the roundings of y and z do not pile up.
+// from the state that WALK_DQ_DG left at every anchor.  R carries the float32 roundings of the terms that it has passed
+// since then, whose magnitudes M adds up, and so does w.  Where the chunk forgets (e^{G_end} < 2^-24) and R - sum z is
+// not above those roundings (2^-22 M, two bits above one of M), w is 0, so that they do not reach the tokens before.
+// The decay alone does not say so: a state that is large next to what the chunk adds leaves a w above them.
 // One workgroup fills a compute unit (96 KiB of LDS, 8 waves of up to 256 registers); it is bound by
 // latency: the matrix cores are busy 23% of the time, the waves wait for LDS, barriers and one another.
 // T = 8192, H = 32, d = 128, bf16, with dg: 200 to 220 us of a call's 355 us (without dg 166 us).
@@ -1043,6 +1045,7 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
         }
     }
     double R = 0.0, sum_dg = 0.0;
+    float M = 0.f;
     for (int i = 0; i < nc; ++i) {
         const int c = nc - 1 - i, n = min(C, toks - c * C), row = row0 + c * C;
         const int pos = first + c * C + n;
@@ -1121,6 +1124,7 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
                     R = 0.0;
 #pragma unroll
                     for (int j = 0; j < NW; ++j) R += s.r[j];
+                    M = fabsf((float)R);
                 }
                 float up = z, down = cx;                       // inclusive sums from below, from above
 #pragma unroll
@@ -1129,8 +1133,11 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
                     if (u >= m) up += a;
                     if (u + m < C) down += e;
                 }
-                const double wt = d.total < 0x1p-24f ? 0.0 : R - wave_total((double)z);
+                double wt = R - wave_total((double)z);
+                M += wave_sum(fabsf(z));
+                if (d.total == 0.f || (d.total < 0x1p-24f && fabs(wt) <= 0x1p-22 * (double)M)) wt = M = 0.f;
                 R = wt + wave_total(u < C ? (double)y : 0.0);
+                M += wave_sum(u < C ? fabsf(y) : 0.f);
                 const float dg = down + (up - z) + (float)wt;
                 if (u < n) {
                     if (p.g_per_head) sum_dg += dg; else b.dg[(size_t)(row + u) * p.H + h] = dg;
