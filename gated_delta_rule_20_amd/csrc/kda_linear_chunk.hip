@@ -221,6 +221,27 @@ __device__ __forceinline__ float row_total(float v)
     return dpp_add<0x140, 0xF>(v);  // row_mirror
 }
 
+// Sums over a row's 16 lanes from this one on, and over those before it.
+__device__ __forceinline__ float row_from(float v)
+{
+    v = dpp_add<0x101, 0xF>(v);  // row_shl:1, 2, 4, 8; nothing comes in from outside the row
+    v = dpp_add<0x102, 0xF>(v);
+    v = dpp_add<0x104, 0xF>(v);
+    return dpp_add<0x108, 0xF>(v);
+}
+__device__ __forceinline__ float row_before(float v)
+{
+    v = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x111, 0xF, 0xF, false));
+    v = dpp_add<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    return dpp_add<0x118, 0xF>(v);
+}
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
 __device__ __forceinline__ double wave_total(double v)
 {
 #pragma unroll
@@ -964,7 +985,10 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const LinearBwdParams 
 //   x_ts = scale D_ts (q_t . k_s)(dO_t . v_s),  t > s
 //   w = e^{G_end} <S, dS>                       (S enters, dS leaves the chunk)
 //   dg_u = sum_{t >= u} y_t + sum_{s < u} z_s + sum_{s < u <= t} x_ts + w
-// none of which cancel.  w follows from R = <state, its gradient> at the chunk's end:
+// and each sum is formed from its own terms alone (a running sum of what enters and leaves it would leave the large
+// terms' roundings in the small sums behind a strong decay): the pairs by tiles of 16 x 16, on the diagonal summed over
+// t >= u in the products' registers, and elsewhere as prefix and suffix sums inside a tile of 16 tokens plus
+// totals of whole tiles.  w follows from R = <state, its gradient> at the chunk's end:
 // w = R - sum z, and R at the chunk's start is w + sum y, both in float64; R is formed anew
 // from the state that WALK_DQ_DG left at every anchor.  R carries the float32 roundings of the terms that it has passed
 // since then, whose magnitudes M adds up, and so does w.  Where the chunk forgets (e^{G_end} < 2^-24) and R - sum z is
@@ -980,7 +1004,7 @@ template <typename T, int DK, int DV> struct DkdvLds {
     Decay<C> decay[2];
     float z[NW][C];           // by wave: sums over its columns
     // x summed over the 16 s of a tile (for each t, by the tile's s), over its 16 t (for each s, by its t); 0 where no
-    // tile is
+    // tile is.  On the diagonal x_t holds the tile's sum over s < u <= t for each u, and x_s is 0.
     float x_t[C / 16][C], x_s[C / 16][C];
     double r[NW];             // by wave: <state, gradient> at an anchor
 };
@@ -1073,13 +1097,21 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
                     const f32x4 a = G::decayed(G::scores(s.k, s.q, rt, st), d, p.scale, rt, st);
                     const f32x4 dov = GK::scores(s.v, s.d_o, rt, st);
                     G::put_scores(s.p[0], a, rt, st);
-                    f32x4 xs;
+                    f32x4 xs = a * dov;
+                    if (rt == st) {                            // a lane's s is x, its t are 4 g .. + 3
+                        xs[2] += xs[3];
+                        xs[1] += xs[2];
+                        xs[0] += xs[1];
+                        const float pair = __shfl_xor(xs[0], 16), half = __shfl_xor(xs[0] + pair, 32);
+                        const float later = ((g & 1) == 0 ? pair : 0.f) + (g < 2 ? half : 0.f);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) xs[e] = rt == st && 4 * g + e <= x ? 0.f : a[e] * dov[e];
-                    float over = (xs[0] + xs[1]) + (xs[2] + xs[3]);
-                    over += __shfl_xor(over, 16);
-                    over += __shfl_xor(over, 32);
-                    if (g == 0) s.x_s[st][16 * rt + x] = over;
+                        for (int e = 0; e < 4; ++e) xs[e] = x < 4 * g + e ? xs[e] + later : 0.f;
+                    } else {
+                        float over = (xs[0] + xs[1]) + (xs[2] + xs[3]);
+                        over += __shfl_xor(over, 16);
+                        over += __shfl_xor(over, 32);
+                        if (g == 0) s.x_s[st][16 * rt + x] = over;
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) xs[e] = row_total(xs[e]);
                     if (x == 0) *reinterpret_cast<f32x4 *>(&s.x_t[rt][16 * st + 4 * g]) = xs;
@@ -1111,14 +1143,20 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
             G::store((T *)b.dv + ((size_t)row * p.H + h) * DV, sv, n, O, wv);
             grp.update(s.q, s.d_o, d, wv);
             if (DG && scribe) {
-                const int u = lane_id();
-                float z = 0.f, cx = 0.f;
+                const int u = lane_id(), tile = u >> 4;
+                float z = 0.f, yu = 0.f, own = 0.f, from = 0.f, to = 0.f, over[NT] = {};
                 if (u < C) {
 #pragma unroll
                     for (int j = 0; j < NW; ++j) z += s.z[j][u];
-                    cx = y;
+                    yu = y;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) cx += s.x_t[j][u] - s.x_s[j][u];
+                    for (int j = 0; j < NT; ++j) {
+                        const float x = s.x_t[j][u];           // u as t, s in tile j
+                        own = tile == j ? x : own;
+                        if (j > 0 && j + 1 < NT) over[j] = tile > j ? to : 0.f;
+                        to += tile > j ? x : 0.f;
+                        from += s.x_s[j][u];                   // u as s, t in tile j
+                    }
                 }
                 if (anchor >= 0) {
                     R = 0.0;
@@ -1126,19 +1164,29 @@ __device__ __forceinline__ void dkdv_walk(const LinearBwdParams &b, DkdvLds<T, D
                     for (int j = 0; j < NW; ++j) R += s.r[j];
                     M = fabsf((float)R);
                 }
-                float up = z, down = cx;                       // inclusive sums from below, from above
+                // inside the tile; then the other tiles' y behind it, z before it and pairs over it
+                float dg = (own + row_from(yu + to)) + row_before(z + from);
+                const float yt = row_total(yu), zt = row_total(z);
+                double ys = 0.0, zs = 0.0;
 #pragma unroll
-                for (int m = 1; m < C; m *= 2) {
-                    const float a = __shfl_up(up, m), e = __shfl_down(down, m);
-                    if (u >= m) up += a;
-                    if (u + m < C) down += e;
+                for (int j = 0; j < NT; ++j) {
+                    const float yj = lane_value(yt, 16 * j), zj = lane_value(zt, 16 * j);
+                    ys += (double)yj;
+                    zs += (double)zj;
+                    dg += (tile < j ? yj : 0.f) + (tile > j ? zj : 0.f);
                 }
-                double wt = R - wave_total((double)z);
+#pragma unroll
+                for (int j = 1; j + 1 < NT; ++j) {
+                    const float pairs = wave_sum(over[j]);
+                    dg += tile == j ? pairs : 0.f;
+                }
+                double wt = R - zs;
                 M += wave_sum(fabsf(z));
                 if (d.total == 0.f || (d.total < 0x1p-24f && fabs(wt) <= 0x1p-22 * (double)M)) wt = M = 0.f;
-                R = wt + wave_total(u < C ? (double)y : 0.0);
-                M += wave_sum(u < C ? fabsf(y) : 0.f);
-                const float dg = down + (up - z) + (float)wt;
+                if (c == 0 && w.part == 0 && !p.h0) wt = 0.0;  // no state enters
+                R = wt + ys;
+                M += wave_sum(fabsf(yu));
+                dg += (float)wt;
                 if (u < n) {
                     if (p.g_per_head) sum_dg += dg; else b.dg[(size_t)(row + u) * p.H + h] = dg;
                 }

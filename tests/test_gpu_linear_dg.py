@@ -72,3 +72,26 @@ def test_large_state_before_a_strong_decay(at, T, size, dtype):
     assert np.all(np.abs(got - want) <= tol)
     if size == 1e6:                                        # there the bound is below the values themselves
         assert np.all(np.abs(want[at]) > 2 * tol[at])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("part", ["pairs", "keys", "queries"])
+def test_small_elements_among_large_ones(part, dtype):
+    """Sequences of one chunk whose dg has no w: pairs of tokens alone, with what the tokens leave for the final state's
+    gradient (no outputs' gradients), with what they read from the entering state.  Tokens that forget nearly everything have a
+    dg far below their neighbours', made of small terms only, and every element is held to float32 of its own
+    terms; the first one without an entering state is 0."""
+    H = 3
+    lens = [1, 2, 15, 16, 17, 31, 32] + ([33, 48, 49, 63, 64] if dtype == torch.bfloat16 else [])
+    R = sum(lens)
+    r = np.random.RandomState(5)
+    g = -0.002 * torch.rand((R, H), generator=torch.Generator().manual_seed(6))
+    for i in r.choice(R, R // 6, replace=False):
+        g[i, r.randint(H)] = float(r.choice([-5.0, -12.0, -17.0, -25.0]))
+    d, cu = _inputs(lens, H, dtype, g, h0=1.0 if part == "queries" else None, dhT=1.0 if part == "keys" else None,
+                    do=0.0 if part == "keys" else 1.0, seed=7)
+    got = ref.f64(_run(d, cu)[3])
+    want, mags = _want(d, cu)
+    err, tol = np.abs(got - want), ref.bound(want, mags, torch.float32, 64)
+    assert np.all(err <= tol), (float((err / np.maximum(mags, 1e-30)).max()), int((err > tol).sum()))
+    assert ref.rel2(got, want) <= TOL2
