@@ -95,3 +95,56 @@ def test_small_elements_among_large_ones(part, dtype):
     err, tol = np.abs(got - want), ref.bound(want, mags, torch.float32, 64)
     assert np.all(err <= tol), (float((err / np.maximum(mags, 1e-30)).max()), int((err > tol).sum()))
     assert ref.rel2(got, want) <= TOL2
+
+
+def _interval_bound(d, cu, want, mags):
+    """Element bound with R's way: its own terms, and those of the 512 tokens that R is carried over (an anchor lies at
+    every multiple of 512 tokens and at the end), as magnitudes of q . dq and k . dk, which hold all of a token's y
+    and z, and of R itself, which is among the interval's elements."""
+    m = {x: None if y is None else np.abs(ref.f64(y)) if x != "g" else ref.f64(y) for x, y in d.items()}
+    H = m["v"].shape[1]
+    q, k = ref.widen(m["q"], H), ref.widen(m["k"], H)
+    mq, mk = ref.backward(q, k, m["v"], m["g"], m["do"], 1.0, cu, m["h0"], m["dhT"])[:2]
+    token = (q * mq).sum(-1) + (k * mk).sum(-1)
+    passed = np.zeros_like(mags)
+    for a, b in zip(cu[:-1], cu[1:]):
+        for i in range(a, b, 512):
+            rows = slice(i, min(i + 512, b))
+            passed[rows] = token[rows].sum(0) + mags[rows].max(0)
+    n = max(b - a for a, b in zip(cu[:-1], cu[1:]))
+    return ref.bound(want, mags + passed, torch.float32, n)
+
+
+def _many(n):
+    return np.random.RandomState(9).randint(0, 9, n).tolist()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lens", [[5000, 0, 1, 3300, 511, 700], [600, *_many(70), 4990, *_many(140), 3200]], ids=["searched", "tabulated"])
+@pytest.mark.parametrize("Hk,states", [(32, True), (16, False)])
+def test_segments_of_several_anchors(lens, Hk, states, dtype):
+    """Enough tokens and heads that a workgroup's segment (1024 tokens) holds two anchors, on sequences of several segments
+    among short ones: all gradients of the first and the last two value heads against the recurrence.  Decays forget over
+    some 100 to 1000 tokens, and now and then at once, so states reach across anchors and segments."""
+    H, R = 32, sum(lens)
+    assert R * H > 512 * 512                                # from here on segments are longer than an anchor's interval
+    gen = torch.Generator().manual_seed(10)
+    g = -0.004 * torch.rand((R, H), generator=gen)
+    g[torch.rand((R, H), generator=gen) < 1e-3] = -9.0
+    size = 1.0 if states else None
+    d, cu = _inputs(lens, H, dtype, g, h0=size, dhT=size, seed=11, Hk=Hk)
+    got = [ref.f64(x) for x in _run(d, cu)]
+    group = H // Hk
+    for first in (0, H - 2):
+        heads, kheads = slice(first, first + 2), slice(first // group, (first + 1) // group + 1)
+        sub = {x: None if y is None else (y[:, kheads] if x in ("q", "k") else y[:, heads]).contiguous() for x, y in d.items()}
+        a = [ref.f64(sub[x]) for x in ("q", "k", "v", "g", "do")]
+        want = ref.backward(*a, 1.0, cu, ref.f64(sub["h0"]), ref.f64(sub["dhT"]))
+        mags = ref.backward(*(y if i == 3 else np.abs(y) for i, y in enumerate(a)), 1.0, cu,
+                            *(None if sub[x] is None else np.abs(ref.f64(sub[x])) for x in ("h0", "dhT")))
+        for name, x, w, m, hs in zip(("dq", "dk", "dv", "dg", "dh0"), got, want, mags, (kheads, kheads, heads, heads, heads)):
+            x = x[:, hs]
+            t = dtype if name in ("dq", "dk", "dv") else torch.float32
+            tol = _interval_bound(sub, cu, w, m) if name == "dg" else ref.bound(w, m, t, max(lens))
+            assert np.all(np.abs(x - w) <= tol), name
+            assert ref.rel2(x, w) <= (2.0 ** -8 if t == torch.bfloat16 else TOL2), name
