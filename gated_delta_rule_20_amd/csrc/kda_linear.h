@@ -72,6 +72,9 @@ struct LinearBwdParams {
 // sequences of 64 tokens, H = 8: searched 86 us, tabulated 77 us; 20000 of 16: 54 and 3.4 ms.
 constexpr int TABLE_SEQUENCES = 128;
 
+// Threads of the largest workgroup that each direction launches for a segment and head.
+constexpr int LINEAR_FWD_THREADS = 256, LINEAR_BWD_THREADS = 512;
+
 hipError_t launch_linear_fwd(int bf16, int Dk, int Dv, const LinearChunkParams &p, hipStream_t stream);
 hipError_t launch_linear_bwd(int bf16, int Dk, int Dv, const LinearBwdParams &p, hipStream_t stream);
 

@@ -98,9 +98,12 @@ kda_status_t check_list(const int32_t *a, int n, const char *name)
     return KDA_SUCCESS;
 }
 
+// A launch has fewer than 2^32 threads.  Checked here, so that no call is turned away after its first kernel.
+bool launchable(long long workgroups, long long threads) { return workgroups <= 0xffffffffLL / threads; }
+
 kda_status_t check_grid(const kda::CachePools &pools, long long pages)
 {
-    if (pages * (long long)pools.slices > 0x7fffffffLL)
+    if (!launchable(pages * (long long)pools.slices, 256))
         return fail(KDA_ERROR_NOT_SUPPORTED, "too many page bytes for one call");
     return KDA_SUCCESS;
 }
@@ -163,6 +166,15 @@ kda_status_t plan_linear(const LinearShape &a, bool backward, LinearPlan *pl)
     pl->first_pass = over(a.T, pl->seg) > 0;     // packed: some sequence may be that long
     // where summing them once pays: figures at linear_scan_kernel
     pl->sum_parts = backward && pl->first_pass && longest > 6 * seg && (long long)pl->N * a.H <= 16;
+    return KDA_SUCCESS;
+}
+
+// One workgroup for each segment and head.
+kda_status_t check_segments(const LinearPlan &pl, int H, int threads)
+{
+    if (!launchable((long long)pl.n_seg * H, threads))
+        return fail(KDA_ERROR_NOT_SUPPORTED, "too many segments for one call: %d of %d heads, at most %lld in all", pl.n_seg, H,
+                    0xffffffffLL / threads);
     return KDA_SUCCESS;
 }
 
@@ -303,6 +315,7 @@ kda_status_t kda_linear_chunk_fwd(const kda_linear_fwd_args_t *a, void *stream)
     if (!a) return fail(KDA_ERROR_INVALID_VALUE, "args is NULL");
     LinearPlan pl;
     KDA_TRY(plan_linear(shape_of(a), false, &pl));
+    KDA_TRY(check_segments(pl, a->H, kda::LINEAR_FWD_THREADS));
     if (pl.rows > 0) {
         KDA_TRY(check_decay(a->g));
         const Ptr req[] = {{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->o, "o"}};
@@ -339,6 +352,7 @@ kda_status_t kda_linear_chunk_bwd(const kda_linear_bwd_args_t *a, void *stream)
     if (!a) return fail(KDA_ERROR_INVALID_VALUE, "args is NULL");
     LinearPlan pl;
     KDA_TRY(plan_linear(shape_of(a), true, &pl));
+    KDA_TRY(check_segments(pl, a->H, kda::LINEAR_BWD_THREADS));
     if (pl.rows > 0) {
         KDA_TRY(check_decay(a->g));
         const Ptr req[] = {{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->d_o, "d_o"}, {a->dq, "dq"}, {a->dk, "dk"}, {a->dv, "dv"}};
@@ -364,8 +378,8 @@ kda_status_t kda_linear_recurrent_step(const kda_linear_step_args_t *a, void *st
     if (a->n_slots < 0) return fail(KDA_ERROR_INVALID_VALUE, "need n_slots >= 0 (got %d)", a->n_slots);
     if (!a->slots && a->n_slots < a->N)
         return fail(KDA_ERROR_INVALID_VALUE, "without slots n_slots=%d must be at least N=%d", a->n_slots, a->N);
-    // up to four workgroups per (sequence, head) pair, where pairs are few
-    if ((long long)a->N * a->H > 0x3fffffffLL) return fail(KDA_ERROR_NOT_SUPPORTED, "N*H too large");
+    // one workgroup of 256 threads per (sequence, head) pair (more where pairs are few)
+    if (!launchable((long long)a->N * a->H, 256)) return fail(KDA_ERROR_NOT_SUPPORTED, "N*H too large");
     if (a->N == 0) return ok();
     KDA_TRY(check_decay(a->g));
     const Ptr req[] = {{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->state, "state"}, {a->new_state, "new_state"}, {a->o, "o"}};

@@ -1269,6 +1269,7 @@ __global__ __launch_bounds__(256) void linear_share_kernel(const LinearChunkPara
 template <typename T, int DK, int DV> static hipError_t fwd_t(const LinearChunkParams &p, hipStream_t stream)
 {
     const dim3 grid((unsigned)((size_t)p.n_seg * p.H)), block(64 * NW);
+    static_assert(64 * NW <= LINEAR_FWD_THREADS && 128 * NW <= LINEAR_BWD_THREADS, "grids are checked for these");
     hipError_t e = launch_table(p, stream);
     if (e != hipSuccess) return e;
     if (p.part) {

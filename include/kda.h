@@ -311,6 +311,10 @@ KDA_API kda_status_t kda_recurrent_replay(const kda_replay_args_t *args, void *s
  *   - Outputs must not overlap inputs or one another, but where it is said.
  * Sums, states and decays are held in float32 or more; float32 results
  * (states, their gradients, dg) are accurate to float32 also for bf16 inputs.
+ * Calls that one launch cannot hold are refused with KDA_ERROR_NOT_SUPPORTED: a
+ * forward of 2^24, gradients of 2^23 segments x value heads (each sequence has
+ * one segment or more, so N * H is below that; the workspace queries do not
+ * ask), a step of N * H = 2^24.
  * A NaN or infinity among a sequence's tokens can reach the outputs of the
  * KDA_CHUNK tokens around it, not only those behind it, and no other sequence.
  */
@@ -421,6 +425,8 @@ KDA_API kda_status_t kda_linear_recurrent_step(const kda_linear_step_args_t *arg
  * is the one still being written, the ones before it are read only.
  * All tables are device memory (4-byte aligned); pages and rows out of range
  * are skipped and never accessed.  The arrays must not overlap.
+ * A copy or fork of 2^24 or more pieces (pages x pieces of 32 KiB of each pool's
+ * page) is refused with KDA_ERROR_NOT_SUPPORTED.
  */
 typedef struct {
     void *dst;                     /* pool that is written (compact, fork: the pool) */

@@ -266,3 +266,42 @@ def test_plans_of_the_largest_calls(lib):
                       ("kda_linear_chunk_bwd_workspace_size", _bwd_args(dg=None, Hk=over["H"], **{k: v for k, v in over.items() if k != "Hk"}))):
             assert getattr(lib, fn)(ctypes.byref(a), ctypes.byref(n)) == 0, _message(lib)
             assert n.value < 1 << 50
+
+
+# A launch has fewer than 2^32 threads: 2^24 - 1 workgroups of 256 or 2^23 - 1 of 512.  What is beyond is refused with the
+# other checks, before the first of a call's kernels.
+
+@pytest.mark.parametrize("over", [dict(H=64, N=1 << 18), dict(H=1, Hk=1, N=1 << 24), dict(H=1 << 15, N=(1 << 13) - 1)])
+def test_forward_refuses_more_workgroups_than_a_launch_holds(lib, over):
+    a = _fwd_args(cu_seqlens=0x20000, T=0, **over)
+    assert lib.kda_linear_chunk_fwd(ctypes.byref(a), None) == 2
+    assert "too many segments" in _message(lib)
+
+
+@pytest.mark.parametrize("over", [dict(H=32, N=1 << 18), dict(H=1, Hk=1, N=1 << 23), dict(H=1 << 15, N=(1 << 13) - 1)])
+def test_backward_refuses_more_workgroups_than_a_launch_holds(lib, over):
+    a = _bwd_args(cu_seqlens=0x20000, T=0, **over)
+    assert lib.kda_linear_chunk_bwd(ctypes.byref(a), None) == 2
+    assert "too many segments" in _message(lib)
+
+
+def test_largest_calls_of_one_launch_pass_the_check(lib):
+    """One less, and the next check speaks (or, without anything to write, nothing does)."""
+    fwd = _fwd_args(cu_seqlens=0x20000, T=0, H=1, Hk=1, N=(1 << 24) - 1)
+    assert lib.kda_linear_chunk_fwd(ctypes.byref(fwd), None) == 0
+    fwd.initial_state = 0x10004
+    assert lib.kda_linear_chunk_fwd(ctypes.byref(fwd), None) == 1 and "initial_state" in _message(lib)
+    bwd = _bwd_args(cu_seqlens=0x20000, T=0, H=1, Hk=1, N=(1 << 23) - 1, initial_state=0x10004)
+    assert lib.kda_linear_chunk_bwd(ctypes.byref(bwd), None) == 1 and "initial_state" in _message(lib)
+
+
+def test_step_and_pages_refuse_more_workgroups_than_a_launch_holds(lib):
+    a = _step_args(N=1 << 22, q=None)
+    assert lib.kda_linear_recurrent_step(ctypes.byref(a), None) == 2 and "too large" in _message(lib)
+    a.N -= 1
+    assert lib.kda_linear_recurrent_step(ctypes.byref(a), None) == 1 and "q is NULL" in _message(lib)
+    big = _pool(page=(1 << 25) + 1)                         # 1025 pieces
+    n = (1 << 24) // 1025 + 1
+    assert lib.kda_cache_copy(big, 1, 4, 4, A, A, n, None) == 2 and "too many" in _message(lib)
+    assert lib.kda_cache_fork(big, 1, 4, A, 2, 2, A, A, A, n, A, A, None) == 2 and "too many" in _message(lib)
+    assert lib.kda_cache_copy(_pool(), 1, 4, 4, A, A, 1 << 24, None) == 2
