@@ -14,7 +14,7 @@ from __future__ import annotations
 import torch
 
 from . import CACHE_MAX_POOLS, CachePool, _dev
-from .linear import _call, _check_tensors, _on_stream
+from .linear import _call, _check_tensors, _on_stream, _required
 
 
 def _pools(dst, src=None):
@@ -26,6 +26,8 @@ def _pools(dst, src=None):
         raise ValueError(f"need 1..{CACHE_MAX_POOLS} pools and as many sources, got {len(dst)} and {len(src)}")
     arr = (CachePool * len(dst))()
     for i, (d, s) in enumerate(zip(dst, src)):
+        if d is None or s is None:
+            raise ValueError(f"pool {i} must be a device tensor")
         _dev(d, "pool")
         if d.device != dst[0].device:
             raise ValueError(f"pool {i} is on another device than the first")
@@ -48,14 +50,14 @@ def _pools(dst, src=None):
 
 
 def _list(t, name, device):
-    _check_tensors(device, torch.int32, **{name: t})
-    if t is None or t.dim() != 1:
+    _required(device, torch.int32, **{name: t})
+    if t.dim() != 1:
         raise ValueError(f"{name} must be a 1-d int32 tensor")
     return t.shape[0]
 
 
 def _tables(table, refcount, device, n_pages=None):
-    _check_tensors(device, torch.int32, table=table, refcount=refcount)
+    _required(device, torch.int32, table=table, refcount=refcount)
     if table.dim() != 2:
         raise ValueError(f"table must be [rows, per_row], got {tuple(table.shape)}")
     if refcount.dim() != 1 or (n_pages is not None and refcount.shape[0] != n_pages):
@@ -99,6 +101,8 @@ def cache_fork(pools, table, refcount, parents, children):
 @_on_stream
 def cache_free(table, refcount, rows) -> None:
     """Give up the pages of the named rows: their counts fall by one (not below 0) and the rows become -1."""
+    if table is None:
+        raise ValueError("table must be a device tensor")
     _dev(table, "table", torch.int32)
     _tables(table, refcount, table.device)
     n = _list(rows, "rows", table.device)

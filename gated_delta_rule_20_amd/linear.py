@@ -27,6 +27,14 @@ def _check_tensors(device, dtype, **tensors):
         raise ValueError(f"{name} is on {t.device}, the call is on {device}")
 
 
+def _required(device, dtype, **tensors):
+    """As _check_tensors, of tensors that have to be given."""
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} must be a device tensor")
+    _check_tensors(device, dtype, **tensors)
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -171,9 +179,9 @@ def linear_chunk_bwd(q, k, v, g, d_o, *, scale: float = 1.0, cu_seqlens=None, in
     H, Hk, Dk, Dv, per_head = _heads(q, k, v, g)
     B, T, N = _sequences(q, v, cu_seqlens)
     dev, shape = q.device, (N, H, Dk, Dv)
-    if d_o is None or d_o.shape != v.shape:
-        raise ValueError(f"d_o must have v's shape {tuple(v.shape)}, got {None if d_o is None else tuple(d_o.shape)}")
-    _check_tensors(dev, q.dtype, d_o=d_o)
+    _required(dev, q.dtype, d_o=d_o)
+    if d_o.shape != v.shape:
+        raise ValueError(f"d_o must have v's shape {tuple(v.shape)}, got {tuple(d_o.shape)}")
     _state(initial_state, "initial_state", shape, dev)
     _state(dfinal_state, "dfinal_state", shape, dev)
     dq, dk, dv = _like(dq, "dq", q), _like(dk, "dk", k), _like(dv, "dv", v)
@@ -233,10 +241,10 @@ def linear_recurrent_step(q, k, v, g, state, *, scale: float = 1.0, slots=None, 
     H, Hk, Dk, Dv, per_head = _heads(q, k, v, g)
     if q.dim() != 3:
         raise ValueError(f"q must be [N, Hk, Dk], got {tuple(q.shape)}")
-    if not isinstance(state, torch.Tensor):
-        raise ValueError("state must be a device tensor")
-    N, dev, shape = q.shape[0], q.device, state.shape
-    _check_tensors(dev, torch.float32, state=state, new_state=new_state)
+    N, dev = q.shape[0], q.device
+    _required(dev, torch.float32, state=state)
+    _check_tensors(dev, torch.float32, new_state=new_state)
+    shape = state.shape
     if len(shape) != 4 or shape[1] != H or shape[2] != Dk or shape[3] != Dv:
         raise ValueError(f"state must be [n_slots, H, Dk, Dv] with H, Dk, Dv = {(H, Dk, Dv)}, got {tuple(shape)}")
     if slots is not None:

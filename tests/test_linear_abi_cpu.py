@@ -305,3 +305,19 @@ def test_step_and_pages_refuse_more_workgroups_than_a_launch_holds(lib):
     assert lib.kda_cache_copy(big, 1, 4, 4, A, A, n, None) == 2 and "too many" in _message(lib)
     assert lib.kda_cache_fork(big, 1, 4, A, 2, 2, A, A, A, n, A, A, None) == 2 and "too many" in _message(lib)
     assert lib.kda_cache_copy(_pool(), 1, 4, 4, A, A, 1 << 24, None) == 2
+
+
+def test_binding_refuses_missing_tensors(lib):
+    """None in the place of a tensor that has to be given is a ValueError, as any other wrong argument."""
+    s, i = torch.zeros(3, 2, 64, 64), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="pool 0 must be a device tensor"):
+        kda.cache_copy([None], None, i, i)
+    with pytest.raises(ValueError, match="pool 0 must be a device tensor"):
+        kda.cache_copy([s], [None], i, i)
+    with pytest.raises(ValueError, match="table must be a device tensor"):
+        kda.cache_free(None, i, i)
+    for table, count, name in ((None, i, "table"), (i.view(1, 3), None, "table|refcount")):
+        with pytest.raises(ValueError, match=name):
+            kda.cache._tables(table, count, torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="rows must be a device tensor"):
+        kda.cache._list(None, "rows", torch.device("cuda", 0))
