@@ -46,9 +46,10 @@ def _on_stream(fn):
     def call(*args, stream=None, **kwargs):
         if stream is None:
             return fn(*args, **kwargs)
-        first = args[0] if args else next(iter(kwargs.values()), None)
-        first = first[0] if isinstance(first, (list, tuple)) and first else first
-        if isinstance(first, torch.Tensor) and first.device != stream.device:
+        # all tensors of a call are on one device (checked there), so the first one speaks for them
+        given = (t for x in (*args, *kwargs.values()) for t in (x if isinstance(x, (list, tuple)) else (x,)))
+        first = next((t for t in given if isinstance(t, torch.Tensor)), None)
+        if first is not None and first.device != stream.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
         with torch.cuda.stream(stream):
             return fn(*args, **kwargs)

@@ -321,3 +321,23 @@ def test_binding_refuses_missing_tensors(lib):
             kda.cache._tables(table, count, torch.device("cuda", 0))
     with pytest.raises(ValueError, match="rows must be a device tensor"):
         kda.cache._list(None, "rows", torch.device("cuda", 0))
+
+
+class _Stream:
+    device = torch.device("cuda", 1)
+
+
+@pytest.mark.parametrize("call", [
+    lambda t, i, s: kda.linear_recurrent_step(t, t, t, t, t, stream=s),
+    lambda t, i, s: kda.linear_recurrent_step(scale=1.0, q=t, k=t, v=t, g=t, state=t, stream=s),
+    lambda t, i, s: kda.linear_chunk_fwd(cu_seqlens=None, scale=0.5, q=t, k=t, v=t, g=t, stream=s),
+    lambda t, i, s: kda.linear_chunk_bwd(need_dg=False, q=t, k=t, v=t, g=t, d_o=t, stream=s),
+    lambda t, i, s: kda.cache_copy(t, None, i, i, stream=s),
+    lambda t, i, s: kda.cache_copy([t], None, i, i, stream=s),
+    lambda t, i, s: kda.cache_copy(src_pools=None, pools=[t], dst_pages=i, src_pages=i, stream=s),
+    lambda t, i, s: kda.cache_free(rows=i, table=i, refcount=i, stream=s),
+])
+def test_stream_of_another_device(lib, call):
+    """A stream that is not of the tensors' device is refused, in whatever order the call names its arguments."""
+    with pytest.raises(ValueError, match="stream is on cuda:1, the tensors on cpu"):
+        call(torch.zeros(3, 2, 64), torch.zeros(3, dtype=torch.int32), _Stream())
