@@ -4,7 +4,9 @@ The recurrence next to KDA's that writes without the delta rule and forgets with
 one scalar per head: S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale * S_t^T q_t.
 
 Every call also takes ``stream`` (a torch.cuda.Stream; None: the current one), on which
-it runs and allocates.
+it runs and allocates.  Outputs carry no autograd history, whether or not the inputs require
+gradients: a training step calls :func:`linear_chunk_bwd` itself, for instance from the
+``backward`` of a ``torch.autograd.Function`` whose ``forward`` calls :func:`linear_chunk_fwd`.
 """
 from __future__ import annotations
 
@@ -176,7 +178,8 @@ def linear_chunk_bwd(q, k, v, g, d_o, *, scale: float = 1.0, cu_seqlens=None, in
                      need_dg: bool = True, dq=None, dk=None, dv=None, dg=None, dinitial_state=None, workspace=None):
     """Gradients of :func:`linear_chunk_fwd` (``kda_linear_chunk_bwd``) for the same arguments, given ``d_o`` (shaped
     like o, in its dtype) and ``dfinal_state`` ([N, H, Dk, Dv] fp32, None: zeros).  Returns (dq, dk, dv, dg, dinitial_state):
-    the first three shaped and typed like q, k, v; dg fp32 shaped like g (None without ``need_dg``)."""
+    the first three shaped and typed like q, k, v; dg fp32 shaped like g (None without ``need_dg``).  With ``need_dg`` dq and
+    dk of bf16 calls take the state unrounded, without it rounded once, so their last bits differ."""
     H, Hk, Dk, Dv, per_head = _heads(q, k, v, g)
     B, T, N = _sequences(q, v, cu_seqlens)
     dev, shape = q.device, (N, H, Dk, Dv)

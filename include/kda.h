@@ -309,14 +309,21 @@ KDA_API kda_status_t kda_recurrent_replay(const kda_replay_args_t *args, void *s
  *     h reads query / key head h / (H / Hk).  Hk = H is the plain layout.
  *   - q and k need no norm bound.
  *   - Outputs must not overlap inputs or one another, but where it is said.
- * Sums, states and decays are held in float32 or more; float32 results
- * (states, their gradients, dg) are accurate to float32 also for bf16 inputs.
+ * Sums, states and decays are held in float32 or more, and states and their
+ * gradients are accurate to float32 also for bf16 inputs.  dg is a sum of terms
+ * in float32; the part of it that crosses a whole chunk also carries the roundings
+ * of the terms of up to 512 tokens behind it (see kda_linear_chunk_bwd).  For
+ * bf16 inputs o, dq, dk and dv take two roundings to bf16 besides their own: the
+ * decayed scores of a chunk, and the state where it is multiplied by q (for
+ * dq, dk, dv: by d_o, v, k).  Against 64 bits they are 2.4e-3 off in the 2-norm, where
+ * one rounding of the result alone is 1.7e-3; float32 calls keep float32.
  * Calls that one launch cannot hold are refused with KDA_ERROR_NOT_SUPPORTED: a
  * forward of 2^24, gradients of 2^23 segments x value heads (each sequence has
  * one segment or more, so N * H is below that; the workspace queries do not
  * ask), a step of N * H = 2^24.
  * A NaN or infinity among a sequence's tokens can reach the outputs of the
- * KDA_CHUNK tokens around it, not only those behind it, and no other sequence.
+ * KDA_CHUNK tokens around it, not only those that the formula carries it to, and dg
+ * of up to 512 tokens before it; it reaches no other sequence.
  */
 
 /*
@@ -357,7 +364,14 @@ KDA_API kda_status_t kda_linear_chunk_fwd(const kda_linear_fwd_args_t *args, voi
  * dtype) and d_final_state (gradient of final_state, or NULL for zeros):
  *   dq, dk : [B, T, Hk, Dk]   dv : [B, T, H, Dv]   (call's dtype, required)
  *   dg : float32 shaped like g, or NULL if not wanted.  The gradient of a g
- *        outside its range is that of the value it counts as.
+ *        outside its range is that of the value it counts as.  dg_u is the sum
+ *        over s < u <= t of what token s (or the entering state) writes and
+ *        token t (or the leaving state's gradient) reads.  What crosses u's
+ *        chunk is taken from <state, its gradient>, formed anew every 512 tokens
+ *        (fewer in short segments) and carried from there by the tokens' own
+ *        terms: its error is relative to the largest of those sums.
+ *        With dg, dq and dk of bf16 calls take the state unrounded (three bf16
+ *        terms), without it rounded once, so their last bits differ.
  *   d_initial_state : [N, H, Dk, Dv] float32, or NULL if not wanted; it may
  *        alias d_final_state.
  * Rows of dq, dk, dv and dg outside every sequence are left as they were.

@@ -148,3 +148,34 @@ def test_segments_of_several_anchors(lens, Hk, states, dtype):
             tol = _interval_bound(sub, cu, w, m) if name == "dg" else ref.bound(w, m, t, max(lens))
             assert np.all(np.abs(x - w) <= tol), name
             assert ref.rel2(x, w) <= (2.0 ** -8 if t == torch.bfloat16 else TOL2), name
+
+
+@pytest.mark.parametrize("H", [2, 32])
+@pytest.mark.parametrize("name,where", [("v", "before"), ("k", "before"), ("do", "behind"), ("q", "behind")])
+def test_non_finite_gradients(name, where, H):
+    """An infinity among q, k, v or d_o reaches no other sequence.  In its own it reaches what the formula carries it to
+    (v and k by the state: dq and dg behind them; q and d_o by its gradient: dk, dv and dg before them), its
+    own chunk, and dg of up to 512 tokens before it; all else keeps its bits."""
+    lens = [2100, 300] if H == 2 else [9000, 300]
+    at = lens[0] - 200
+    gen = torch.Generator().manual_seed(13)
+    g = -0.01 * torch.rand((sum(lens), H), generator=gen)
+    d, cu = _inputs(lens, H, torch.bfloat16, g, seed=14)
+    clean = _run(d, cu)
+    d[name][at] = float("inf")
+    got = _run(d, cu)
+    chunk, n = at // 64 * 64, lens[0]
+    for x, y in zip(got[:4], clean):
+        assert torch.equal(x[n:], y[n:])
+    assert torch.equal(got[4][1], clean[4][1])
+    dq, dk, dv, dg = (torch.eq(x, y).flatten(1).all(1).cpu() for x, y in zip(got[:4], clean))
+    if where == "before":                                  # the state behind it, so nothing of dk and dv but its own chunk's
+        assert dq[:chunk].all() and dg[:max(0, at - 512)].all()
+        rest = torch.arange(n + lens[1])
+        rest = (rest < chunk) | (rest >= chunk + 64)
+        assert dk[rest].all() and dv[rest].all()
+    else:                                                  # the gradient of the state before it
+        assert dk[chunk + 64:].all() and dv[chunk + 64:].all() and dg[chunk + 64:].all()
+        rest = torch.arange(n + lens[1])
+        assert dq[(rest < chunk) | (rest >= chunk + 64)].all()
+    assert not torch.isfinite(torch.cat([x[chunk:chunk + 64].flatten().float() for x in got[:4]])).all()
