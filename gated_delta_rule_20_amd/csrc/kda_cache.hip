@@ -44,7 +44,7 @@ __device__ __forceinline__ void copy_range(char *dst, const char *src, size_t be
 template <typename F> __device__ __forceinline__ void copy_slice(const CachePools &pools, int slice, int from, int to, F go)
 {
     // Which pool the slice is of.  Field by field, without a variable index: that would put the kernel's arguments into
-    // scratch memory, at every workgroup's start (2000 pages of 17 KiB: 84 us, against 20 us).
+    // scratch memory, at every workgroup's start (without it 2000 pages of 17 KiB take 15 us).
     char *dst = pools.pool[0].dst;
     const char *src = pools.pool[0].src;
     size_t bytes = pools.pool[0].page_bytes;

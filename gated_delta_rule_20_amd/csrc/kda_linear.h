@@ -68,8 +68,8 @@ struct LinearBwdParams {
 };
 
 // Above this many packed sequences a kernel tabulates their segments first (about 5 us
-// with its launch); up to it every wave searches 64 of them at a time.  300
-// sequences of 64 tokens, H = 8: searched 86 us, tabulated 77 us; 20000 of 16: 54 and 3.4 ms.
+// with its launch); up to it every wave searches 64 of them at a time.  Forward, H = 8, sequences of
+// 64 tokens: 64 searched 17 us, tabulated 19 us; 128: 27 and 28 us; 300: 59 and 50 us; 20000 of 16: 46 and 2.2 ms.
 constexpr int TABLE_SEQUENCES = 128;
 
 // Threads of the largest workgroup that each direction launches for a segment and head.
@@ -90,8 +90,8 @@ struct CachePool {
 
 constexpr int CACHE_MAX_POOLS = 8;
 // Bytes one workgroup copies: eight 16-byte accesses of each of its 256 threads,
-// all in flight at once (256 pages of 2.1 MiB: 208 us, 5.3 TB/s; with 64 or 128 KiB
-// 210 and 219 us, and 16 KiB is slower for pages of 135 KiB, 14.8 against 12.9 us).
+// all in flight at once (256 pages of 2.1 MiB: 209 us, 5.3 TB/s; with 16, 64 and 128 KiB
+// 203, 212 and 217 us; 237 pages of 135 KiB: 11.2 us, with the others 14.1, 14.6 and 19.3 us).
 constexpr size_t CACHE_SLICE = 32768;
 
 struct CachePools {

@@ -114,10 +114,10 @@ kda_status_t check_grid(const kda::CachePools &pools, long long pages)
 // the shortest segments do not fill the chip, a call's time is one workgroup's:
 // about 7 us for every 64 tokens of a segment, over both passes, and 0.8 us for every segment
 // before its own, which is least at sqrt(7.3 * tokens) tokens (T = 1024, H = 4: 256
-// tokens 33 us, 128 tokens 24 us; T = 4096, H = 8, backward: 138 and 152 us).
+// tokens 31 us, 128 tokens 22 us; T = 4096, H = 8: 128, 192, 256 and 512 tokens 39, 37, 40 and 58 us, backward 96, 99, 109 and 167 us).
 // Backwards one workgroup fills a unit, so segments below ANCHOR tokens are made for one
-// workgroup a unit (T = 2048, H = 32: 128 us, with twice the segments 157 us); above, two rounds of shorter
-// segments are better again (T = 8192, H = 32: 512 tokens 460 us, 1024 tokens 499 us).
+// workgroup a unit (T = 2048, H = 32: 256 tokens 124 us, with twice the segments 149 us); above, two rounds of shorter
+// segments are as good (T = 8192, H = 32: 512 tokens 365 us, 1024 tokens 362 us; T = 16384: 1024 tokens 639 us, 2048 tokens 668 us).
 constexpr int MIN_SEGMENT = 128, SEGMENTS = 512, ANCHOR = 512;
 
 struct LinearPlan {

@@ -759,9 +759,10 @@ enum { WALK_STATE, WALK_STATE_REV, WALK_OUT, WALK_DQ, WALK_STATE_DQ, WALK_DQ_DG 
 // unit, and one computes while the other waits for memory.  Eight waves of half the
 // columns each hide more latency but read Q and K from LDS twice as often (133 K packed
 // tokens: 1.41 ms against 1.26 ms at the time).
-// Measured at H = 32, d = 128, bf16: 64 packed sequences of 128 to 4096 tokens 1.09 ms, 4.66 GB,
-// 4.3 TB/s or 87% of a copy: bound by HBM.  T = 8192: state pass 40 us (3.4 TB/s), output 76 us
-// (3.5 TB/s, with 16 states summed at the start).  T = 131072: 1.42 ms for both.
+// Measured at H = 32, d = 128, bf16: 64 packed sequences of 128 to 4096 tokens 1.10 ms, 4.66 GB,
+// 4.2 TB/s or 86% of a copy: bound by HBM.  T = 8192: 111 us a call; state pass 38 us (3.5 TB/s), output 74 us
+// (3.6 TB/s, with up to 15 states summed at the start; matrix cores busy 22% of the time, bank conflicts 17% of the
+// LDS cycles).  T = 131072: 1.44 ms for both.
 template <typename T, int DK, int DV, int MODE>
 __global__ __launch_bounds__(64 * NW, 2) void linear_walk_kernel(const LinearChunkParams p)
 {
@@ -929,10 +930,10 @@ __global__ __launch_bounds__(256) void linear_deferred_kernel(const LinearChunkP
 // one state and one decay: part i becomes what all of the sequence's parts up to i
 // (backwards: from i on) leave at its end.  For calls of at most 16 (sequence, head)
 // pairs with more than 6 segments to a sequence, where a segment's own sum of up to n
-// states is the longer path (whole backward, bf16, D = 128): T = 1024, H = 4: 76 -> 66
-// us, T = 4096, H = 8: 137 -> 100, T = 8192, H = 2: 179 -> 110, T = 16384, H = 16:
-// 419 -> 382.  With more pairs the segments' own sums hide behind one another's
-// products, and a launch more costs (H = 32: T = 1024 89 -> 96, T = 4096 194 -> 204).
+// states is the longer path (whole backward, bf16, D = 128): T = 1024, H = 4: 73 -> 62
+// us, T = 4096, H = 8: 135 -> 99, T = 8192, H = 2: 177 -> 108, T = 16384, H = 16:
+// 414 -> 370.  With more pairs the segments' own sums hide behind one another's
+// products, and a launch more costs (H = 32: T = 1024 85 -> 91, T = 4096 193 -> 200).
 // blockIdx.x: the pair; .y: which array; .z: 1024 elements of the state.
 __global__ __launch_bounds__(256) void linear_scan_kernel(const LinearBwdParams b, int state)
 {
@@ -995,8 +996,9 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const LinearBwdParams 
 // not above those roundings (2^-22 M, two bits above one of M), w is 0, so that they do not reach the tokens before.
 // The decay alone does not say so: a state that is large next to what the chunk adds leaves a w above them.
 // One workgroup fills a compute unit (96 KiB of LDS, 8 waves of up to 256 registers); it is bound by
-// latency: the matrix cores are busy 23% of the time, the waves wait for LDS, barriers and one another.
-// T = 8192, H = 32, d = 128, bf16, with dg: 200 to 220 us of a call's 355 us (without dg 166 us).
+// latency: the matrix cores are busy 22% of the time, and the waves wait for LDS, barriers and one another for 40% of theirs.
+// T = 8192, H = 32, d = 128, bf16: 196 to 239 us with dg, of a call's 355 to 365 us, 150 to 199 us without (kernel
+// traces; with dg 94 scalar registers are kept in lanes of a vector register, without it 5).
 template <typename T, int DK, int DV> struct DkdvLds {
     static constexpr int C = chunk_of<T>, LK = ld_of<T>(DK), LV = ld_of<T>(DV), LP = ldp_of<T>;
     T q[C * LK], k[C * LK], v[C * LV], d_o[C * LV];

@@ -4,7 +4,7 @@
 // Bound by moving the state once in and once out (2 x Dk x Dv x 4 bytes per
 // sequence and head against 5 Dk Dv operations): every thread holds its part of
 // the state in registers between one 16-byte load and one 16-byte store each.
-// 512 sequences x 32 heads of 128 x 128 (2.13 GB): 388 us, 5.5 TB/s, above a copy's 4.9; 4 sequences: 4.5 us.
+// 512 sequences x 32 heads of 128 x 128 (2.13 GB): 391 us, 5.4 TB/s, above a copy's 4.9; 4 sequences: 4.3 us.
 #include "kda_common.h"
 #include "kda_linear.h"
 
