@@ -19,7 +19,10 @@ import torch
 __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "NOALLOC_WORKSPACE_BYTES", "recurrent_step", "recurrent_replay", "chunk_fwd_workspace_size", "load_library",
            "Fusion", "KDAError", "LIB_PATH", "EXPORTED_SYMBOLS",
            "linear_chunk_fwd", "linear_chunk_fwd_workspace_size", "linear_chunk_bwd", "linear_chunk_bwd_workspace_size",
-           "linear_recurrent_step", "cache_copy", "cache_fork", "cache_free", "cache_compact"]
+           "linear_recurrent_step", "cache_copy", "cache_fork", "cache_free", "cache_compact",
+           "gated_scan_fwd", "gated_scan_fwd_workspace_size", "gated_scan_bwd", "gated_scan_bwd_workspace_size", "gated_scan_step",
+           "block_norm_fwd", "block_norm_bwd", "block_norm_bwd_workspace_size", "BlockNormGrads", "BlockNormSaved",
+           "act_pack", "act_unpack", "Packed", "ACT_GROUP"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 EXPORTED_SYMBOLS = ("kda_chunk_fwd_workspace_size", "kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_recurrent_step",
@@ -27,7 +30,10 @@ EXPORTED_SYMBOLS = ("kda_chunk_fwd_workspace_size", "kda_chunk_fwd", "kda_chunk_
                     "kda_linear_chunk_fwd_workspace_size", "kda_linear_chunk_fwd",
                     "kda_linear_chunk_bwd_workspace_size", "kda_linear_chunk_bwd",
                     "kda_linear_recurrent_step", "kda_cache_copy", "kda_cache_fork", "kda_cache_free",
-                    "kda_cache_compact")
+                    "kda_cache_compact",
+                    "kda_gated_scan_fwd_workspace_size", "kda_gated_scan_fwd", "kda_gated_scan_bwd_workspace_size",
+                    "kda_gated_scan_bwd", "kda_gated_scan_step", "kda_block_norm_fwd", "kda_block_norm_bwd_workspace_size",
+                    "kda_block_norm_bwd", "kda_act_pack", "kda_act_unpack")
 
 KDA_F32, KDA_BF16 = 0, 1
 _DTYPES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
@@ -184,6 +190,32 @@ class CachePool(ctypes.Structure):
     _fields_ = [("dst", ctypes.c_void_p), ("src", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t)]
 
 
+def _struct(name, spec):
+    """A ctypes structure from "type: field, field; ..."."""
+    types = {"i32": ctypes.c_int32, "i64": ctypes.c_int64, "f32": ctypes.c_float, "ptr": ctypes.c_void_p, "size": ctypes.c_size_t}
+    fields = [(field.strip(), types[kind.strip()]) for group in spec.split(";") for kind, names in [group.split(":")]
+              for field in names.split(",")]
+    return type(name, (ctypes.Structure,), {"_fields_": fields})
+
+
+GatedScanFwdArgs = _struct("GatedScanFwdArgs", """
+    i32: B, T, C, dtype, g_dtype; ptr: x; i64: x_stride; ptr: g; i64: g_stride; ptr: A_log; f32: g_min; i32: complement;
+    ptr: cu_seqlens; i32: N; ptr: initial_state, h, final_state, h_codes, h_scales, workspace; size: workspace_bytes""")
+GatedScanBwdArgs = _struct("GatedScanBwdArgs", """
+    i32: B, T, C, dtype, g_dtype; ptr: x; i64: x_stride; ptr: x_scales, g; i64: g_stride; ptr: A_log; f32: g_min;
+    i32: complement; ptr: cu_seqlens; i32: N; ptr: initial_state, h, h_scales, d_h, d_final_state, dx; i64: dx_stride;
+    ptr: dg; i64: dg_stride; ptr: dA_log, d_initial_state, workspace; size: workspace_bytes""")
+GatedScanStepArgs = _struct("GatedScanStepArgs", """
+    i32: N, C, dtype, g_dtype; ptr: x; i64: x_stride; ptr: g; i64: g_stride; ptr: A_log; f32: g_min; i32: complement;
+    ptr: slots; i32: n_slots; ptr: state, new_state, h""")
+BlockNormFwdArgs = _struct("BlockNormFwdArgs", """
+    i32: R, D, dtype, x_dtype; ptr: x, y; i64: y_stride; ptr: gate; i64: gate_stride; ptr: post_weight, res_scale, pre_weight;
+    f32: scale, eps; ptr: x_out, n, x_codes, x_scales, y_codes, y_scales, gate_codes, gate_scales""")
+BlockNormBwdArgs = _struct("BlockNormBwdArgs", """
+    i32: R, D, dtype, x_dtype; ptr: x_new, x_scales, y; i64: y_stride; ptr: y_scales, gate; i64: gate_stride;
+    ptr: gate_scales, post_weight, res_scale, pre_weight; f32: scale, eps; ptr: d_x_new, d_n, dx, dy; i64: dy_stride;
+    ptr: dgate; i64: dgate_stride; ptr: d_post_weight, d_res_scale, d_pre_weight, workspace; size: workspace_bytes""")
+
 CACHE_MAX_POOLS = 8  # KDA_CACHE_MAX_POOLS
 
 _lib = None
@@ -218,7 +250,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             ("kda_cache_copy", pools + [i32, i32, ptr, ptr, i32, ptr]),
             ("kda_cache_fork", pools + [i32, ptr, i32, i32, ptr, ptr, ptr, i32, ptr, ptr, ptr]),
             ("kda_cache_free", [ptr, i32, i32, ptr, i32, ptr, i32, ptr]),
-            ("kda_cache_compact", pools + [i32, ptr, i32, i32, ptr, ptr, ptr, ptr, ptr])):
+            ("kda_cache_compact", pools + [i32, ptr, i32, i32, ptr, ptr, ptr, ptr, ptr]),
+            ("kda_gated_scan_fwd_workspace_size", [ctypes.POINTER(GatedScanFwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
+            ("kda_gated_scan_fwd", [ctypes.POINTER(GatedScanFwdArgs), ptr]),
+            ("kda_gated_scan_bwd_workspace_size", [ctypes.POINTER(GatedScanBwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
+            ("kda_gated_scan_bwd", [ctypes.POINTER(GatedScanBwdArgs), ptr]),
+            ("kda_gated_scan_step", [ctypes.POINTER(GatedScanStepArgs), ptr]),
+            ("kda_block_norm_fwd", [ctypes.POINTER(BlockNormFwdArgs), ptr]),
+            ("kda_block_norm_bwd_workspace_size", [ctypes.POINTER(BlockNormBwdArgs), ctypes.POINTER(ctypes.c_size_t)]),
+            ("kda_block_norm_bwd", [ctypes.POINTER(BlockNormBwdArgs), ptr]),
+            ("kda_act_pack", [i32, ptr, ctypes.c_int64, ctypes.c_int64, i32, ptr, ptr, ptr]),
+            ("kda_act_unpack", [i32, ptr, ptr, ctypes.c_int64, i32, ptr, ptr])):
         getattr(lib, name).argtypes = argtypes
         getattr(lib, name).restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
@@ -517,3 +559,8 @@ def recurrent_replay(q, k, v, g, beta, state, *, replay=None, n_replay=None, n_c
 from .cache import cache_compact, cache_copy, cache_fork, cache_free  # noqa: E402
 from .linear import (linear_chunk_bwd, linear_chunk_bwd_workspace_size, linear_chunk_fwd,  # noqa: E402
                      linear_chunk_fwd_workspace_size, linear_recurrent_step)
+from .act import ACT_GROUP, Packed, act_pack, act_unpack  # noqa: E402
+from .block import (BlockNormGrads, BlockNormSaved, block_norm_bwd, block_norm_bwd_workspace_size,  # noqa: E402
+                    block_norm_fwd)
+from .scan import (gated_scan_bwd, gated_scan_bwd_workspace_size, gated_scan_fwd,  # noqa: E402
+                   gated_scan_fwd_workspace_size, gated_scan_step)

@@ -1,0 +1,185 @@
+"""What stands between two blocks of a model (``kda_block_norm_*``): the norm after a block's output, its gate, the residual
+stream, and the norm before the next block, in one pass over the rows.
+
+    u  = post_weight * y / rms(y)
+    x' = x + scale * res_scale * Sigmoid(gate) * u
+    n  = pre_weight * x' / rms(x')
+
+Every call also takes ``stream`` (a torch.cuda.Stream; None: the current one), on which it runs and allocates.  Outputs
+carry no autograd history: a training step calls :func:`block_norm_bwd` itself.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import _DTYPES, BlockNormBwdArgs, BlockNormFwdArgs
+from .act import Packed, _packed_out, _rows, _saved, _two
+from .linear import _at, _call, _check_tensors, _like, _need, _on_stream, _required, _workspace
+
+
+class BlockNormGrads(NamedTuple):
+    dx: torch.Tensor
+    dy: torch.Tensor | None
+    dgate: torch.Tensor | None
+    dpost_weight: torch.Tensor | None
+    dres_scale: torch.Tensor | None
+    dpre_weight: torch.Tensor | None
+
+
+class BlockNormSaved(NamedTuple):
+    """What the backward pass reads, in 8 bits; in the order of its arguments."""
+    x_new: Packed
+    y: Packed | None
+    gate: Packed | None
+
+
+def _weights(D, device, **weights):
+    for name, w in weights.items():
+        if w is not None:
+            _check_tensors(device, torch.float32, **{name: w})
+            if w.shape != (D,):
+                raise ValueError(f"{name} must be [D] = [{D}], got {tuple(w.shape)}")
+
+
+def _stream_rows(x, name):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError(f"{name} must be a device tensor [..., D]")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    _required(x.device, x.dtype, **{name: x})
+
+
+@_on_stream
+def block_norm_fwd(x, y=None, *, gate=None, post_weight=None, res_scale=None, scale: float = 1.0, pre_weight=None,
+                   eps: float = 1e-6, x_out=None, n_out=None, pack=False):
+    """Forward (``kda_block_norm_fwd``).
+
+    x: the residual stream [..., D] (the blocks' dtype, or fp32 next to bf16 blocks); y, gate: the block's output and its gate's
+    logits, like x in the blocks' dtype, rows of any even spacing; post_weight, res_scale, pre_weight: [D] fp32, each optional
+    (without pre_weight there is no n).  Without y there is no block before: x' is x itself and only n is computed (in
+    ``n_out``'s dtype when given, else x's).  x_out may be x.  ``pack`` (True or a :class:`BlockNormSaved` to write to): x', y
+    and the gate in 8 bits as well.  Returns (x', n or None), with ``pack`` (x', n or None, BlockNormSaved)."""
+    _stream_rows(x, "x")
+    dev, shape = x.device, x.shape
+    R, D = _two(x)
+    if y is not None:
+        dtype = y.dtype if isinstance(y, torch.Tensor) else None
+    else:
+        dtype = x.dtype if n_out is None else n_out.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    a = BlockNormFwdArgs(R, D, _DTYPES[dtype], _DTYPES[x.dtype], x.data_ptr(), y_stride=D, gate_stride=D, scale=scale, eps=eps)
+    if y is not None:
+        a.y, a.y_stride = _rows(y, "y", dev, dtype, shape)
+        x_out = _like(x_out, "x_out", x)
+        a.x_out = x_out.data_ptr()
+    elif x_out is not None:
+        raise ValueError("x_out without y: there is no new residual stream")
+    else:
+        x_out = x
+    if gate is not None:
+        a.gate, a.gate_stride = _rows(gate, "gate", dev, dtype, shape)
+    _weights(D, dev, post_weight=post_weight, res_scale=res_scale, pre_weight=pre_weight)
+    a.post_weight, a.res_scale, a.pre_weight = _at(post_weight), _at(res_scale), _at(pre_weight)
+    n = None
+    if pre_weight is not None:
+        if n_out is None:
+            n = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _check_tensors(dev, dtype, n_out=n_out)
+            if n_out.shape != shape:
+                raise ValueError(f"n_out must be {tuple(shape)}, got {tuple(n_out.shape)}")
+            n = n_out
+        a.n = n.data_ptr()
+    saved = None
+    if pack is not None and pack is not False:
+        given = pack if isinstance(pack, BlockNormSaved) else (True, y is not None, gate is not None)
+        if (given[1] is None and y is not None) or (given[2] is None and gate is not None):
+            raise ValueError("pack must hold a Packed for each of x_new, y and gate that there is")
+        saved = BlockNormSaved(_packed_out(given[0], "pack.x_new", shape, dev),
+                               _packed_out(given[1] if y is not None else None, "pack.y", shape, dev),
+                               _packed_out(given[2] if gate is not None else None, "pack.gate", shape, dev))
+        for name, p in zip(("x", "y", "gate"), saved):
+            if p is not None:
+                setattr(a, name + "_codes", p.codes.data_ptr())
+                setattr(a, name + "_scales", p.scales.data_ptr())
+    _call("kda_block_norm_fwd", (ctypes.byref(a),), dev)
+    return (x_out, n, saved) if saved is not None else (x_out, n)
+
+
+@_on_stream
+def block_norm_bwd(x_new, y, dx_new, dn=None, *, gate=None, post_weight=None, res_scale=None, scale: float = 1.0,
+                   pre_weight=None, eps: float = 1e-6, need_dweights: bool = True, dtype=None, dx=None, dy=None, dgate=None,
+                   workspace=None) -> BlockNormGrads:
+    """Gradients of :func:`block_norm_fwd` (``kda_block_norm_bwd``), given ``dx_new`` (gradient of x', x's dtype) and ``dn``
+    (gradient of n, the blocks' dtype), one of which may be None (zeros).
+
+    x_new: x' as the forward returned it (read, and required, with ``dn`` only); y, gate: its inputs; each a tensor or a
+    :class:`Packed`.  ``dtype``: the blocks' dtype (None: that of dn, else of y, the gate or dy where they are tensors, else of
+    dx_new).  dx may be dx_new; dy and dgate may go to rows of any even spacing.  Returns a
+    :class:`BlockNormGrads`; the weights' gradients are fp32, None where there is no weight or without ``need_dweights``."""
+    ref = dx_new if dx_new is not None else dn
+    _stream_rows(ref, "dx_new" if dx_new is not None else "dn")
+    dev, shape = ref.device, ref.shape
+    R, D = _two(ref)
+    if dn is not None:
+        _stream_rows(dn, "dn")
+    if dtype is None:
+        dtype = next((t.dtype for t in (dn, y, gate, dy) if isinstance(t, torch.Tensor)), ref.dtype)
+    x_dtype = dx_new.dtype if dx_new is not None else x_new.dtype if isinstance(x_new, torch.Tensor) else \
+        dx.dtype if dx is not None else dtype
+    if dtype not in _DTYPES or x_dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtypes {dtype}, {x_dtype}")
+    if y is None and (gate is not None or post_weight is not None or res_scale is not None):
+        raise ValueError("gate, post_weight and res_scale belong to y, which is None")
+    if dn is not None and pre_weight is None:
+        raise ValueError("dn without pre_weight")
+    a = BlockNormBwdArgs(R, D, _DTYPES[dtype], _DTYPES[x_dtype], y_stride=D, gate_stride=D, scale=scale, eps=eps, dy_stride=D,
+                         dgate_stride=D)
+    if dn is not None:
+        _check_tensors(dev, dtype, dn=dn)
+        if dn.shape != shape:
+            raise ValueError(f"dn must be {tuple(shape)}, got {tuple(dn.shape)}")
+        a.d_n = dn.data_ptr()
+        if isinstance(x_new, Packed):
+            a.x_new, _, a.x_scales = _saved(x_new, "x_new", dev, x_dtype, shape)
+        else:
+            _required(dev, x_dtype, x_new=x_new)
+            if x_new.shape != shape:
+                raise ValueError(f"x_new must be {tuple(shape)}, got {tuple(x_new.shape)}")
+            a.x_new = x_new.data_ptr()
+    a.d_x_new = _at(dx_new)
+    if dx is None:
+        dx = torch.empty(shape, dtype=x_dtype, device=dev)
+    else:
+        _check_tensors(dev, x_dtype, dx=dx)
+        if dx.shape != shape:
+            raise ValueError(f"dx must be {tuple(shape)}, got {tuple(dx.shape)}")
+    a.dx = dx.data_ptr()
+    dy, dgate = (dy if y is not None else None), (dgate if gate is not None else None)
+    if y is not None:
+        a.y, a.y_stride, a.y_scales = _saved(y, "y", dev, dtype, shape)
+        dy = torch.empty(shape, dtype=dtype, device=dev) if dy is None else dy
+        a.dy, a.dy_stride = _rows(dy, "dy", dev, dtype, shape)
+    if gate is not None:
+        a.gate, a.gate_stride, a.gate_scales = _saved(gate, "gate", dev, dtype, shape)
+        dgate = torch.empty(shape, dtype=dtype, device=dev) if dgate is None else dgate
+        a.dgate, a.dgate_stride = _rows(dgate, "dgate", dev, dtype, shape)
+    _weights(D, dev, post_weight=post_weight, res_scale=res_scale, pre_weight=pre_weight)
+    a.post_weight, a.res_scale, a.pre_weight = _at(post_weight), _at(res_scale), _at(pre_weight)
+    grads = [torch.empty_like(w) if w is not None and need_dweights else None for w in (post_weight, res_scale, pre_weight)]
+    a.d_post_weight, a.d_res_scale, a.d_pre_weight = map(_at, grads)
+    workspace = _workspace("kda_block_norm_bwd_workspace_size", a, workspace, dev)
+    _call("kda_block_norm_bwd", (ctypes.byref(a),), dev)
+    return BlockNormGrads(dx, dy, dgate, *grads)
+
+
+def block_norm_bwd_workspace_size(x_new, *, weights: int = 3) -> int:
+    """Workspace bytes :func:`block_norm_bwd` needs for x_new [..., D] when gradients of ``weights`` weights are wanted (0: none)."""
+    R, D = _two(x_new.codes if isinstance(x_new, Packed) else x_new)
+    a = BlockNormBwdArgs(R, D, scale=1.0)
+    a.d_pre_weight = 16 if weights else None   # only whether one is given is read
+    return _need("kda_block_norm_bwd_workspace_size", a)

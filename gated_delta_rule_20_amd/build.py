@@ -11,7 +11,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_abi.hip", "kda_prefill.hip", "kda_replay.hip",
-           "kda_linear_abi.hip", "kda_linear_step.hip", "kda_linear_chunk.hip", "kda_cache.hip"]
+           "kda_linear_abi.hip", "kda_linear_step.hip", "kda_linear_chunk.hip", "kda_cache.hip",
+           "kda_block_abi.hip", "kda_scan.hip", "kda_block_norm.hip", "kda_act.hip"]
 
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-shared", "--offload-arch=gfx950",

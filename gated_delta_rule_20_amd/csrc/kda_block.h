@@ -1,0 +1,93 @@
+// kda_block.h -- host-side interface of the gated scan, of the norms around a
+// block and of activations in 8 bits.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace kda {
+
+constexpr int ACT_GROUP = 128;        // channels that share a scale
+constexpr int NORM_MAX_D = 16384;     // channels of a row that block norms hold in registers
+
+// Rows of C elements: of a type, or (scales set) int8 codes with their scales.
+struct Rows {
+    const void *p;
+    const float *scales;              // [rows, groups] or null
+    int64_t stride;                   // elements from row to row
+};
+
+// An 8-bit copy that a kernel also writes.
+struct PackedOut {
+    int8_t *codes;                    // null: none
+    float *scales;
+};
+
+struct ScanParams {
+    int rows, T, C;                   // rows of all sequences; tokens per sequence when cu is null
+    const int32_t *cu;                // [N + 1] or null
+    int N;
+    Rows x, g;                        // backward: x only with complement
+    const float *A_log;               // [C] or null: g holds log-decays
+    float g_min;
+    int complement;
+    const float *h0;                  // [N, C] or null
+    // forward
+    void *h;
+    float *hT;
+    PackedOut h8;
+    // backward
+    Rows hs;                          // p null: no dg
+    const void *d_h;
+    const float *dhT;
+    void *dx, *dg;
+    int64_t dx_stride, dg_stride;
+    float *dA, *dh0;
+    float *dA_part;                   // [parts, C]
+};
+
+struct ScanStepParams {
+    int N, C;
+    Rows x, g;
+    const float *A_log;
+    float g_min;
+    int complement;
+    const int32_t *slots;             // [N] or null
+    int n_slots;
+    const float *state;
+    float *new_state;
+    void *h;
+};
+
+hipError_t launch_scan_fwd(int bf16, int g_bf16, const ScanParams &p, hipStream_t stream);
+hipError_t launch_scan_bwd(int bf16, int g_bf16, const ScanParams &p, hipStream_t stream);
+hipError_t launch_scan_step(int bf16, int g_bf16, const ScanStepParams &p, hipStream_t stream);
+
+struct NormParams {
+    int R, D;
+    Rows x, y, gate;                  // backward: x is the stream behind the block; y.p, gate.p may be null
+    const float *post, *res, *pre;    // [D] or null
+    float scale, eps;
+    // forward
+    void *x_out, *n;
+    PackedOut x8, y8, gate8;
+    // backward
+    const void *d_x, *d_n;            // or null
+    void *dx, *dy, *dgate;
+    int64_t dy_stride, dgate_stride;
+    float *dpost, *dres, *dpre;       // [D] or null
+    float *part;                      // [3, parts, D]
+    int parts;
+};
+
+hipError_t launch_norm_fwd(int bf16, int x_bf16, const NormParams &p, hipStream_t stream);
+hipError_t launch_norm_bwd(int bf16, int x_bf16, const NormParams &p, hipStream_t stream);
+
+// rows x D values at a stride to codes and scales, and back.
+// With first and last only rows [*first, *last) are packed.
+hipError_t launch_act_pack(int bf16, const Rows &x, long long rows, int D, const PackedOut &out, hipStream_t stream,
+                           const int32_t *first = nullptr, const int32_t *last = nullptr);
+hipError_t launch_act_unpack(int bf16, const Rows &x, long long rows, int D, void *out, hipStream_t stream);
+
+}  // namespace kda

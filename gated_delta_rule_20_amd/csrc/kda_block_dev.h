@@ -1,0 +1,206 @@
+// kda_block_dev.h -- device-side building blocks of the gated scan, the norms
+// around a block and 8-bit activations: eight consecutive channels a lane.
+#pragma once
+
+#include "kda_block.h"
+#include "kda_common.h"
+
+namespace kda {
+
+constexpr int LANE_CH = 8;            // channels a lane holds: 16 bytes of bf16, one lane's share of a group of 128
+constexpr float LOG2E = 1.44269504088896340736f;
+
+// Global memory takes 16-byte accesses at any element address, so rows of odd
+// length need no path of their own but for the last, shorter group of 8.
+typedef __bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef int8_t i8x8_any __attribute__((ext_vector_type(8), aligned(1)));
+
+// Channels [c, c + n) of a row, n in 0..8 (the rest 0).
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16> {
+    bf16x8 v;
+    __device__ __forceinline__ float operator[](int i) const { return (float)v[i]; }
+    __device__ __forceinline__ void load(const bf16 *p, int n)
+    {
+        if (n == 8) {
+            v = *reinterpret_cast<const bf16x8_any *>(p);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : (bf16)0.f;
+    }
+    __device__ static __forceinline__ void store(bf16 *p, int n, const float *x)
+    {
+        if (n == 8) {
+            bf16x8 f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = (bf16)x[i];
+            *reinterpret_cast<bf16x8_any *>(p) = f;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = (bf16)x[i];
+    }
+};
+template <> struct Raw8<float> {
+    f32x4 a, b;
+    __device__ __forceinline__ float operator[](int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
+    __device__ __forceinline__ void load(const float *p, int n)
+    {
+        if (n == 8) {
+            a = *reinterpret_cast<const f32x4_any *>(p);
+            b = *reinterpret_cast<const f32x4_any *>(p + 4);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = i < n ? p[i] : 0.f;
+            b[i] = i + 4 < n ? p[i + 4] : 0.f;
+        }
+    }
+    __device__ static __forceinline__ void store(float *p, int n, const float *x)
+    {
+        if (n == 8) {
+            const f32x4 lo = {x[0], x[1], x[2], x[3]}, hi = {x[4], x[5], x[6], x[7]};
+            *reinterpret_cast<f32x4_any *>(p) = lo;
+            *reinterpret_cast<f32x4_any *>(p + 4) = hi;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = x[i];
+    }
+};
+
+__device__ __forceinline__ int act_groups(int C) { return (C + ACT_GROUP - 1) / ACT_GROUP; }
+
+// Channels [c, c + n) of a row of codes, as values; scales: the row's.
+__device__ __forceinline__ void load_codes(const int8_t *row, const float *scales, int c, int n, float *x)
+{
+    const float s = n > 0 ? scales[c / ACT_GROUP] : 0.f;
+    if (n == 8) {
+        const i8x8_any q = *reinterpret_cast<const i8x8_any *>(row + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (float)q[i] * s;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)row[c + i] * s : 0.f;
+}
+
+// Channels [c, c + n) of row r as float32, whatever they are stored as.
+template <typename T> __device__ __forceinline__ void load_row8(const Rows &m, size_t r, int C, int c, int n, float *x)
+{
+    if (m.scales) {
+        load_codes((const int8_t *)m.p + r * m.stride, m.scales + r * act_groups(C), c, n, x);
+        return;
+    }
+    Raw8<T> raw;
+    raw.load((const T *)m.p + r * m.stride + c, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = raw[i];
+}
+
+__device__ __forceinline__ void load_f8(const float *p, int n, float *x)
+{
+    Raw8<float> raw;
+    raw.load(p, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = raw[i];
+}
+
+// The largest of |x| over the 16 lanes that hold a group (a DPP row), as bits:
+// integers order non-negative floats, and infinities and NaN above them.  All 64 lanes are active.
+template <int CTRL> __device__ __forceinline__ uint32_t dpp_umax(uint32_t v)
+{
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+    return o > v ? o : v;
+}
+__device__ __forceinline__ uint32_t group_amax(const float *x)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, x[i]) & 0x7fffffffu;
+        m = b > m ? b : m;
+    }
+    m = dpp_umax<0xB1>(m);   // quad_perm [1, 0, 3, 2]
+    m = dpp_umax<0x4E>(m);   // quad_perm [2, 3, 0, 1]
+    m = dpp_umax<0x141>(m);  // row_half_mirror
+    return dpp_umax<0x140>(m);
+}
+
+// Packs the lane's channels [c, c + n) of row r; x holds 0 from n on.  A group
+// with an infinity or a NaN stands for NaN throughout (its scale is NaN); one whose largest value
+// is below 2^-118 (127 over it would overflow) stands for zeros.
+__device__ __forceinline__ void store_codes(const PackedOut &out, size_t r, int C, int c, int n, const float *x)
+{
+    const uint32_t bits = group_amax(x);
+    const float amax = __builtin_bit_cast(float, bits);
+    const bool finite = bits < 0x7f800000u, some = bits >= 0x04800000u;
+    const float inv = finite && some ? 127.0f / amax : 0.f;
+    if (n == 0) return;
+    if (c % ACT_GROUP == 0)
+        out.scales[r * act_groups(C) + c / ACT_GROUP] =
+            !finite ? __builtin_bit_cast(float, 0x7fc00000u) : some ? amax * (1.0f / 127.0f) : 0.f;
+    int8_t q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = finite ? (int8_t)(int)__builtin_rintf(x[i] * inv) : (int8_t)0;
+    int8_t *p = out.codes + r * C + c;
+    if (n == 8) {
+        i8x8_any v;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = q[i];
+        *reinterpret_cast<i8x8_any *>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = q[i];
+}
+
+// 1 / sqrt(mean of squares + eps): as rsq_norm, but a NaN stays one.
+__device__ __forceinline__ float rstd_of(float x)
+{
+    return __builtin_amdgcn_rsqf(x < 1.17549435e-38f ? 1.17549435e-38f : x);
+}
+
+struct Sigmoid {
+    float s, r;                       // Sigmoid(x) and 1 - Sigmoid(x), each to a few units in its own last place
+};
+__device__ __forceinline__ Sigmoid sigmoid2(float x)
+{
+    // below 2^-120 it counts as 0, so that neither part overflows
+    const float y = x * -LOG2E;
+    const bool shut = y > 120.f;
+    const float e = __builtin_amdgcn_exp2f(shut ? 120.f : y);
+    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    return {shut ? 0.f : s, e * s};
+}
+
+// A decay e^g (g <= 0; above 0 it counts as 0), kept as one number w: e^g - 1
+// where that is negative and g > -0.1 (to its own last place: the series to g^5 leaves g^5 / 720 < 2^-25), else e^g, which
+// is not negative.  A state that fades over 10^4 tokens would carry 10^4 times the rounding of e^g itself.
+__device__ __forceinline__ float decay_code(float g)
+{
+    const float x = g > 0.f ? 0.f : g;
+    const float m = x * __builtin_fmaf(x, __builtin_fmaf(x, __builtin_fmaf(x, __builtin_fmaf(x, 1.f / 120, 1.f / 24), 1.f / 6), 0.5f), 1.f);
+    return x > -0.1f && m < 0.f ? m : __builtin_amdgcn_exp2f(x * LOG2E);
+}
+// e^g h + x.  An infinite h may give NaN (inf - 0.05 inf).
+__device__ __forceinline__ float decay_apply(float w, float h, float x)
+{
+    const float b = w < 0.f ? h : 0.f;
+    return b + __builtin_fmaf(w, h, x);
+}
+__device__ __forceinline__ float decay_times(float w, float h)
+{
+    const float b = w < 0.f ? h : 0.f;
+    return __builtin_fmaf(w, h, b);
+}
+// 1 - e^g
+__device__ __forceinline__ float decay_rest(float w) { return w < 0.f ? -w : 1.f - w; }
+
+}  // namespace kda

@@ -488,6 +488,228 @@ KDA_API kda_status_t kda_cache_compact(const kda_cache_pool_t *pools, int32_t n_
                                        int32_t rows, int32_t per_row, int32_t *refcount, int32_t *moved_to,
                                        int32_t *moves, int32_t *counts, void *stream);
 
+/*
+ * The gated scan, the norms around a block, activations in 8 bits.  What a
+ * recurrent block needs next to the mixing layers above, in training and in
+ * serving.  The conventions at the top of this header hold, with these differences:
+ *   - Arrays need no more than their elements' alignment, and rows any length.
+ *     Where a stride is named, it is the number of elements from one row to the
+ *     next (at least the row), so that rows may be parts of wider ones; all
+ *     other arrays are dense.
+ *   - Arithmetic, states and sums are float32 or more; each result is rounded
+ *     once to its type.
+ *   - Outputs must not overlap inputs or one another, but where it is said.
+ *
+ * Activations in 8 bits: a row of D values is D int8 codes and one float32
+ * scale for each KDA_ACT_GROUP consecutive values (the last group may be shorter).
+ * In float32 steps, with amax the group's largest |x|:
+ *   scale = amax * (1 / 127),   code = rint(x * (127 / amax)),   value = code * scale,
+ * ties to the even code.  A group with a NaN or an infinity has a NaN for its scale
+ * (all its values are NaN); one whose amax is below 2^-118 stands for zeros.  A value is
+ * off by amax / 254 at most (and the roundings).  codes : [R, D], scales : [R, ceil(D / KDA_ACT_GROUP)], dense.  Calls that read
+ * activations take codes in place of elements where `..._scales` is given.
+ */
+#define KDA_ACT_GROUP 128
+
+/* Packs R rows of D values (x_stride elements apart) of type dtype; unpacks to dense rows. */
+KDA_API kda_status_t kda_act_pack(int32_t dtype, const void *x, int64_t x_stride, int64_t R, int32_t D, int8_t *codes,
+                                  float *scales, void *stream);
+KDA_API kda_status_t kda_act_unpack(int32_t dtype, const int8_t *codes, const float *scales, int64_t R, int32_t D, void *x,
+                                    void *stream);
+
+/*
+ * Gated scan: per channel c of C, over the tokens of each sequence,
+ *   h_t = a_t h_{t-1} + m_t x_t,   a_t = exp(g_t),
+ *   m_t = 1, or 1 - a_t when complement is set.
+ *   x, h : [B, T, C] of dtype      g : [B, T, C] of g_dtype (dtype or KDA_F32)
+ * Decays: with A_log NULL g holds log-decays (above 0 they count as 0; -inf
+ * forgets the state); with A_log [C] float32 it holds logits z, and eq. (5) is applied,
+ * g_t = g_min Sigmoid(exp(A_log) z_t), g_min finite and below 0.
+ * cu_seqlens / N, initial_state, final_state as for kda_chunk_fwd, with states
+ * [N, C] float32 (final_state may alias initial_state).  Rows of h outside
+ * every sequence are left as they were.
+ * h_codes, h_scales : h, as returned, in 8 bits as well, or NULL.  (Rows outside every sequence are left as they were.)
+ * States are accurate to float32 however slowly they fade: e^g - 1 is kept to
+ * its own last place where e^g is near 1.  A NaN or infinity reaches the tokens behind it in its own
+ * channel and sequence only; an infinite state may turn into NaN.
+ */
+typedef struct {
+    int32_t B, T, C;
+    int32_t dtype, g_dtype;        /* kda_dtype_t */
+    const void *x;
+    int64_t x_stride;
+    const void *g;
+    int64_t g_stride;
+    const float *A_log;
+    float g_min;
+    int32_t complement;
+    const int32_t *cu_seqlens;
+    int32_t N;
+    const float *initial_state;
+    void *h;
+    float *final_state;
+    int8_t *h_codes;
+    float *h_scales;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_gated_scan_fwd_args_t;
+
+KDA_API kda_status_t kda_gated_scan_fwd_workspace_size(const kda_gated_scan_fwd_args_t *args, size_t *bytes);
+KDA_API kda_status_t kda_gated_scan_fwd(const kda_gated_scan_fwd_args_t *args, void *stream);
+
+/*
+ * Gradients of kda_gated_scan_fwd, given d_h (gradient of h, [B, T, C] of dtype)
+ * and d_final_state ([N, C] float32, or NULL for zeros).  With
+ * D_t = d_h_t + e_{t+1} (d_final_state at a sequence's end) and e_t = a_t D_t:
+ *   dx_t = m_t D_t   (dtype, dx_stride)
+ *   dg_t = e_t (h_{t-1} - [complement] x_t), through the gate to the logits with A_log
+ *          (g_dtype, dg_stride), or dg NULL if not wanted.  A g above 0 gets the gradient of
+ *          the 0 it counts as.
+ *   dA_log : [C] float32, the sum of z_t dz_t over all tokens, or NULL; needs dg
+ *   d_initial_state : [N, C] float32 e of the first token, or NULL; it may alias d_final_state
+ * h is what the forward returned, elements or (h_scales) 8-bit codes; dg uses these
+ * values, and initial_state in front of them.  h is read only with dg, x only with dg and
+ * complement.  Rows of dx and dg outside every sequence are left as they were.
+ */
+typedef struct {
+    int32_t B, T, C;
+    int32_t dtype, g_dtype;
+    const void *x;
+    int64_t x_stride;
+    const float *x_scales;
+    const void *g;
+    int64_t g_stride;
+    const float *A_log;
+    float g_min;
+    int32_t complement;
+    const int32_t *cu_seqlens;
+    int32_t N;
+    const float *initial_state;
+    const void *h;
+    const float *h_scales;
+    const void *d_h;
+    const float *d_final_state;
+    void *dx;
+    int64_t dx_stride;
+    void *dg;
+    int64_t dg_stride;
+    float *dA_log;
+    float *d_initial_state;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_gated_scan_bwd_args_t;
+
+KDA_API kda_status_t kda_gated_scan_bwd_workspace_size(const kda_gated_scan_bwd_args_t *args, size_t *bytes);
+KDA_API kda_status_t kda_gated_scan_bwd(const kda_gated_scan_bwd_args_t *args, void *stream);
+
+/*
+ * One token for each of N sequences:  x, h : [N, C]   g : [N, C]
+ *   state, new_state : [n_slots, C] float32 (the same pointer, or not overlapping).
+ * slots, empty places and slots that several rows name as for kda_linear_recurrent_step.
+ */
+typedef struct {
+    int32_t N, C;
+    int32_t dtype, g_dtype;
+    const void *x;
+    int64_t x_stride;
+    const void *g;
+    int64_t g_stride;
+    const float *A_log;
+    float g_min;
+    int32_t complement;
+    const int32_t *slots;
+    int32_t n_slots;
+    const float *state;
+    float *new_state;
+    void *h;
+} kda_gated_scan_step_args_t;
+
+KDA_API kda_status_t kda_gated_scan_step(const kda_gated_scan_step_args_t *args, void *stream);
+
+/*
+ * What stands between two blocks: the norm after a block's output y, its gate,
+ * the residual stream x, and the norm before the next block.  Per row of D:
+ *   u  = post_weight * y / rms(y)            (post_weight NULL: u = y)
+ *   x' = x + scale * res_scale * Sigmoid(gate) * u   (res_scale, gate NULL: 1)
+ *   n  = pre_weight * x' / rms(x')           (pre_weight NULL: no n), of x' as it is returned
+ * with rms(v) = sqrt(mean(v^2) + eps) (a mean of squares plus eps below 2^-126 counts as 2^-126).
+ * y NULL: there is no block before, x' is x and is not written.
+ *   x, x_out : [R, D] of x_dtype (dtype or KDA_F32: a float32 residual stream); x_out may be x
+ *   y, gate  : [R, D] of dtype, with strides      n : [R, D] of dtype
+ *   post_weight, res_scale, pre_weight : [D] float32
+ *   x_codes / y_codes / gate_codes (and scales): x', y and the gate in 8 bits as well, or NULL
+ * 1 <= D <= 16384.  Squares are summed in float32, so values above 1e18 overflow.
+ */
+typedef struct {
+    int32_t R, D;
+    int32_t dtype, x_dtype;
+    const void *x;
+    const void *y;
+    int64_t y_stride;
+    const void *gate;
+    int64_t gate_stride;
+    const float *post_weight;
+    const float *res_scale;
+    const float *pre_weight;
+    float scale;
+    float eps;
+    void *x_out;
+    void *n;
+    int8_t *x_codes;
+    float *x_scales;
+    int8_t *y_codes;
+    float *y_scales;
+    int8_t *gate_codes;
+    float *gate_scales;
+} kda_block_norm_fwd_args_t;
+
+KDA_API kda_status_t kda_block_norm_fwd(const kda_block_norm_fwd_args_t *args, void *stream);
+
+/*
+ * Gradients of kda_block_norm_fwd from x' (as returned), y and the gate, each as elements
+ * or (scales given) as 8-bit codes, given d_x_new (gradient of x', x_dtype) and
+ * d_n (gradient of n, dtype), one of which may be NULL (zeros).  x^ = x' / rms(x'), y^ = y / rms(y):
+ *   G  = d_x_new + (pre_weight d_n - x^ mean(pre_weight d_n x^)) / rms(x')
+ *   dx = G (x_dtype; it may be d_x_new)          r = Sigmoid(gate) u
+ *   d_res_scale = sum scale G r                  dr = scale res_scale G
+ *   dgate = dr u S (1 - S) (dtype, dgate_stride) du = dr S
+ *   d_post_weight = sum du y^                    d_pre_weight = sum d_n x^   (sums over the rows, [D] float32, or NULL)
+ *   dy = (post_weight du - y^ mean(post_weight du y^)) / rms(y), or du   (dtype, dy_stride)
+ * x_new is read only with d_n.  Results do not depend on the order in which workgroups run.
+ */
+typedef struct {
+    int32_t R, D;
+    int32_t dtype, x_dtype;
+    const void *x_new;
+    const float *x_scales;
+    const void *y;
+    int64_t y_stride;
+    const float *y_scales;
+    const void *gate;
+    int64_t gate_stride;
+    const float *gate_scales;
+    const float *post_weight;
+    const float *res_scale;
+    const float *pre_weight;
+    float scale;
+    float eps;
+    const void *d_x_new;
+    const void *d_n;
+    void *dx;
+    void *dy;
+    int64_t dy_stride;
+    void *dgate;
+    int64_t dgate_stride;
+    float *d_post_weight;
+    float *d_res_scale;
+    float *d_pre_weight;
+    void *workspace;
+    size_t workspace_bytes;
+} kda_block_norm_bwd_args_t;
+
+KDA_API kda_status_t kda_block_norm_bwd_workspace_size(const kda_block_norm_bwd_args_t *args, size_t *bytes);
+KDA_API kda_status_t kda_block_norm_bwd(const kda_block_norm_bwd_args_t *args, void *stream);
+
 /* Static description of a status code. */
 KDA_API const char *kda_status_string(kda_status_t status);
 
