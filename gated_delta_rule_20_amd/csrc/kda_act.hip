@@ -19,7 +19,7 @@ template <typename T> __global__ __launch_bounds__(256) void act_pack_kernel(Row
     raw.load((const T *)x.p + r * x.stride + c, n);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = raw[i];
-    store_codes(out, r, D, c, n, v);
+    store_codes<LANE_CH>(out, r, D, c, n, v);
 }
 
 template <typename T> __global__ __launch_bounds__(256) void act_unpack_kernel(Rows x, long long groups, int D, T *out)

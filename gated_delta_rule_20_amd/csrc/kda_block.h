@@ -24,6 +24,18 @@ struct PackedOut {
     float *scales;
 };
 
+// A workgroup of a scan takes SCAN_ROWS rows (a segment) of SCAN_CHANNELS channels.
+constexpr int SCAN_ROWS = 64, SCAN_CHANNELS = 128;
+
+// Hand-over between segments, cleared at the start of a call: [segments, C] pairs of log-decay and state, every
+// `group` segments the state behind them [groups, C], the next ticket, whether a wait was given up.
+struct ScanChain {
+    uint64_t *part, *whole;
+    uint32_t *ticket, *gave_up;
+    size_t words;                     // of 8 bytes, all of the above
+    int segments, group;
+};
+
 struct ScanParams {
     int rows, T, C;                   // rows of all sequences; tokens per sequence when cu is null
     const int32_t *cu;                // [N + 1] or null
@@ -44,7 +56,10 @@ struct ScanParams {
     void *dx, *dg;
     int64_t dx_stride, dg_stride;
     float *dA, *dh0;
-    float *dA_part;                   // [parts, C]
+    float *dA_part;                   // [segments, C]
+    // more than one segment: the call's tickets and what the segments hand on
+    ScanChain chain;
+    float *state_copy;                // of the entering states, where the resulting ones overwrite them, or null
 };
 
 struct ScanStepParams {

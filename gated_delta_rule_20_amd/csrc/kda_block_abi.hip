@@ -107,7 +107,10 @@ template <typename A> kda_status_t plan_scan(const A *a, kda::ScanParams *p)
     p->N = a->cu_seqlens ? a->N : a->B;
     const long long rows = (long long)a->B * a->T;
     if (rows > 0x7fffff00LL) return fail(KDA_ERROR_NOT_SUPPORTED, "too many tokens for 32-bit indices");
-    if (!launchable((long long)p->N * ((a->C + 63) / 64), 64)) return fail(KDA_ERROR_NOT_SUPPORTED, "N * C too large for one call");
+    // one workgroup for each segment of rows and of channels
+    const long long wide = (a->C + kda::SCAN_CHANNELS - 1) / kda::SCAN_CHANNELS;
+    if (!launchable((rows / kda::SCAN_ROWS + 1) * wide, 256) || p->N > (1 << 28))
+        return fail(KDA_ERROR_NOT_SUPPORTED, "rows * C too large for one call");
     p->rows = (int)rows;
     p->T = a->T;
     p->C = a->C;
@@ -124,16 +127,49 @@ template <typename A> kda_status_t plan_scan(const A *a, kda::ScanParams *p)
     return check_array(a->initial_state, 4, "initial_state");
 }
 
-size_t plan_scan_fwd(const kda_gated_scan_fwd_args_t *, kda::ScanParams *) { return 0; }
+struct Carver {
+    size_t used = 0;
+    char *base;
+    explicit Carver(void *b) : base((char *)b) {}
+    void *take(size_t bytes)
+    {
+        const size_t at = used;
+        used += (bytes + 255) / 256 * 256;
+        return base ? base + at : nullptr;
+    }
+};
+
+// The hand-over between segments, and the entering states' copy where the resulting ones overwrite them.
+void plan_chain(Carver &c, const float *from, const float *to, kda::ScanParams *p)
+{
+    kda::ScanChain &k = p->chain;
+    const size_t C = (size_t)p->C, states = (size_t)p->N * C;
+    k.segments = p->rows > 0 ? (p->rows - 1) / kda::SCAN_ROWS + 1 : 1;
+    k.group = 8;
+    if (k.segments > 1) {
+        const size_t whole = (size_t)((k.segments - 1) / k.group + 1);
+        k.words = ((size_t)k.segments + whole) * C + 1;
+        k.part = (uint64_t *)c.take(8 * k.words);
+        k.whole = k.part + (size_t)k.segments * C;
+        k.ticket = (uint32_t *)(k.whole + whole * C);
+        k.gave_up = k.ticket + 1;
+    }
+    if (overlap(from, 4 * states, to, 4 * states)) p->state_copy = (float *)c.take(4 * states);
+}
+
+size_t plan_scan_fwd(const kda_gated_scan_fwd_args_t *a, kda::ScanParams *p)
+{
+    Carver c(a->workspace);
+    plan_chain(c, a->initial_state, a->final_state, p);
+    return c.used;
+}
 
 size_t plan_scan_bwd(const kda_gated_scan_bwd_args_t *a, kda::ScanParams *p)
 {
-    size_t need = 0;
-    if (a->dA_log) {
-        p->dA_part = (float *)a->workspace;
-        need += sizeof(float) * (size_t)p->N * p->C;
-    }
-    return need;
+    Carver c(a->workspace);
+    plan_chain(c, a->d_final_state, a->d_initial_state, p);
+    if (a->dA_log) p->dA_part = (float *)c.take(sizeof(float) * (size_t)p->chain.segments * p->C);
+    return c.used;
 }
 
 // ---- block norms -----------------------------------------------------------------

@@ -74,6 +74,65 @@ template <> struct Raw8<float> {
     }
 };
 
+// The same for four channels.
+typedef __bf16 bf16x4_any __attribute__((ext_vector_type(4), aligned(2)));
+template <typename T> struct Raw4;
+template <> struct Raw4<bf16> {
+    bf16x4 v;
+    __device__ __forceinline__ float operator[](int i) const { return (float)v[i]; }
+    __device__ __forceinline__ void load(const bf16 *p, int n)
+    {
+        if (n == 4) {
+            v = *reinterpret_cast<const bf16x4_any *>(p);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < n ? p[i] : (bf16)0.f;
+    }
+    __device__ static __forceinline__ void store(bf16 *p, int n, const float *x)
+    {
+        if (n == 4) {
+            const bf16x4 f = {(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
+            *reinterpret_cast<bf16x4_any *>(p) = f;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = (bf16)x[i];
+    }
+};
+template <> struct Raw4<float> {
+    f32x4 v;
+    __device__ __forceinline__ float operator[](int i) const { return v[i]; }
+    __device__ __forceinline__ void load(const float *p, int n)
+    {
+        if (n == 4) {
+            v = *reinterpret_cast<const f32x4_any *>(p);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < n ? p[i] : 0.f;
+    }
+    __device__ static __forceinline__ void store(float *p, int n, const float *x)
+    {
+        if (n == 4) {
+            const f32x4 f = {x[0], x[1], x[2], x[3]};
+            *reinterpret_cast<f32x4_any *>(p) = f;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = x[i];
+    }
+};
+__device__ __forceinline__ void load_f4(const float *p, int n, float *x)
+{
+    Raw4<float> raw;
+    raw.load(p, n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = raw[i];
+}
+
 __device__ __forceinline__ int act_groups(int C) { return (C + ACT_GROUP - 1) / ACT_GROUP; }
 
 // Channels [c, c + n) of a row of codes, as values; scales: the row's.
@@ -111,33 +170,39 @@ __device__ __forceinline__ void load_f8(const float *p, int n, float *x)
     for (int i = 0; i < 8; ++i) x[i] = raw[i];
 }
 
-// The largest of |x| over the 16 lanes that hold a group (a DPP row), as bits:
-// integers order non-negative floats, and infinities and NaN above them.  All 64 lanes are active.
+// The largest of |x| over the 128 / CH lanes that hold a group (a DPP row, or two), as bits: integers order
+// non-negative floats, and infinities and NaN above them.  All 64 lanes are active.
 template <int CTRL> __device__ __forceinline__ uint32_t dpp_umax(uint32_t v)
 {
     const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
     return o > v ? o : v;
 }
-__device__ __forceinline__ uint32_t group_amax(const float *x)
+template <int CH> __device__ __forceinline__ uint32_t group_amax(const float *x)
 {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < CH; ++i) {
         const uint32_t b = __builtin_bit_cast(uint32_t, x[i]) & 0x7fffffffu;
         m = b > m ? b : m;
     }
     m = dpp_umax<0xB1>(m);   // quad_perm [1, 0, 3, 2]
     m = dpp_umax<0x4E>(m);   // quad_perm [2, 3, 0, 1]
     m = dpp_umax<0x141>(m);  // row_half_mirror
-    return dpp_umax<0x140>(m);
+    m = dpp_umax<0x140>(m);  // row_mirror
+    if (CH == 4) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_ds_swizzle((int)m, 0x401F);  // lane ^ 16
+        m = o > m ? o : m;
+    }
+    return m;
 }
 
 // Packs the lane's channels [c, c + n) of row r; x holds 0 from n on.  A group
 // with an infinity or a NaN stands for NaN throughout (its scale is NaN); one whose largest value
 // is below 2^-118 (127 over it would overflow) stands for zeros.
-__device__ __forceinline__ void store_codes(const PackedOut &out, size_t r, int C, int c, int n, const float *x)
+template <int CH> __device__ __forceinline__ void store_codes(const PackedOut &out, size_t r, int C, int c, int n, const float *x)
 {
-    const uint32_t bits = group_amax(x);
+    typedef int8_t codes_any __attribute__((ext_vector_type(CH), aligned(1)));
+    const uint32_t bits = group_amax<CH>(x);
     const float amax = __builtin_bit_cast(float, bits);
     const bool finite = bits < 0x7f800000u, some = bits >= 0x04800000u;
     const float inv = finite && some ? 127.0f / amax : 0.f;
@@ -145,19 +210,16 @@ __device__ __forceinline__ void store_codes(const PackedOut &out, size_t r, int 
     if (c % ACT_GROUP == 0)
         out.scales[r * act_groups(C) + c / ACT_GROUP] =
             !finite ? __builtin_bit_cast(float, 0x7fc00000u) : some ? amax * (1.0f / 127.0f) : 0.f;
-    int8_t q[8];
+    codes_any q;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = finite ? (int8_t)(int)__builtin_rintf(x[i] * inv) : (int8_t)0;
+    for (int i = 0; i < CH; ++i) q[i] = finite ? (int8_t)(int)__builtin_rintf(x[i] * inv) : (int8_t)0;
     int8_t *p = out.codes + r * C + c;
-    if (n == 8) {
-        i8x8_any v;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = q[i];
-        *reinterpret_cast<i8x8_any *>(p) = v;
+    if (n == CH) {
+        *reinterpret_cast<codes_any *>(p) = q;
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < CH; ++i)
         if (i < n) p[i] = q[i];
 }
 

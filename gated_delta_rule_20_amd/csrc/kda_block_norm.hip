@@ -53,7 +53,7 @@ __global__ __launch_bounds__(norm_threads(NW)) void norm_fwd_kernel(const NormPa
             for (int j = 0; j < NCH; ++j) {
                 const int c = (j * NT + t) * LANE_CH;
                 load_row8<T>(p.y, r, p.D, c, cnt[j], u[j]);
-                if (p.y8.codes) store_codes(p.y8, r, p.D, c, cnt[j], u[j]);
+                if (p.y8.codes) store_codes<LANE_CH>(p.y8, r, p.D, c, cnt[j], u[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) ss[0] += u[j][i] * u[j][i];
             }
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(norm_threads(NW)) void norm_fwd_kernel(const NormPa
                 }
                 if (p.gate.p) {
                     load_row8<T>(p.gate, r, p.D, c, cnt[j], w);
-                    if (p.gate8.codes) store_codes(p.gate8, r, p.D, c, cnt[j], w);
+                    if (p.gate8.codes) store_codes<LANE_CH>(p.gate8, r, p.D, c, cnt[j], w);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[j][i] *= sigmoid2(w[i]).s;
                 }
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(norm_threads(NW)) void norm_fwd_kernel(const NormPa
                 for (int i = 0; i < 8; ++i) x[j][i] = to_f<X>(from_f<X>(x[j][i] + p.scale * u[j][i]));
                 if (cnt[j] > 0) Raw8<X>::store((X *)p.x_out + r * p.D + c, cnt[j], x[j]);
             }
-            if (p.x8.codes) store_codes(p.x8, r, p.D, c, cnt[j], x[j]);
+            if (p.x8.codes) store_codes<LANE_CH>(p.x8, r, p.D, c, cnt[j], x[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss[0] += x[j][i] * x[j][i];
         }
