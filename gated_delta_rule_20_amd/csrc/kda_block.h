@@ -27,13 +27,17 @@ struct PackedOut {
 // A workgroup of a scan takes SCAN_ROWS rows (a segment) of SCAN_CHANNELS channels.
 constexpr int SCAN_ROWS = 64, SCAN_CHANNELS = 128;
 
-// Hand-over between segments, cleared at the start of a call: [segments, C] pairs of log-decay and state, every
-// `group` segments the state behind them [groups, C], the next ticket, whether a wait was given up.
+// Segments that join their pairs, and blocks of them that join theirs; counters that lie 128 bytes apart.
+constexpr int SCAN_BLOCK = 8, SCAN_TICKET_STEP = 32;
+
+// Hand-over between segments, cleared at the start of a call: pairs of decay and state for each segment and each
+// SCAN_BLOCK segments [.., C], the state behind every SCAN_BLOCK^2 [.., C]; the tickets of each SCAN_CHANNELS channels;
+// whether a wait was given up.
 struct ScanChain {
-    uint64_t *part, *whole;
-    uint32_t *ticket, *gave_up;
-    size_t words;                     // of 8 bytes, all of the above
-    int segments, group;
+    uint64_t *part, *blocks, *whole;
+    uint32_t *tickets, *gave_up;
+    size_t words, counters;           // pairs, all three kinds; counters of 4 bytes, the flag among them
+    int segments;
 };
 
 struct ScanParams {

@@ -49,8 +49,8 @@ kda_status_t check_given(const void *p, int bytes, const char *name)
 
 kda_status_t check_stride(int64_t stride, int C, const char *name)
 {
-    if (stride < C || stride > ((int64_t)1 << 40))
-        return fail(KDA_ERROR_INVALID_VALUE, "%s=%lld: must be %d (the row) to 2^40", name, (long long)stride, C);
+    if (stride < C || stride > (1 << 24))
+        return fail(KDA_ERROR_INVALID_VALUE, "%s=%lld: must be %d (the row) to 2^24", name, (long long)stride, C);
     return KDA_SUCCESS;
 }
 
@@ -145,14 +145,16 @@ void plan_chain(Carver &c, const float *from, const float *to, kda::ScanParams *
     kda::ScanChain &k = p->chain;
     const size_t C = (size_t)p->C, states = (size_t)p->N * C;
     k.segments = p->rows > 0 ? (p->rows - 1) / kda::SCAN_ROWS + 1 : 1;
-    k.group = 8;
     if (k.segments > 1) {
-        const size_t whole = (size_t)((k.segments - 1) / k.group + 1);
-        k.words = ((size_t)k.segments + whole) * C + 1;
+        const size_t parts = (size_t)k.segments * C, blocks = (size_t)(k.segments / kda::SCAN_BLOCK) * C;
+        const size_t whole = (size_t)(k.segments / (kda::SCAN_BLOCK * kda::SCAN_BLOCK)) * C;
+        k.words = parts + blocks + whole;
+        k.counters = (C + kda::SCAN_CHANNELS - 1) / kda::SCAN_CHANNELS * kda::SCAN_TICKET_STEP + 1;
         k.part = (uint64_t *)c.take(8 * k.words);
-        k.whole = k.part + (size_t)k.segments * C;
-        k.ticket = (uint32_t *)(k.whole + whole * C);
-        k.gave_up = k.ticket + 1;
+        k.blocks = k.part + parts;
+        k.whole = k.blocks + blocks;
+        k.tickets = (uint32_t *)c.take(4 * k.counters);
+        k.gave_up = k.tickets + k.counters - 1;
     }
     if (overlap(from, 4 * states, to, 4 * states)) p->state_copy = (float *)c.take(4 * states);
 }

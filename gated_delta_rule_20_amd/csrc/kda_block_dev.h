@@ -242,27 +242,41 @@ __device__ __forceinline__ Sigmoid sigmoid2(float x)
     return {shut ? 0.f : s, e * s};
 }
 
-// A decay e^g (g <= 0; above 0 it counts as 0), kept as one number w: e^g - 1
-// where that is negative and g > -0.1 (to its own last place: the series to g^5 leaves g^5 / 720 < 2^-25), else e^g, which
-// is not negative.  A state that fades over 10^4 tokens would carry 10^4 times the rounding of e^g itself.
-__device__ __forceinline__ float decay_code(float g)
+// A decay e^x (x <= 0, and -0 for 0) kept as one number w: e^x - 1, its sign set, where x > -0.1 (to its own last
+// place: the series to x^5 leaves x^5 / 720 < 2^-25); else e^x, its sign clear.  A state that fades over
+// 10^4 tokens would carry 10^4 times the rounding of e^x itself.
+struct Decay {
+    float w;
+    bool near;
+};
+__device__ __forceinline__ Decay decay_of(float x)
 {
-    const float x = g > 0.f ? 0.f : g;
     const float m = x * __builtin_fmaf(x, __builtin_fmaf(x, __builtin_fmaf(x, __builtin_fmaf(x, 1.f / 120, 1.f / 24), 1.f / 6), 0.5f), 1.f);
-    return x > -0.1f && m < 0.f ? m : __builtin_amdgcn_exp2f(x * LOG2E);
+    const bool near = x > -0.1f;
+    return {near ? m : __builtin_amdgcn_exp2f(x * LOG2E), near};
 }
-// e^g h + x.  An infinite h may give NaN (inf - 0.05 inf).
-__device__ __forceinline__ float decay_apply(float w, float h, float x)
+// A log-decay above 0 counts as 0; NaN passes.
+__device__ __forceinline__ float not_above_0(float g) { return g >= 0.f ? -0.f : g; }
+__device__ __forceinline__ Decay decay_held(float w) { return {w, __builtin_bit_cast(int, w) < 0}; }
+// e^x h + b.  An infinite h may give NaN (inf - 0.05 inf).
+__device__ __forceinline__ float decay_apply(Decay d, float h, float b) { return (d.near ? h : 0.f) + __builtin_fmaf(d.w, h, b); }
+__device__ __forceinline__ float decay_times(Decay d, float h) { return __builtin_fmaf(d.w, h, d.near ? h : 0.f); }
+// The product of two decays.
+__device__ __forceinline__ Decay decay_product(Decay a, Decay b)
 {
-    const float b = w < 0.f ? h : 0.f;
-    return b + __builtin_fmaf(w, h, x);
+    const float t = __builtin_fmaf(a.w, b.w, (b.near ? a.w : 0.f) + (a.near ? b.w : 0.f));
+    // near 1 it stays e^x - 1 as long as that keeps its last place
+    const bool near = a.near && b.near;
+    return near && t < -0.5f ? Decay{1.f + t, false} : Decay{near ? -__builtin_fabsf(t) : t, near};  // (-0 for 1)
 }
-__device__ __forceinline__ float decay_times(float w, float h)
-{
-    const float b = w < 0.f ? h : 0.f;
-    return __builtin_fmaf(w, h, b);
-}
-// 1 - e^g
-__device__ __forceinline__ float decay_rest(float w) { return w < 0.f ? -w : 1.f - w; }
+// A token's value times 1 - e^x with complement, else as it is.
+struct Share {
+    bool complement;
+    __device__ __forceinline__ explicit Share(bool c) : complement(c) {}
+    __device__ __forceinline__ float operator()(Decay d, float x) const
+    {
+        return complement ? __builtin_fmaf(-d.w, x, d.near ? 0.f : x) : x;
+    }
+};
 
 }  // namespace kda

@@ -26,19 +26,22 @@ __device__ __forceinline__ void sequence_of(const ScanParams &p, int s, int *lo,
 // runs over its rows again from registers: x and g are read once, h written
 // once.
 //
-// Segments of a call's packed rows are joined in one pass.  Workgroups take
-// tickets (so a segment's predecessors run or have run already), publish what
-// their rows do to a state before waiting for anything, and wait for the pairs of the segments before
-// them, back to the nearest one whose last row's state is published whole
-// (every `group`-th).  The order in which pairs are joined is fixed, so results do
-// not depend on timing.  Where sequences begin, the state is replaced, and nothing behind it is
-// looked at.
+// Segments of a call's packed rows are joined in the same pass.  Workgroups take
+// tickets of their channels (so a segment's predecessors run or have run already) and publish what
+// their rows do to a state, a pair (product of decays, state from zero), before waiting for anything.  The
+// last segment of every 8 joins these pairs and publishes the block's; the last of every 64 publishes the state behind it.  So
+// a segment waits for at most 7 pairs of its block, 7 of blocks and one state, and what has to pass from one to the next is one
+// state every 4096 rows (with one in every 512, as pairs of segments alone allow, 131072 rows x 2048 took 556 us).  The order in which pairs
+// are joined is fixed, so results do not depend on timing.  Where sequences begin, the state is replaced, and what
+// lies before is not waited for.
 
 constexpr int CH = 4, LANES = SCAN_CHANNELS / CH;           // channels a lane; lanes of a row
 constexpr int RUN = 8, RUNS = SCAN_ROWS / RUN;
 static_assert(LANES * RUNS == 256, "a workgroup holds a segment");
-constexpr uint32_t EMPTY = 0xffffffffu;                     // no log-decay has these bits
-constexpr float CUT = 1.f;                                  // in place of a log-decay: a sequence began among the rows
+constexpr uint32_t EMPTY = 0xffffffffu;                     // no decay has these bits
+constexpr float CUT = 2.f;                                  // in place of a decay: a sequence began among the rows
+constexpr int BLOCK = SCAN_BLOCK;
+constexpr int TICKET_STEP = SCAN_TICKET_STEP;
 constexpr int SPINS = 1 << 20;                              // about a second
 
 struct Marks {
@@ -46,14 +49,35 @@ struct Marks {
     int any;
 };
 
+// What a thread needs of the offsets, loaded ahead of the segment's values: memory answers in order.
+struct Offsets {
+    int lo, a, b, begin, end;                               // rows [a, b) of sequence lo + thread; of all sequences
+    __device__ __forceinline__ Offsets(const ScanParams &p, int r0)
+    {
+        lo = a = b = begin = 0;
+        end = p.rows;
+        if (!p.cu) return;
+        // of a long list, from the last sequence that begins before these rows
+        for (int hi = p.N; hi - lo > 1024;) {
+            const int mid = (lo + hi) / 2;
+            if (p.cu[mid] < r0) lo = mid; else hi = mid;
+        }
+        if (lo + (int)threadIdx.x < p.N) sequence_of(p, lo + threadIdx.x, &a, &b);
+        begin = min(max(p.cu[0], 0), p.rows);
+        end = min(max(p.cu[p.N], 0), p.rows);
+    }
+};
+
 // Notes where sequences begin and end among rows [r0, r0 + SCAN_ROWS).  Sequences without rows that fall here (into
 // the last segment: or behind it) get their resulting state at once, for channels [c0, c0 + SCAN_CHANNELS).
-__device__ __forceinline__ void mark_rows(const ScanParams &p, int r0, bool tail, Marks &m, const float *from, float *to, int c0)
+__device__ __forceinline__ void mark_rows(const ScanParams &p, const Offsets &o, int r0, bool tail, Marks &m, const float *from,
+                                          float *to, int c0)
 {
     const int t = threadIdx.x;
     if (t < SCAN_ROWS) m.first[t] = m.last[t] = -1;
     if (t == 0) m.any = 0;
     lds_barrier();
+    if (!p.cu && p.T > 0 && r0 % p.T != 0 && r0 % p.T + SCAN_ROWS < p.T) return;   // inside a sequence
     const auto pass_on = [&](int s) {
         for (int c = c0; c < min(p.C, c0 + SCAN_CHANNELS); ++c) to[(size_t)s * p.C + c] = from ? from[(size_t)s * p.C + c] : 0.f;
     };
@@ -68,15 +92,9 @@ __device__ __forceinline__ void mark_rows(const ScanParams &p, int r0, bool tail
         if (p.T == 0 && to)
             for (int s = t; s < p.N; s += 256) pass_on(s);
     } else {
-        // of a long list, from the last sequence that begins before these rows
-        int lo = 0;
-        for (int hi = p.N; hi - lo > 1024;) {
-            const int mid = (lo + hi) / 2;
-            if (p.cu[mid] < r0) lo = mid; else hi = mid;
-        }
-        for (int s = lo + t; s < p.N; s += 256) {
-            int a, b;
-            sequence_of(p, s, &a, &b);
+        int a = o.a, b = o.b;
+        for (int s = o.lo + t; s < p.N; s += 256) {
+            if (s != o.lo + t) sequence_of(p, s, &a, &b);
             if (a >= r0 + SCAN_ROWS && !tail) break;
             if (b > a) {
                 if (a >= r0 && a < r0 + SCAN_ROWS) m.first[a - r0] = s, any = true;
@@ -99,25 +117,21 @@ __device__ __forceinline__ unsigned run_marks(const int *mark, int run)
     return bits;
 }
 
-// Bit i: row r0 + run * RUN + i belongs to a sequence.
-__device__ __forceinline__ unsigned run_rows(const ScanParams &p, int r)
+// Bit i: row r + i belongs to a sequence.
+__device__ __forceinline__ unsigned run_rows(const Offsets &o, int r)
 {
-    int lo = 0, hi = p.rows;
-    if (p.cu) {
-        lo = min(max(p.cu[0], 0), p.rows);
-        hi = min(max(p.cu[p.N], 0), p.rows);
-    }
-    const int a = min(max(lo - r, 0), RUN), b = min(max(hi - r, 0), RUN);
+    const int a = min(max(o.begin - r, 0), RUN), b = min(max(o.end - r, 0), RUN);
     return (0xffu >> (8 - b)) & (0xffu << a) & 0xffu;
 }
 
-__device__ __forceinline__ uint64_t pair_of(float g, float h)
+__device__ __forceinline__ uint64_t pair_of(float w, float h)
 {
-    const uint32_t gb = g != g ? 0x7fc00000u : __builtin_bit_cast(uint32_t, g);
-    return (uint64_t)gb << 32 | __builtin_bit_cast(uint32_t, h);
+    const uint32_t wb = w != w ? 0x7fc00000u : __builtin_bit_cast(uint32_t, w);
+    return (uint64_t)wb << 32 | __builtin_bit_cast(uint32_t, h);
 }
-__device__ __forceinline__ float pair_g(uint64_t v) { return __builtin_bit_cast(float, (uint32_t)(v >> 32)); }
+__device__ __forceinline__ float pair_w(uint64_t v) { return __builtin_bit_cast(float, (uint32_t)(v >> 32)); }
 __device__ __forceinline__ float pair_h(uint64_t v) { return __builtin_bit_cast(float, (uint32_t)v); }
+__device__ __forceinline__ float join(float w, float h1, float h) { return w == CUT ? h1 : decay_apply(decay_held(w), h, h1); }
 __device__ __forceinline__ uint64_t peek(const uint64_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 __device__ __forceinline__ void publish(uint64_t *p, uint64_t v)
 {
@@ -125,102 +139,125 @@ __device__ __forceinline__ void publish(uint64_t *p, uint64_t v)
     asm volatile("" ::: "memory");                          // before any wait that follows
 }
 
-// Waits for up to LOOK pairs at[0], at[-C], ...: n of them.  A wait that lasts about a second (another call writes to this
-// call's workspace) is given up, by all waits of the call: the pair counts as a cut with NaN.
-constexpr int LOOK = 8;
-__device__ __forceinline__ void await_pairs(const ScanChain &k, const uint64_t *at, int C, int n, uint64_t *v)
+// Waits for the pairs at(0) .. at(n - 1), n <= BLOCK.  A wait that lasts about a second (another call writes to this call's
+// workspace) is given up, by all waits of the call: the pair counts as a cut with NaN.
+template <typename F> __device__ __forceinline__ void await_pairs(const ScanChain &k, int n, F at, uint64_t *v)
 {
     for (int spin = 0;; ++spin) {
         bool all = true;
 #pragma unroll
-        for (int u = 0; u < LOOK; ++u) v[u] = u < n ? peek(at - (size_t)u * C) : 0;
+        for (int u = 0; u < BLOCK; ++u)
+            if (u < n) v[u] = peek(at(u));
 #pragma unroll
-        for (int u = 0; u < LOOK; ++u) all = all && (uint32_t)(v[u] >> 32) != EMPTY;
+        for (int u = 0; u < BLOCK; ++u) all = all && (u >= n || (uint32_t)(v[u] >> 32) != EMPTY);
         if (all) return;
         if ((spin & 63) == 63 &&
             (spin >= SPINS || __hip_atomic_load(k.gave_up, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))) {
             __hip_atomic_store(k.gave_up, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-            for (int u = 0; u < LOOK; ++u)
-                if ((uint32_t)(v[u] >> 32) == EMPTY) v[u] = pair_of(CUT, __builtin_bit_cast(float, 0x7fc00000u));
+            for (int u = 0; u < BLOCK; ++u)
+                if (u < n && (uint32_t)(v[u] >> 32) == EMPTY) v[u] = pair_of(CUT, __builtin_bit_cast(float, 0x7fc00000u));
             return;
         }
         __builtin_amdgcn_s_sleep(1);
     }
 }
 
-// The state before segment q (in the order of the scan) in channel c.
-__device__ __forceinline__ float state_before(const ScanChain &k, int q, int c, int C)
-{
-    const int base = q / k.group * k.group;                 // behind segment base - 1 the state is published whole
-    float G = 0.f, h = 0.f;
-    for (int j = q - 1; j >= base; j -= LOOK) {
-        uint64_t v[LOOK];
-        const int n = min(LOOK, j - base + 1);
-        await_pairs(k, k.part + (size_t)j * C + c, C, n, v);
-#pragma unroll
-        for (int u = 0; u < LOOK; ++u) {
-            if (u >= n) break;
-            h = decay_apply(decay_code(G), pair_h(v[u]), h);
-            if (pair_g(v[u]) > 0.f) return h;
-            G += pair_g(v[u]);
-        }
-    }
-    if (base == 0) return h;
-    uint64_t v[LOOK];
-    await_pairs(k, k.whole + (size_t)(base / k.group - 1) * C + c, C, 1, v);
-    return decay_apply(decay_code(G), pair_h(v[0]), h);
-}
-
 struct Joined {
-    float G[RUNS][SCAN_CHANNELS], h[RUNS][SCAN_CHANNELS];   // of each run, then of the runs before it
-    float in[SCAN_CHANNELS];                                // the state before the segment
+    float w[RUNS][SCAN_CHANNELS], h[RUNS][SCAN_CHANNELS];   // of each run; then the state before it from the segment's
+    float G[RUNS][SCAN_CHANNELS];                           // log-decay of a run, then of the runs before it (cut: +1)
+    float in[SCAN_CHANNELS];                                // the state before the segment's block, then before the segment
     unsigned ticket;
 };
 
 // Joins the runs of every channel in the order of the scan (BACK: the last run first) and gets the state before the
-// segment.  need: that state is looked at (no sequence begins at the segment's first row).
+// segment.  need: that state is looked at (no sequence begins at the segment's first row).  Waves 0 and 1 join, publish and wait for the
+// segments of the block, the other two for what lies before the block.
 template <bool CHAIN, bool BACK>
 __device__ __forceinline__ void join_runs(const ScanParams &p, int q, int c0, bool need, Joined &s)
 {
     lds_barrier();
-    const int t = threadIdx.x, c = c0 + t;
-    if (t < SCAN_CHANNELS) {
-        float G = 0.f, h = 0.f;
+    const ScanChain &k = p.chain;
+    const int block = q / BLOCK, n = q % BLOCK;             // of the segments; n of the block lie before
+    const bool ends_block = n == BLOCK - 1, ends_all = ends_block && block % BLOCK == BLOCK - 1;
+    const bool joins = threadIdx.x < SCAN_CHANNELS;
+    const unsigned t = joins ? threadIdx.x : threadIdx.x - SCAN_CHANNELS, c = c0 + t;
+    const bool there = CHAIN && c < (unsigned)p.C;
+    need = need && q > 0;
+    float w = 0.f, h = 0.f;
+    uint64_t v[BLOCK];
+    if (joins) {
+        float G = 0.f;
+        bool cut = false;
 #pragma unroll
         for (int i = 0; i < RUNS; ++i) {
-            const int k = BACK ? RUNS - 1 - i : i;
-            const float g1 = s.G[k][t], h1 = s.h[k][t];
-            s.G[k][t] = G;
-            s.h[k][t] = h;
-            const bool cut = g1 > 0.f;
-            h = cut ? h1 : decay_apply(decay_code(g1), h, h1);
-            G = cut || G > 0.f ? CUT : G + g1;
+            const int j = BACK ? RUNS - 1 - i : i;
+            const float g1 = s.G[j][t], w1 = s.w[j][t], h1 = s.h[j][t];
+            s.G[j][t] = cut ? 1.f : G;
+            s.h[j][t] = h;
+            h = join(w1, h1, h);
+            cut = cut || w1 == CUT;
+            G += g1;
         }
-        if (CHAIN && c < p.C) {
-            publish(p.chain.part + (size_t)q * p.C + c, pair_of(G, h));
-            const bool hand_on = (q + 1) % p.chain.group == 0;
-            float in = 0.f;
-            if (q > 0 && (need || (hand_on && !(G > 0.f)))) in = state_before(p.chain, q, c, p.C);
-            if (hand_on)
-                publish(p.chain.whole + (size_t)(q / p.chain.group) * p.C + c,
-                        pair_of(0.f, G > 0.f ? h : decay_apply(decay_code(G), in, h)));
-            s.in[t] = in;
+        w = cut ? CUT : decay_of(not_above_0(G)).w;
+        if (there) {
+            publish(k.part + (size_t)q * p.C + c, pair_of(w, h));
+            if (n > 0 && (need || ends_block))
+                await_pairs(k, n, [&](int u) { return k.part + (size_t)(q - n + u) * p.C + c; }, v);
+            if (ends_block) {
+                float to = pair_h(v[0]);
+                Decay all = decay_held(pair_w(v[0]));
+                cut = pair_w(v[0]) == CUT;
+#pragma unroll
+                for (int u = 1; u < BLOCK - 1; ++u) {
+                    cut = cut || pair_w(v[u]) == CUT;
+                    to = join(pair_w(v[u]), pair_h(v[u]), to);
+                    all = decay_product(all, decay_held(pair_w(v[u])));
+                }
+                const float bw = w == CUT || cut ? CUT : decay_product(all, decay_held(w)).w;
+                publish(k.blocks + (size_t)block * p.C + c, pair_of(bw, join(w, h, to)));
+            }
         }
+    } else if (there) {
+        float in = 0.f;
+        if ((need || ends_all) && block > 0) {
+            const int b0 = block / BLOCK * BLOCK, before = b0 > 0;
+            await_pairs(k, before + block - b0, [&](int u) {
+                return u < before ? k.whole + (size_t)(b0 / BLOCK - 1) * p.C + c : k.blocks + (size_t)(b0 + u - before) * p.C + c;
+            }, v);
+            // the state behind the blocks before counts as a cut: pair (2, state)
+#pragma unroll
+            for (int u = 0; u < BLOCK; ++u)
+                if (u < before + block - b0) in = join(pair_w(v[u]), pair_h(v[u]), in);
+        }
+        s.in[t] = in;
     }
     lds_barrier();
+    if (CHAIN) {
+        if (joins && there) {
+            float in = s.in[t];
+            if (need)
+#pragma unroll
+                for (int u = 0; u < BLOCK - 1; ++u)
+                    if (u < n) in = join(pair_w(v[u]), pair_h(v[u]), in);
+            if (ends_all) {
+                // (without need the segment is a cut)
+                publish(k.whole + (size_t)(block / BLOCK) * p.C + c, pair_of(CUT, join(w, h, in)));
+            }
+            s.in[t] = in;
+        }
+        lds_barrier();
+    }
 }
 
 // The state before run `run` in channels [4 l, 4 l + 4) of the segment.
 template <bool CHAIN> __device__ __forceinline__ void state_of_run(const Joined &s, int run, int l, float *h)
 {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        h[i] = s.h[run][CH * l + i];
-        if (CHAIN) {
-            const float G = s.G[run][CH * l + i];
-            if (!(G > 0.f)) h[i] = decay_apply(decay_code(G), s.in[CH * l + i], h[i]);
-        }
+    for (int i = 0; i < CH; ++i) h[i] = s.h[run][CH * l + i];
+    if (CHAIN && !(s.G[run][CH * l] > 0.f)) {               // cuts are rows': the same in all channels
+#pragma unroll
+        for (int i = 0; i < CH; ++i) h[i] = decay_apply(decay_of(not_above_0(s.G[run][CH * l + i])), s.in[CH * l + i], h[i]);
     }
 }
 
@@ -228,55 +265,75 @@ __device__ __forceinline__ void put_run(Joined &s, int run, int l, bool cut, con
 {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        s.G[run][CH * l + i] = cut ? CUT : G[i];
+        s.G[run][CH * l + i] = G[i];
+        s.w[run][CH * l + i] = cut ? CUT : decay_of(not_above_0(G[i])).w;
         s.h[run][CH * l + i] = h[i];
     }
 }
 
-// The segment and channels of a workgroup; false: none left (never, unless another call writes to the workspace).
-template <bool CHAIN> __device__ __forceinline__ bool take_segment(const ScanParams &p, Joined &s, int *q, int *c0)
-{
-    const unsigned wide = (p.C + SCAN_CHANNELS - 1) / SCAN_CHANNELS;
-    unsigned at = blockIdx.x;
-    if (CHAIN) {
-        if (threadIdx.x == 0) s.ticket = __hip_atomic_fetch_add(p.chain.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        lds_barrier();
-        at = __builtin_amdgcn_readfirstlane(s.ticket);
+// A lane's part of a segment in memory: rows of CH channels, at 32-bit offsets from the segment's first element
+// (64 rows of at most 2^24 elements).  In segments whose channels all exist, or whose C is a multiple of CH, every lane reads whole
+// vectors (a lane or row without elements those of the last that has some, and nothing looks at them); in others the last lane
+// goes element by element.
+struct Window {
+    int rows, n;                                            // rows of the segment that there are; the lane's channels
+    bool vec, full;                                         // full: all channels of the segment exist
+    int row0;                                               // the lane's first row
+    unsigned col;
+    __device__ __forceinline__ Window(const ScanParams &p, int r0, int c0)
+    {
+        const int c = c0 + (threadIdx.x % LANES) * CH;
+        rows = min(p.rows - r0, SCAN_ROWS);
+        n = max(0, min(CH, p.C - c));
+        full = c0 + SCAN_CHANNELS <= p.C;
+        vec = full || p.C % CH == 0;
+        row0 = (threadIdx.x / LANES) * RUN;
+        col = (vec ? min(c, p.C - CH) : min(c, p.C - 1)) - c0;
     }
-    *q = (int)(at / wide);
-    *c0 = (int)(at % wide) * SCAN_CHANNELS;
-    return *q < p.chain.segments;
-}
+    template <typename T> __device__ __forceinline__ void load(Raw4<T> *raw, const T *base, int64_t stride) const
+    {
+        const unsigned end = (unsigned)(rows - 1) * (unsigned)stride;
+        unsigned off = (unsigned)row0 * (unsigned)stride;
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                raw[i].load(base + (min(off, end) + col), CH);
+                off += (unsigned)stride;
+                asm("" : "+v"(off));                        // one addition a row, not a product
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                raw[i].load(base + (min(off, end) + col), n);
+                off += (unsigned)stride;
+            }
+        }
+    }
+    template <typename T> __device__ __forceinline__ void put(T *at, const float *x) const
+    {
+        if (vec) {
+            if (n > 0) Raw4<T>::store(at, CH, x);
+        } else {
+            if (n > 0) Raw4<T>::store(at, n, x);
+        }
+    }
+};
+
+// The lane's rows of an array one after the other, up or down.
+template <typename T> struct Cursor {
+    T *base;
+    unsigned off, step;
+    __device__ __forceinline__ Cursor(T *b, const Window &w, int64_t stride, int i)
+        : base(b), off((unsigned)(w.row0 + i) * (unsigned)stride + w.col), step((unsigned)stride) {}
+    __device__ __forceinline__ T *at() const { return reinterpret_cast<T *>(reinterpret_cast<char *>(base) + off * (unsigned)sizeof(T)); }
+    __device__ __forceinline__ void up() { off += step; asm("" : "+v"(off)); }
+    __device__ __forceinline__ void down() { off -= step; asm("" : "+v"(off)); }
+};
 
 // Four channels as they are stored: elements, or codes with their scale.
 template <typename T> struct Held {
     static constexpr int WORDS = sizeof(T);
     uint32_t v[WORDS];
-    __device__ __forceinline__ void load(const Rows &m, size_t r, int C, int c, int n)
-    {
-        if (m.scales) {
-            const int8_t *at = (const int8_t *)m.p + r * m.stride + c;
-            if (n == CH) {
-                typedef uint32_t u32_any __attribute__((aligned(1)));
-                v[0] = *reinterpret_cast<const u32_any *>(at);
-            } else {
-                v[0] = 0;
-#pragma unroll
-                for (int i = 0; i < CH; ++i)
-                    if (i < n) v[0] |= (uint32_t)(uint8_t)at[i] << (8 * i);
-            }
-            v[1] = n > 0 ? __builtin_bit_cast(uint32_t, m.scales[r * act_groups(C) + c / ACT_GROUP]) : 0;
-            return;
-        }
-        Raw4<T> raw;
-        raw.load((const T *)m.p + r * m.stride + c, n);
-        __builtin_memcpy(v, &raw, sizeof(raw));
-    }
-    __device__ __forceinline__ void clear()
-    {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) v[i] = 0;
-    }
     __device__ __forceinline__ void get(bool packed, float *x) const
     {
         if (packed) {
@@ -292,203 +349,292 @@ template <typename T> struct Held {
     }
 };
 
-template <typename T, typename G, bool CHAIN, bool FULL>
-__device__ __forceinline__ void scan_fwd_segment(const ScanParams &p, int q, int c0, Joined &s, Marks &m)
+// The lane's rows of the segment from row r0 on, or (BEFORE) the rows before them, where there is one.
+template <bool BEFORE, typename T>
+__device__ __forceinline__ void load_held(Held<T> *to, const Window &w, const Rows &m, int r0, int c0, int C)
 {
-    const int l = threadIdx.x % LANES, run = threadIdx.x / LANES, c = c0 + l * CH;
-    const int r0 = q * SCAN_ROWS, r1 = r0 + run * RUN;
-    const int n = FULL ? CH : max(0, min(CH, p.C - c));
-    Raw4<T> x[RUN];
-    Raw4<G> z[RUN];
+    const int base = BEFORE && r0 > 0 ? r0 - 1 : r0, skip = BEFORE && r0 == 0;
+    const unsigned stride = (unsigned)m.stride;
+    if (m.scales) {
+        const int8_t *codes = (const int8_t *)m.p + (size_t)base * m.stride + c0;
+        const float *scales = m.scales + (size_t)base * act_groups(C) + c0 / ACT_GROUP;
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+            const unsigned r = (unsigned)max(min(w.row0 + i, w.rows - 1) - skip, 0);
+            const int8_t *at = codes + (r * stride + w.col);
+            to[i].v[0] = 0;
+            if (w.vec) {
+                typedef uint32_t u32_any __attribute__((aligned(1)));
+                to[i].v[0] = *reinterpret_cast<const u32_any *>(at);
+            } else {
+#pragma unroll
+                for (int j = 0; j < CH; ++j)
+                    if (j < w.n) to[i].v[0] |= (uint32_t)(uint8_t)at[j] << (8 * j);
+            }
+            to[i].v[1] = __builtin_bit_cast(uint32_t, scales[r * (unsigned)act_groups(C)]);
+        }
+        return;
+    }
+    const T *rows = (const T *)m.p + (size_t)base * m.stride + c0;
 #pragma unroll
     for (int i = 0; i < RUN; ++i) {
-        const size_t r = r1 + i;
-        const int k = FULL || r1 + i < p.rows ? n : 0;
-        x[i].load((const T *)p.x.p + r * p.x.stride + c, k);
-        z[i].load((const G *)p.g.p + r * p.g.stride + c, k);
+        const unsigned r = (unsigned)max(min(w.row0 + i, w.rows - 1) - skip, 0);
+        Raw4<T> raw;
+        if (w.vec) raw.load(rows + (r * stride + w.col), CH); else raw.load(rows + (r * stride + w.col), w.n);
+        __builtin_memcpy(to[i].v, &raw, sizeof(raw));
     }
-    float eA[CH];
-    if (p.A_log) {
-        load_f4(p.A_log + c, n, eA);
+}
+
+// A channel's gate (eq. (5)), or log-decays as they are.
+template <bool GATED> struct Gates {
+    float k[CH];                                            // -e^A log2(e)
+    __device__ __forceinline__ void load(const Window &win, const float *A_log, int c0)
+    {
+        if (!GATED) return;
+        Raw4<float> raw;
+        if (win.vec) raw.load(A_log + c0 + win.col, CH); else raw.load(A_log + c0 + win.col, win.n);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) eA[i] = __expf(eA[i]);
+        for (int j = 0; j < CH; ++j) k[j] = raw[j];
     }
-    mark_rows(p, r0, q == p.chain.segments - 1, m, p.h0, p.hT, c0);
-    unsigned first = 0, last = 0;
-    const unsigned rows = run_rows(p, r1);
-    if (m.any) {
+    __device__ __forceinline__ void make()
+    {
+        if (GATED)
+#pragma unroll
+            for (int j = 0; j < CH; ++j) k[j] = __expf(k[j]) * -LOG2E;
+    }
+    __device__ __forceinline__ float log_decay(float z, int j, float g_min) const
+    {
+        return GATED ? g_min * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * k[j])) : not_above_0(z);
+    }
+    // d log_decay / d z, but for g_min e^A
+    __device__ __forceinline__ float slope(float z, int j) const
+    {
+        const float e = __builtin_amdgcn_exp2f(fminf(z * k[j], 120.f)), s = __builtin_amdgcn_rcpf(1.f + e);
+        return s * (e * s);
+    }
+};
+
+struct Yes { static constexpr bool on = true; };
+struct No { static constexpr bool on = false; };
+
+// The segment a workgroup takes of its column of channels, by a ticket of that column; false: none (never, unless another call
+// writes to this call's workspace).
+template <bool CHAIN> __device__ __forceinline__ bool take_segment(const ScanParams &p, int column, Joined &s, int *q)
+{
+    *q = 0;
+    if (CHAIN) {
+        if (threadIdx.x == 0)
+            s.ticket = __hip_atomic_fetch_add(p.chain.tickets + (size_t)column * TICKET_STEP, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        lds_barrier();
+        *q = (int)__builtin_amdgcn_readfirstlane(s.ticket);
+    }
+    return (unsigned)*q < (unsigned)p.chain.segments;
+}
+
+// Each pass has a form for segments that lie inside a sequence and whose channels all exist, with no questions
+// asked, and one for all others.
+template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 ? 4 : 3) void scan_fwd_kernel(const ScanParams p)
+{
+    __shared__ Joined s;
+    __shared__ Marks m;
+    const int column = blockIdx.x % ((p.C + SCAN_CHANNELS - 1) / SCAN_CHANNELS), c0 = column * SCAN_CHANNELS;
+    int q;
+    if (!take_segment<CHAIN>(p, column, s, &q)) return;
+    const int l = threadIdx.x % LANES, run = threadIdx.x / LANES, r0 = q * SCAN_ROWS, c = c0 + l * CH;
+    const Window win(p, r0, c0);
+    const Share share(p.complement);
+    const Offsets offsets(p, r0);
+    Gates<GATED> gates;
+    gates.load(win, p.A_log, c0);
+    Raw4<T> x[RUN];
+    Raw4<G> z[RUN];
+    if (p.rows > 0) {
+        win.load<T>(x, (const T *)p.x.p + (size_t)r0 * p.x.stride + c0, p.x.stride);
+        win.load<G>(z, (const G *)p.g.p + (size_t)r0 * p.g.stride + c0, p.g.stride);
+    }
+    mark_rows(p, offsets, r0, q == p.chain.segments - 1, m, p.h0, p.hT, c0);
+    gates.make();
+    const bool plain = m.any == 0 && r0 >= offsets.begin && r0 + SCAN_ROWS <= offsets.end && win.full;
+    unsigned first = 0, last = 0, rows = 0;
+    if (!plain) {
+        rows = run_rows(offsets, r0 + win.row0);
         first = run_marks(m.first, run);
         last = run_marks(m.last, run);
     }
-    const bool need = m.first[0] < 0;
     const auto begin = [&](int i, float *h) {
         if (p.h0)
-            load_f4(p.h0 + (size_t)m.first[run * RUN + i] * p.C + c, n, h);
+            load_f4(p.h0 + (size_t)m.first[run * RUN + i] * p.C + c, win.n, h);
         else
 #pragma unroll
             for (int j = 0; j < CH; ++j) h[j] = 0.f;
     };
-    float w[RUN][CH], g[CH] = {}, h[CH] = {};
-    const bool gated = p.A_log != nullptr;
+    float w[RUN][CH], b[RUN][CH], h[CH] = {};
+    const auto pass = [&](auto free) {
+        float g[CH] = {};
 #pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-        if (first >> i & 1) begin(i, h);
-        const bool in = rows >> i & 1;
+        for (int i = 0; i < RUN; ++i) {
+            if (!free.on) {
+                if (first >> i & 1) begin(i, h);
+                if (!(rows >> i & 1)) continue;
+            }
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            float d = gated ? p.g_min * sigmoid2(eA[j] * z[i][j]).s : z[i][j];
-            d = d > 0.f || !in ? 0.f : d;
-            w[i][j] = decay_code(d);
-            g[j] += d;
-            const float b = !in ? 0.f : p.complement ? x[i][j] * decay_rest(w[i][j]) : x[i][j];
-            h[j] = decay_apply(w[i][j], h[j], b);
+            for (int j = 0; j < CH; ++j) {
+                const float v = gates.log_decay(z[i][j], j, p.g_min);
+                const Decay d = decay_of(v);
+                w[i][j] = d.w;
+                g[j] += v;
+                b[i][j] = share(d, x[i][j]);
+                h[j] = decay_apply(d, h[j], b[i][j]);
+            }
         }
-    }
-    put_run(s, run, l, first != 0, g, h);
-    join_runs<CHAIN, false>(p, q, c0, need, s);
+        put_run(s, run, l, !free.on && first != 0, g, h);
+    };
+    if (plain) pass(Yes{}); else pass(No{});
+    join_runs<CHAIN, false>(p, q, c0, m.first[0] < 0, s);
     state_of_run<CHAIN>(s, run, l, h);
+    const auto finish = [&](auto free) {
+        Cursor<T> out((T *)p.h + (size_t)r0 * p.C + c0, win, p.C, 0);
 #pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-        if (first >> i & 1) begin(i, h);
-        const bool in = rows >> i & 1;
-        float out[CH];
+        for (int i = 0; i < RUN; ++i) {
+            const bool in = free.on || (rows >> i & 1);
+            if (!free.on && (first >> i & 1)) begin(i, h);
+            if (in) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const float b = !in ? 0.f : p.complement ? x[i][j] * decay_rest(w[i][j]) : x[i][j];
-            h[j] = decay_apply(w[i][j], h[j], b);
-            out[j] = h[j];
+                for (int j = 0; j < CH; ++j) h[j] = decay_apply(decay_held(w[i][j]), h[j], b[i][j]);
+                if (free.on) Raw4<T>::store(out.at(), CH, h); else win.put(out.at(), h);
+            }
+            out.up();
+            if (p.h8.codes) {
+                float v[CH];
+#pragma unroll
+                for (int j = 0; j < CH; ++j) v[j] = free.on || j < win.n ? to_f<T>(from_f<T>(h[j])) : 0.f;
+                store_codes<CH>(p.h8, r0 + win.row0 + i, p.C, c, free.on ? CH : in ? win.n : 0, v);
+            }
+            if (!free.on && (last >> i & 1) && p.hT && win.n > 0)
+                Raw4<float>::store(p.hT + (size_t)m.last[run * RUN + i] * p.C + c, win.n, h);
         }
-        const size_t at = (size_t)(r1 + i) * p.C + c;
-        if (in && n > 0) Raw4<T>::store((T *)p.h + at, n, out);
-        if (p.h8.codes) {
-#pragma unroll
-            for (int j = 0; j < CH; ++j) out[j] = j < n ? to_f<T>(from_f<T>(out[j])) : 0.f;
-            store_codes<CH>(p.h8, r1 + i, p.C, c, in ? n : 0, out);
-        }
-        if (last >> i & 1 && p.hT && n > 0) Raw4<float>::store(p.hT + (size_t)m.last[run * RUN + i] * p.C + c, n, h);
-    }
-}
-
-template <typename T, typename G, bool CHAIN> __global__ __launch_bounds__(256, 4) void scan_fwd_kernel(const ScanParams p)
-{
-    __shared__ Joined s;
-    __shared__ Marks m;
-    int q, c0;
-    if (!take_segment<CHAIN>(p, s, &q, &c0)) return;
-    if (c0 + SCAN_CHANNELS <= p.C && (q + 1) * SCAN_ROWS <= p.rows)
-        scan_fwd_segment<T, G, CHAIN, true>(p, q, c0, s, m);
-    else
-        scan_fwd_segment<T, G, CHAIN, false>(p, q, c0, s, m);
+    };
+    if (plain) finish(Yes{}); else finish(No{});
 }
 
 // Gradients, from the last row to the first: D_t = d_h_t + e_{t+1}, e_t = a_t D_t; runs, segments and their order mirrored.
-template <typename T, typename G, bool CHAIN, bool FULL>
-__device__ __forceinline__ void scan_bwd_segment(const ScanParams &p, int q, int c0, Joined &s, Marks &m)
+template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(const ScanParams p)
 {
-    const int l = threadIdx.x % LANES, run = threadIdx.x / LANES, c = c0 + l * CH;
-    const int r0 = (p.chain.segments - 1 - q) * SCAN_ROWS, r1 = r0 + run * RUN;
-    const int n = FULL ? CH : max(0, min(CH, p.C - c));
+    __shared__ Joined s;
+    __shared__ Marks m;
+    const int column = blockIdx.x % ((p.C + SCAN_CHANNELS - 1) / SCAN_CHANNELS), c0 = column * SCAN_CHANNELS;
+    int q;
+    if (!take_segment<CHAIN>(p, column, s, &q)) return;
+    const int l = threadIdx.x % LANES, run = threadIdx.x / LANES, r0 = (p.chain.segments - 1 - q) * SCAN_ROWS, c = c0 + l * CH;
+    const Window win(p, r0, c0);
+    const Share share(p.complement);
+    const Offsets offsets(p, r0);
+    Gates<GATED> gates;
+    gates.load(win, p.A_log, c0);
     Raw4<T> d[RUN];
     Raw4<G> z[RUN];
-    const auto there = [&](int i) { return FULL || r1 + i < p.rows ? n : 0; };
-#pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-        const size_t r = r1 + i;
-        d[i].load((const T *)p.d_h + r * p.C + c, there(i));
-        z[i].load((const G *)p.g.p + r * p.g.stride + c, there(i));
+    if (p.rows > 0) {
+        win.load<T>(d, (const T *)p.d_h + (size_t)r0 * p.C + c0, p.C);
+        win.load<G>(z, (const G *)p.g.p + (size_t)r0 * p.g.stride + c0, p.g.stride);
     }
-    float eA[CH];
-    if (p.A_log) {
-        load_f4(p.A_log + c, n, eA);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) eA[i] = __expf(eA[i]);
-    }
-    mark_rows(p, r0, q == 0, m, p.dhT, p.dh0, c0);
-    unsigned first = 0, last = 0;
-    const unsigned rows = run_rows(p, r1);
-    if (m.any) {
+    mark_rows(p, offsets, r0, q == 0, m, p.dhT, p.dh0, c0);
+    gates.make();
+    const bool plain = m.any == 0 && r0 >= offsets.begin && r0 + SCAN_ROWS <= offsets.end && win.full;
+    unsigned first = 0, last = 0, rows = 0;
+    if (!plain) {
+        rows = run_rows(offsets, r0 + win.row0);
         first = run_marks(m.first, run);
         last = run_marks(m.last, run);
     }
-    const bool need = m.last[SCAN_ROWS - 1] < 0;
     const auto begin = [&](int i, float *e) {
         if (p.dhT)
-            load_f4(p.dhT + (size_t)m.last[run * RUN + i] * p.C + c, n, e);
+            load_f4(p.dhT + (size_t)m.last[run * RUN + i] * p.C + c, win.n, e);
         else
 #pragma unroll
             for (int j = 0; j < CH; ++j) e[j] = 0.f;
     };
-    float w[RUN][CH], g[CH] = {}, e[CH] = {};
-    const bool gated = p.A_log != nullptr;
+    float w[RUN][CH], e[CH] = {};
+    const auto pass = [&](auto free) {
+        float g[CH] = {};
 #pragma unroll
-    for (int i = RUN - 1; i >= 0; --i) {
-        if (last >> i & 1) begin(i, e);
-        const bool in = rows >> i & 1;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            float x = gated ? p.g_min * sigmoid2(eA[j] * z[i][j]).s : z[i][j];
-            x = x > 0.f || !in ? 0.f : x;
-            w[i][j] = decay_code(x);
-            g[j] += x;
-            e[j] = decay_times(w[i][j], in ? d[i][j] + e[j] : e[j]);
-        }
-    }
-    put_run(s, run, l, last != 0, g, e);
-    Held<T> hs[RUN], xs[RUN];
-    if (p.dg) {
-#pragma unroll
-        for (int i = 0; i < RUN; ++i) {
-            // the row before; a sequence's first has none
-            const size_t r = r1 + i;
-            if (r > 0) hs[i].load(p.hs, r - 1, p.C, c, FULL || r1 + i - 1 < p.rows ? n : 0); else hs[i].clear();
-            if (p.complement) xs[i].load(p.x, r, p.C, c, there(i));
-        }
-    }
-    join_runs<CHAIN, true>(p, q, c0, need, s);
-    state_of_run<CHAIN>(s, run, l, e);
-    float dA[CH] = {};
-#pragma unroll
-    for (int i = RUN - 1; i >= 0; --i) {
-        if (last >> i & 1) begin(i, e);
-        const bool in = rows >> i & 1;
-        float out[CH];
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const float D = in ? d[i][j] + e[j] : e[j];
-            e[j] = decay_times(w[i][j], D);
-            out[j] = p.complement ? D * decay_rest(w[i][j]) : D;
-        }
-        const size_t r = r1 + i;
-        if (in && n > 0) Raw4<T>::store((T *)p.dx + r * p.dx_stride + c, n, out);
-        if (p.dg) {
-            float prev[CH];
-            hs[i].get(p.hs.scales, prev);
-            if (first >> i & 1) {
-                if (p.h0)
-                    load_f4(p.h0 + (size_t)m.first[run * RUN + i] * p.C + c, n, prev);
-                else
-#pragma unroll
-                    for (int j = 0; j < CH; ++j) prev[j] = 0.f;
-            }
-            if (p.complement) {
-                xs[i].get(p.x.scales, out);
-#pragma unroll
-                for (int j = 0; j < CH; ++j) prev[j] -= out[j];
+        for (int i = RUN - 1; i >= 0; --i) {
+            if (!free.on) {
+                if (last >> i & 1) begin(i, e);
+                if (!(rows >> i & 1)) continue;
             }
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                out[j] = e[j] * prev[j];
-                if (gated) {
-                    const Sigmoid sg = sigmoid2(eA[j] * z[i][j]);
-                    out[j] *= p.g_min * sg.s * sg.r * eA[j];
-                    if (in) dA[j] += out[j] * z[i][j];
-                }
+                const float v = gates.log_decay(z[i][j], j, p.g_min);
+                const Decay k = decay_of(v);
+                w[i][j] = k.w;
+                g[j] += v;
+                e[j] = decay_times(k, d[i][j] + e[j]);
             }
-            if (in && n > 0) Raw4<G>::store((G *)p.dg + r * p.dg_stride + c, n, out);
         }
-        if (first >> i & 1 && p.dh0 && n > 0) Raw4<float>::store(p.dh0 + (size_t)m.first[run * RUN + i] * p.C + c, n, e);
+        put_run(s, run, l, !free.on && last != 0, g, e);
+    };
+    if (plain) pass(Yes{}); else pass(No{});
+    Held<T> hs[RUN], xs[RUN];
+    if (p.dg && p.rows > 0) {
+        load_held<true>(hs, win, p.hs, r0, c0, p.C);
+        if (p.complement) load_held<false>(xs, win, p.x, r0, c0, p.C);
     }
-    if (p.dA) {                                             // the segment's part of dA: runs in their order
+    join_runs<CHAIN, true>(p, q, c0, m.last[SCAN_ROWS - 1] < 0, s);
+    state_of_run<CHAIN>(s, run, l, e);
+    float dA[CH] = {}, unit[CH];
+    if (GATED)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) unit[j] = p.g_min * gates.k[j] * (-1.f / LOG2E);
+    const auto finish = [&](auto free) {
+        Cursor<T> to_x((T *)p.dx + (size_t)r0 * p.dx_stride + c0, win, p.dx_stride, RUN - 1);
+        Cursor<G> to_g((G *)p.dg + (size_t)r0 * p.dg_stride + c0, win, p.dg_stride, RUN - 1);
+#pragma unroll
+        for (int i = RUN - 1; i >= 0; --i) {
+            if (!free.on && (last >> i & 1)) begin(i, e);
+            if (free.on || (rows >> i & 1)) {
+                float out[CH];
+#pragma unroll
+                for (int j = 0; j < CH; ++j) {
+                    const Decay k = decay_held(w[i][j]);
+                    const float D = d[i][j] + e[j];
+                    e[j] = decay_times(k, D);
+                    out[j] = share(k, D);
+                }
+                if (free.on) Raw4<T>::store(to_x.at(), CH, out); else win.put(to_x.at(), out);
+                if (p.dg) {
+                    float prev[CH];
+                    hs[i].get(p.hs.scales, prev);
+                    if (!free.on && (first >> i & 1)) {
+                        if (p.h0)
+                            load_f4(p.h0 + (size_t)m.first[run * RUN + i] * p.C + c, win.n, prev);
+                        else
+#pragma unroll
+                            for (int j = 0; j < CH; ++j) prev[j] = 0.f;
+                    }
+                    if (p.complement) {
+                        xs[i].get(p.x.scales, out);
+#pragma unroll
+                        for (int j = 0; j < CH; ++j) prev[j] -= out[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) {
+                        out[j] = e[j] * prev[j];
+                        if (GATED) {
+                            out[j] *= unit[j] * gates.slope(z[i][j], j);
+                            dA[j] += out[j] * z[i][j];
+                        }
+                    }
+                    if (free.on) Raw4<G>::store(to_g.at(), CH, out); else win.put(to_g.at(), out);
+                }
+                if (!free.on && (first >> i & 1) && p.dh0 && win.n > 0)
+                    Raw4<float>::store(p.dh0 + (size_t)m.first[run * RUN + i] * p.C + c, win.n, e);
+            }
+            to_x.down();
+            to_g.down();
+        }
+    };
+    if (plain) finish(Yes{}); else finish(No{});
+    if (GATED && p.dA) {                                    // the segment's part of dA: runs in their order
         lds_barrier();
 #pragma unroll
         for (int j = 0; j < CH; ++j) s.h[run][CH * l + j] = dA[j];
@@ -503,24 +649,13 @@ __device__ __forceinline__ void scan_bwd_segment(const ScanParams &p, int q, int
     }
 }
 
-template <typename T, typename G, bool CHAIN> __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(const ScanParams p)
+// Clears the hand-over's memory (no pair is there yet; tickets and flag 0) and copies states that the call overwrites.
+__global__ __launch_bounds__(256) void scan_clear_kernel(ScanChain k, const float *from, float *to, size_t states)
 {
-    __shared__ Joined s;
-    __shared__ Marks m;
-    int q, c0;
-    if (!take_segment<CHAIN>(p, s, &q, &c0)) return;
-    if (c0 + SCAN_CHANNELS <= p.C && (p.chain.segments - q) * SCAN_ROWS <= p.rows)
-        scan_bwd_segment<T, G, CHAIN, true>(p, q, c0, s, m);
-    else
-        scan_bwd_segment<T, G, CHAIN, false>(p, q, c0, s, m);
-}
-
-// Clears the hand-over's memory (no pair there yet; ticket and flag, its last word, 0) and copies states that the call overwrites.
-__global__ __launch_bounds__(256) void scan_clear_kernel(uint64_t *words, size_t n, const float *from, float *to, size_t states)
-{
-    const size_t step = (size_t)gridDim.x * 256;
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) words[i] = i + 1 < n ? ~(uint64_t)0 : 0;
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < states; i += step) to[i] = from[i];
+    const size_t step = (size_t)gridDim.x * 256, at = (size_t)blockIdx.x * 256 + threadIdx.x;
+    for (size_t i = at; i < k.words; i += step) k.part[i] = ~(uint64_t)0;
+    for (size_t i = at; i < k.counters; i += step) k.tickets[i] = 0;
+    for (size_t i = at; i < states; i += step) to[i] = from[i];
 }
 
 // Sums of the segments' parts, in their order.
@@ -554,6 +689,7 @@ template <typename T, typename G> __global__ __launch_bounds__(256) void scan_st
     if (cnt == 0) return;
     float h[8];
     if (mine) {
+        const Share share(p.complement);
         Raw8<T> x;
         Raw8<G> g;
         float A[8];
@@ -563,8 +699,8 @@ template <typename T, typename G> __global__ __launch_bounds__(256) void scan_st
         if (p.A_log) load_f8(p.A_log + c, cnt, A);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float w = decay_code(p.A_log ? p.g_min * sigmoid2(__expf(A[i]) * g[i]).s : g[i]);
-            h[i] = decay_apply(w, h[i], p.complement ? x[i] * decay_rest(w) : x[i]);
+            const Decay d = decay_of(p.A_log ? p.g_min * sigmoid2(__expf(A[i]) * g[i]).s : not_above_0(g[i]));
+            h[i] = decay_apply(d, h[i], share(d, x[i]));
         }
         Raw8<float>::store(p.new_state + (size_t)slot * p.C + c, cnt, h);
     } else {
@@ -580,7 +716,7 @@ static hipError_t launch_clear(const ScanParams &p, const float *states, hipStre
     const size_t most = p.chain.words > copied ? p.chain.words : copied;
     if (most == 0) return hipSuccess;
     const size_t grid = (most + 1023) / 1024;
-    hipLaunchKernelGGL(scan_clear_kernel, dim3((unsigned)(grid < 1024 ? grid : 1024)), dim3(256), 0, stream, p.chain.part, p.chain.words, states,
+    hipLaunchKernelGGL(scan_clear_kernel, dim3((unsigned)(grid < 1024 ? grid : 1024)), dim3(256), 0, stream, p.chain, states,
                        p.state_copy, copied);
     return hipGetLastError();
 }
@@ -591,10 +727,9 @@ template <typename T, typename G> static hipError_t launch_fwd_t(ScanParams p, h
     const hipError_t e = launch_clear(p, p.h0, stream);
     if (e != hipSuccess) return e;
     if (p.state_copy) p.h0 = p.state_copy;
-    if (p.chain.words)
-        hipLaunchKernelGGL((scan_fwd_kernel<T, G, true>), grid, dim3(256), 0, stream, p);
-    else
-        hipLaunchKernelGGL((scan_fwd_kernel<T, G, false>), grid, dim3(256), 0, stream, p);
+    const auto kernel = p.A_log ? p.chain.words ? scan_fwd_kernel<T, G, true, true> : scan_fwd_kernel<T, G, true, false>
+                                : p.chain.words ? scan_fwd_kernel<T, G, false, true> : scan_fwd_kernel<T, G, false, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -604,10 +739,9 @@ template <typename T, typename G> static hipError_t launch_bwd_t(ScanParams p, h
     const hipError_t e = launch_clear(p, p.dhT, stream);
     if (e != hipSuccess) return e;
     if (p.state_copy) p.dhT = p.state_copy;
-    if (p.chain.words)
-        hipLaunchKernelGGL((scan_bwd_kernel<T, G, true>), grid, dim3(256), 0, stream, p);
-    else
-        hipLaunchKernelGGL((scan_bwd_kernel<T, G, false>), grid, dim3(256), 0, stream, p);
+    const auto kernel = p.A_log ? p.chain.words ? scan_bwd_kernel<T, G, true, true> : scan_bwd_kernel<T, G, true, false>
+                                : p.chain.words ? scan_bwd_kernel<T, G, false, true> : scan_bwd_kernel<T, G, false, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
     if (p.dA)
         hipLaunchKernelGGL(scan_sum_kernel, dim3((p.C + 63) / 64), dim3(256), 0, stream, p.dA_part, p.chain.segments, p.C, p.dA);
     return hipGetLastError();

@@ -215,6 +215,23 @@ def test_strided_rows(dtype):
     assert torch.equal(s, t)
 
 
+@pytest.mark.parametrize("g", [0.0, 3.0, -1e-7, -0.09, -1.5, float("-inf")])
+def test_constant_decays_over_many_segments(g):
+    """The same decay everywhere, over segments, blocks of them and blocks of blocks; whole numbers while nothing decays."""
+    kda = _kda()
+    T, C = 9000, 5
+    x = torch.randint(-2, 3, (T, C), generator=torch.Generator().manual_seed(1)).float()
+    gs = torch.full((T, C), g)
+    h, hT = kda.gated_scan_fwd(x.cuda()[None], gs.cuda()[None])
+    if g >= 0:
+        assert torch.equal(h[0].cpu(), x.cumsum(0))
+    want, wT, tol, tT = ref.scan(ref.f64(x), ref.f64(gs), None, -5.0, False, [0, T], None)
+    ref.close(h[0], want, tol, FP, "h")
+    ref.close(hT, wT, tT, FP, "final state")
+    back = kda.gated_scan_bwd(None, gs.cuda()[None], None, x.flip(0).cuda()[None], need_dg=False)[0]
+    ref.close(back[0].flip(0), want, tol, FP, "dx")
+
+
 def test_rows_outside_sequences_and_broken_offsets():
     """Rows before the first and behind the last sequence stay as they were; offsets that break their rules write nothing
     outside the outputs (guards on both sides)."""
