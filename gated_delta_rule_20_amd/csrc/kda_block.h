@@ -11,6 +11,10 @@ namespace kda {
 constexpr int ACT_GROUP = 128;        // channels that share a scale
 constexpr int NORM_MAX_D = 16384;     // channels of a row that block norms hold in registers
 
+// Block norms backwards: rows that a workgroup holds side by side, and its waves.
+constexpr int norm_rows(int D) { return D <= 256 ? 4 : D <= 512 ? 2 : 1; }
+constexpr int norm_waves(int D) { return D <= 1024 ? 4 : D <= 2048 ? 8 : 16; }
+
 // Rows of C elements: of a type, or (scales set) int8 codes with their scales.
 struct Rows {
     const void *p;

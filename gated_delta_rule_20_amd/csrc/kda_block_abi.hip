@@ -200,12 +200,18 @@ template <typename A> kda_status_t plan_norm(const A *a, kda::NormParams *p)
     return KDA_SUCCESS;
 }
 
-// Rows whose sums of the weights' gradients one workgroup keeps: as many workgroups as keep the chip busy.
-int norm_parts(int R) { return R < 512 ? R : 512; }
+// Workgroups of the backward pass: 16 waves on each of 256 units, and four rows at least for each, since each leaves
+// its own sums of the weights' gradients.
+int norm_parts(int R, int D)
+{
+    const int rows = 4 * kda::norm_rows(D), most = 256 * 16 / kda::norm_waves(D);
+    const int n = R / rows + (R % rows != 0);
+    return n < most ? n : most;
+}
 
 size_t plan_norm_bwd(const kda_block_norm_bwd_args_t *a, kda::NormParams *p)
 {
-    p->parts = norm_parts(a->R);
+    p->parts = norm_parts(a->R, a->D);
     p->part = (float *)a->workspace;
     return a->d_post_weight || a->d_res_scale || a->d_pre_weight ? sizeof(float) * 3 * (size_t)p->parts * a->D : 0;
 }

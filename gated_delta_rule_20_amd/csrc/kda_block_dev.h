@@ -242,6 +242,26 @@ __device__ __forceinline__ Sigmoid sigmoid2(float x)
     return {shut ? 0.f : s, e * s};
 }
 
+// The sum over `rows` rows of column blockIdx.x * 16 + thread % 16 of a matrix of C columns, on threads 0 .. 15 of 256: in
+// float64, in a fixed order.
+__device__ __forceinline__ double column_sum(const float *part, int rows, int C, double (*s)[16])
+{
+    const int l = threadIdx.x & 15, slice = threadIdx.x >> 4, c = blockIdx.x * 16 + l;
+    double sum = 0.0;
+    for (int i = slice; i < rows; i += 8 * 16) {
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = c < C && i + 16 * u < rows ? part[(size_t)(i + 16 * u) * C + c] : 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum += v[u];
+    }
+    s[slice][l] = sum;
+    __syncthreads();
+    if (slice > 0) return 0.0;
+    for (int k = 1; k < 16; ++k) sum += s[k][l];
+    return sum;
+}
+
 // A decay e^x (x <= 0, and -0 for 0) kept as one number w: e^x - 1, its sign set, where x > -0.1 (to its own last
 // place: the series to x^5 leaves x^5 / 720 < 2^-25); else e^x, its sign clear.  A state that fades over
 // 10^4 tokens would carry 10^4 times the rounding of e^x itself.

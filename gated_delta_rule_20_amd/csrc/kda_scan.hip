@@ -661,14 +661,10 @@ __global__ __launch_bounds__(256) void scan_clear_kernel(ScanChain k, const floa
 // Sums of the segments' parts, in their order.
 __global__ __launch_bounds__(256) void scan_sum_kernel(const float *part, int parts, int C, float *out)
 {
-    __shared__ double s_part[4][64];
-    const int l = threadIdx.x & 63, c = blockIdx.x * 64 + l, slice = threadIdx.x / 64;
-    double sum = 0.0;
-    if (c < C)
-        for (int i = slice; i < parts; i += 4) sum += part[(size_t)i * C + c];
-    s_part[slice][l] = sum;
-    __syncthreads();
-    if (slice == 0 && c < C) out[c] = (float)((s_part[0][l] + s_part[1][l]) + (s_part[2][l] + s_part[3][l]));
+    __shared__ double s_part[16][16];
+    const double sum = column_sum(part, parts, C, s_part);
+    const int c = blockIdx.x * 16 + threadIdx.x;
+    if (threadIdx.x < 16 && c < C) out[c] = (float)sum;
 }
 
 // One token a sequence: 8 channels a lane.  Slots as for kda_linear_recurrent_step.
@@ -743,7 +739,7 @@ template <typename T, typename G> static hipError_t launch_bwd_t(ScanParams p, h
                                 : p.chain.words ? scan_bwd_kernel<T, G, false, true> : scan_bwd_kernel<T, G, false, false>;
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
     if (p.dA)
-        hipLaunchKernelGGL(scan_sum_kernel, dim3((p.C + 63) / 64), dim3(256), 0, stream, p.dA_part, p.chain.segments, p.C, p.dA);
+        hipLaunchKernelGGL(scan_sum_kernel, dim3((p.C + 15) / 16), dim3(256), 0, stream, p.dA_part, p.chain.segments, p.C, p.dA);
     return hipGetLastError();
 }
 
