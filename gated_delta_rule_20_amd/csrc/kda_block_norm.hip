@@ -95,49 +95,61 @@ template <int NW> struct RowSum6 {
     }
 };
 
+template <int V, typename A, typename B> struct Pick { typedef A type; };
+template <typename A, typename B> struct Pick<8, A, B> { typedef B type; };
+
 // A uniform address and a lane's 32-bit offset.
 template <typename T> __device__ __forceinline__ T *at_byte(T *p, unsigned bytes)
 {
     return reinterpret_cast<T *>(reinterpret_cast<uintptr_t>(p) + bytes);
 }
 
-// Four channels of a row as they are stored: elements, or codes with their scale.
-template <typename T> struct Held4 {
-    static constexpr int WORDS = sizeof(T);
+// V (4 or 8) channels of a row as they are stored: elements, or codes with their scale.
+template <typename T, int V> struct HeldV {
+    static constexpr int WORDS = V * sizeof(T) / 4;
+    typedef typename Pick<V, Raw4<T>, Raw8<T>>::type Raw;
     uint32_t v[WORDS];
     // r is uniform
     __device__ __forceinline__ void load(const Rows &m, size_t r, int D, unsigned c, int n)
     {
         if (m.scales) {
             const int8_t *at = (const int8_t *)m.p + r * m.stride + c;
-            if (n == 4) {
-                typedef uint32_t u32_any __attribute__((aligned(1)));
-                v[0] = *reinterpret_cast<const u32_any *>(at);
-            } else {
-                v[0] = 0;
+            if (n == V) {
+                typedef uint32_t codes_any __attribute__((ext_vector_type(V / 4), aligned(1)));
+                const codes_any q = *reinterpret_cast<const codes_any *>(at);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < n) v[0] |= (uint32_t)(uint8_t)at[i] << (8 * i);
+                for (int k = 0; k < V / 4; ++k) v[k] = q[k];
+            } else {
+                v[0] = v[V / 4 - 1] = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i < n) v[i / 4] |= (uint32_t)(uint8_t)at[i] << (8 * (i % 4));
             }
-            v[1] = n > 0 ? __builtin_bit_cast(uint32_t, *at_byte(m.scales + r * act_groups(D), c / ACT_GROUP * 4)) : 0;
+            v[V / 4] = n > 0 ? __builtin_bit_cast(uint32_t, *at_byte(m.scales + r * act_groups(D), c / ACT_GROUP * 4)) : 0;
             return;
         }
-        Raw4<T> raw;
+        Raw raw;
         raw.load(at_byte((const T *)m.p + r * m.stride, c * sizeof(T)), n);
         __builtin_memcpy(v, &raw, sizeof(raw));
     }
-    __device__ __forceinline__ void get(bool packed, float *x) const
+    // channels [4 k, 4 k + 4)
+    __device__ __forceinline__ void get(bool packed, int k, float *x) const
     {
         if (packed) {
-            const float s = __builtin_bit_cast(float, v[1]);
+            const float s = __builtin_bit_cast(float, v[V / 4]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(v[0] >> (8 * i)) * s;
+            for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(v[k] >> (8 * i)) * s;
             return;
         }
-        Raw4<T> raw;
+        Raw raw;
         __builtin_memcpy(&raw, v, sizeof(raw));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = raw[i];
+        for (int i = 0; i < 4; ++i) x[i] = raw[4 * k + i];
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) v[i] = 0;
     }
     __device__ __forceinline__ void hold()                 // what is made from these words is not kept
     {
@@ -168,17 +180,25 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_fwd_kernel(const NormP
     __shared__ float s_sum[ROWS][2][1][NW];
     const int t = threadIdx.x % NT, side = threadIdx.x / NT;
     RowSum<NW, 1> sum = {s_sum[side], 0};
+    constexpr bool HELD = NCH == 1;                        // weights and the next row stay in registers
     int cnt[NCH];
-    float wpost[NCH][8], wres[NCH][8], wpre[NCH][8];
-#pragma unroll
-    for (int j = 0; j < NCH; ++j) {
+    float wpost[8], wres[8], wpre[8];
+    const auto weights = [&](int j, bool after) {
         const int c = (j * NT + t) * LANE_CH;
-        cnt[j] = max(0, min(LANE_CH, p.D - c));
-        load_weight(p.post, c, cnt[j], 1.f, wpost[j]);
-        load_weight(p.res, c, cnt[j], 1.f, wres[j]);
-        load_weight(p.pre, c, cnt[j], 0.f, wpre[j]);
+        if (!after) {
+            load_weight(p.post, c, cnt[j], 1.f, wpost);
+            load_weight(p.res, c, cnt[j], 1.f, wres);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wres[j][i] *= p.scale;
+            for (int i = 0; i < 8; ++i) wres[i] *= p.scale;
+        } else {
+            load_weight(p.pre, c, cnt[j], 0.f, wpre);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) cnt[j] = max(0, min(LANE_CH, p.D - (j * NT + t) * LANE_CH));
+    if (HELD) {
+        weights(0, false);
+        weights(0, true);
     }
     Raw8<X> xr[NCH];
     Raw8<T> yr[NCH], gr[NCH];
@@ -194,12 +214,13 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_fwd_kernel(const NormP
     };
     const float inv_d = 1.f / (float)p.D;
     const int step = gridDim.x * ROWS;
-    load(blockIdx.x * ROWS + side);
+    if (HELD) load(blockIdx.x * ROWS + side);
     // all sides stay while one has a row: sums are joined behind barriers
     for (int row0 = blockIdx.x * ROWS; row0 < p.R; row0 += step) {
         const int row = row0 + side;
         const bool in = row < p.R;
         const size_t r = min(row, p.R - 1);
+        if (!HELD) load(row);
         float x[NCH][8], u[NCH][8], g[NCH][8];
         float ss[1] = {0.f};
 #pragma unroll
@@ -210,7 +231,7 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_fwd_kernel(const NormP
                 if (p.y.p) u[j][i] = yr[j][i];
                 if (p.gate.p) g[j][i] = gr[j][i];
             }
-        if (row0 + step < p.R) load(row + step);
+        if (HELD && row0 + step < p.R) load(row + step);
         if (p.y.p) {
             float rs = 1.f;
             if (p.post) {
@@ -226,11 +247,12 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_fwd_kernel(const NormP
                 const int c = (j * NT + t) * LANE_CH, n = in ? cnt[j] : 0;
                 if (p.y8.codes) store_codes<LANE_CH>(p.y8, r, p.D, c, n, u[j]);
                 if (p.gate8.codes) store_codes<LANE_CH>(p.gate8, r, p.D, c, n, g[j]);
+                if (!HELD) weights(j, false);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float v = wpost[j][i] * (u[j][i] * rs);
+                    float v = wpost[i] * (u[j][i] * rs);
                     if (p.gate.p) v *= sigmoid2(g[j][i]).s;
-                    x[j][i] = to_f<X>(from_f<X>(x[j][i] + wres[j][i] * v));
+                    x[j][i] = to_f<X>(from_f<X>(x[j][i] + wres[i] * v));
                 }
                 if (n > 0) Raw8<X>::store((X *)p.x_out + r * p.D + c, n, x[j]);
             }
@@ -250,8 +272,9 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_fwd_kernel(const NormP
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
                 const int c = (j * NT + t) * LANE_CH;
+                if (!HELD) weights(j, true);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[j][i] = wpre[j][i] * (x[j][i] * rs);
+                for (int i = 0; i < 8; ++i) x[j][i] = wpre[i] * (x[j][i] * rs);
                 if (in && cnt[j] > 0) Raw8<T>::store((T *)p.n + r * p.D + c, cnt[j], x[j]);
             }
         }
@@ -276,20 +299,26 @@ template <int NT, int NQ> struct Quads<NT, NQ, true> {
 // Gradients.  One sum over the row is enough: with A = w_post Sigmoid(gate) s y,
 //   sum of w_post du y = sum A dx + rx sum A w_pre dn - rx^2 mx sum A x,
 // so a row has one barrier between its two looks at the values (two: 160 us for 8192 x 4096 from 8 bits).  NW waves hold a row,
-// NQ times 4 channels a lane.  With 4 the weights, their sums, a row as it is stored and the next one fit 128 registers; with 8 the
-// weights lie in LDS; with 16 two of the sums do, and the weights are read again for every row.
+// NQ times 4 channels a lane.  With 4 (up to 4096 channels) the weights, their sums, a row and the next one as it is stored fit
+// 128 registers, so that 16 waves a unit hide the sum (8 channels a lane and 8 waves: 143 us).  With 8 the weights lie in LDS, with 16 two of
+// the sums do and the weights are read again for every row; either unpacks the row's values a second time for the second look.
 template <typename T, typename X, int NW, int ROWS, int NQ>
 __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormParams p)
 {
-    constexpr int NT = 64 * NW;
-    constexpr bool AHEAD = NQ == 1;
+    constexpr int NT = 64 * NW, V = NQ == 1 ? 4 : 8, NV = 4 * NQ / V;
+    constexpr bool KEEP = NQ == 1;                         // numbers stay from look to look, the next row is on its way
     extern __shared__ __align__(16) float s_mem[];         // NQ 2: weights [3][2][NT][4]; 4: sums [2][4][NT][4]; at the end [ROWS - 1][3][NT][4]
     __shared__ float s_sum[ROWS][2][NW][8];
     const int t = threadIdx.x % NT, side = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
     RowSum6<NW> total = {s_sum[side], 0};
     const bool block = p.y.p, pre = p.pre && p.d_n, gated = p.gate.p;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    int cnt[NQ];
+    // With D a multiple of V a lane has V channels or none, and asks nothing more; else the last one goes by elements.
+    const bool whole = p.D % V == 0;
+    int cnt[NV];
+#pragma unroll
+    for (int g = 0; g < NV; ++g) cnt[g] = max(0, min(V, p.D - (g * NT + t) * V));
+    const auto channel = [&](int j) { return (unsigned)((4 * j / V * NT + t) * V + 4 * j % V); };
     Quads<NT, NQ, NQ == 2> w_post, w_res, w_pre;
     Quads<NT, NQ, NQ == 4> a_post, a_res;
     Quads<NT, NQ, false> a_pre;
@@ -299,18 +328,18 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
     w_res.begin(s_mem + 4 * NQ * NT);
     w_pre.begin(s_mem + 8 * NQ * NT);
     const auto weights = [&](int j, f32x4 &post, f32x4 &res, f32x4 &pre_) {
-        const int c = (j * NT + t) * 4;
+        const unsigned c = channel(j);
+        const int n = max(0, min(4, p.D - (int)c));
         float w[3][4] = {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}};
-        if (p.post) load_f4(p.post + c, cnt[j], w[0]);
-        if (p.res) load_f4(p.res + c, cnt[j], w[1]);
-        if (p.pre) load_f4(p.pre + c, cnt[j], w[2]);
+        if (p.post) load_f4(at_byte(p.post, 4 * c), n, w[0]);
+        if (p.res) load_f4(at_byte(p.res, 4 * c), n, w[1]);
+        if (p.pre) load_f4(at_byte(p.pre, 4 * c), n, w[2]);
         post = f32x4{w[0][0], w[0][1], w[0][2], w[0][3]};
         res = f32x4{w[1][0], w[1][1], w[1][2], w[1][3]} * p.scale;
         pre_ = f32x4{w[2][0], w[2][1], w[2][2], w[2][3]};
     };
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
-        cnt[j] = max(0, min(4, p.D - (j * NT + t) * 4));
         if (NQ <= 2) {
             f32x4 a, b, c;
             weights(j, a, b, c);
@@ -332,58 +361,74 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
         }
     };
     struct Values {
-        Held4<X> x[NQ], dx[NQ];
-        Held4<T> y[NQ], gate[NQ], dn[NQ];
+        HeldV<X, V> x[NV], dx[NV];
+        HeldV<T, V> y[NV], gate[NV], dn[NV];
     };
     Values next;
     const Rows d_n = {p.d_n, nullptr, p.D}, d_x = {p.d_x, nullptr, p.D};
+    const auto load_some = [&](size_t r, int g, int n) {
+        const unsigned c = (g * NT + t) * V;
+        if (block) next.y[g].load(p.y, r, p.D, c, n);
+        if (pre) {
+            next.x[g].load(p.x, r, p.D, c, n);
+            next.dn[g].load(d_n, r, p.D, c, n);
+        }
+        if (p.d_x) next.dx[g].load(d_x, r, p.D, c, n);
+        if (gated) next.gate[g].load(p.gate, r, p.D, c, n);
+    };
     const auto load = [&](int row) {
         const size_t r = min(row, p.R - 1);
 #pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-            const int c = (j * NT + t) * 4;
-            if (block) next.y[j].load(p.y, r, p.D, c, cnt[j]);
-            if (pre) {
-                next.x[j].load(p.x, r, p.D, c, cnt[j]);
-                next.dn[j].load(d_n, r, p.D, c, cnt[j]);
+        for (int g = 0; g < NV; ++g) {
+            if (whole) {
+                if (cnt[g] > 0) load_some(r, g, V);
+            } else {
+                load_some(r, g, cnt[g]);
             }
-            if (p.d_x) next.dx[j].load(d_x, r, p.D, c, cnt[j]);
-            if (gated) next.gate[j].load(p.gate, r, p.D, c, cnt[j]);
         }
     };
+#pragma unroll
+    for (int g = 0; g < NV; ++g) {                         // lanes without channels keep zeros
+        next.y[g].clear();
+        next.x[g].clear();
+        next.dn[g].clear();
+        next.dx[g].clear();
+        next.gate[g].clear();
+    }
     struct Floats {                                        // zeros (an open gate) where there is no such part
         float x[4], y[4], dx[4], dn[4];
         Sigmoid gate[4];
     };
     const float inv_d = 1.f / (float)p.D;
     const int step = p.parts * ROWS;
-    if (AHEAD) load(blockIdx.x * ROWS + side);
+    if (KEEP) load(blockIdx.x * ROWS + side);
     for (int row0 = blockIdx.x * ROWS; row0 < p.R; row0 += step) {
         const int row = row0 + side;
         const bool in = ROWS == 1 || row < p.R;            // a side without a row adds zeros
         const size_t r = min(row, p.R - 1);
-        if (!AHEAD) load(row);
+        if (!KEEP) load(row);
         Values now = next;
-        if (AHEAD && row0 + step < p.R) load(row + step);
+        if (KEEP && row0 + step < p.R) load(row + step);
         const auto floats = [&](int j, Floats &f) {
+            const int g = 4 * j / V, k = j - g * V / 4;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 f.x[i] = f.y[i] = f.dn[i] = f.dx[i] = 0.f;
                 f.gate[i] = Sigmoid{1.f, 0.f};
             }
             if (!in) return;
-            if (block) now.y[j].get(p.y.scales, f.y);
+            if (block) now.y[g].get(p.y.scales, k, f.y);
             if (gated) {
-                float g[4];
-                now.gate[j].get(p.gate.scales, g);
+                float z[4];
+                now.gate[g].get(p.gate.scales, k, z);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f.gate[i] = sigmoid2(g[i]);
+                for (int i = 0; i < 4; ++i) f.gate[i] = sigmoid2(z[i]);
             }
             if (pre) {
-                now.x[j].get(p.x.scales, f.x);
-                now.dn[j].get(false, f.dn);
+                now.x[g].get(p.x.scales, k, f.x);
+                now.dn[g].get(false, k, f.dn);
             }
-            if (p.d_x) now.dx[j].get(false, f.dx);
+            if (p.d_x) now.dx[g].get(false, k, f.dx);
         };
         float s[6] = {};                                   // y^2, x^2, w_pre dn x, A dx, A w_pre dn, A x
         Floats f;
@@ -402,27 +447,27 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
                 s[4] += A * d;
                 s[5] += A * f.x[i];
             }
-            if (NQ > 1) __builtin_amdgcn_sched_barrier(0);
+            if (!KEEP) __builtin_amdgcn_sched_barrier(0);
         }
         total(s);
         const float ry = p.post ? rstd_of(s[0] * inv_d + p.eps) : 1.f;
         const float rx = pre ? rstd_of(s[1] * inv_d + p.eps) : 0.f;
         const float mx = s[2] * rx * inv_d;                // mean of w_pre dn x^
         const float my = p.post ? (s[3] + rx * (s[4] - rx * mx * s[5])) * ry * inv_d : 0.f;
-        if (NQ > 1)
+        if (!KEEP)
 #pragma unroll
-            for (int j = 0; j < NQ; ++j) {
-                now.x[j].hold();
-                now.y[j].hold();
-                now.gate[j].hold();
-                now.dx[j].hold();
-                now.dn[j].hold();
+            for (int g = 0; g < NV; ++g) {
+                now.x[g].hold();
+                now.y[g].hold();
+                now.gate[g].hold();
+                now.dx[g].hold();
+                now.dn[g].hold();
             }
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const unsigned c = (j * NT + t) * 4;
-            const int n = in ? cnt[j] : 0;
-            if (NQ > 1) {
+            const unsigned c = channel(j);
+            const int n = in ? max(0, min(4, p.D - (int)c)) : 0;
+            if (!KEEP) {
                 weight(j, wpost, wres, wpre);
                 floats(j, f);
             }
@@ -442,12 +487,15 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
             a_pre.put(j, sum);
             a_post.put(j, post);
             a_res.put(j, res);
+            const auto store = [&](int m) {
+                Raw4<X>::store(at_byte((X *)p.dx + r * p.D, c * sizeof(X)), m, G);
+                if (block) Raw4<T>::store(at_byte((T *)p.dy + r * p.dy_stride, c * sizeof(T)), m, dy);
+                if (gated) Raw4<T>::store(at_byte((T *)p.dgate + r * p.dgate_stride, c * sizeof(T)), m, dgate);
+            };
             if (n > 0) {
-                Raw4<X>::store(at_byte((X *)p.dx + r * p.D, c * sizeof(X)), n, G);
-                if (block) Raw4<T>::store(at_byte((T *)p.dy + r * p.dy_stride, c * sizeof(T)), n, dy);
-                if (gated) Raw4<T>::store(at_byte((T *)p.dgate + r * p.dgate_stride, c * sizeof(T)), n, dgate);
+                if (whole) store(4); else store(n);
             }
-            if (NQ > 1) __builtin_amdgcn_sched_barrier(0);
+            if (!KEEP) __builtin_amdgcn_sched_barrier(0);
         }
     }
 #pragma unroll
@@ -469,18 +517,18 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
     }
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
-        const int c = (j * NT + t) * 4;
-        if (cnt[j] == 0) continue;
+        const unsigned c = channel(j);
+        const int n = max(0, min(4, p.D - (int)c));
+        if (n == 0) continue;
         float *at = p.part + (size_t)blockIdx.x * p.D + c;
         const size_t other = (size_t)p.parts * p.D;
-        const auto put = [&](const auto &sums, float *to) {
-            const f32x4 q = sums.get(j);
+        const auto put = [&](f32x4 q, float *to) {
             const float v[4] = {q[0], q[1], q[2], q[3]};
-            Raw4<float>::store(to, cnt[j], v);
+            Raw4<float>::store(to, n, v);
         };
-        if (p.dpost) put(a_post, at);
-        if (p.dres) put(a_res, at + other);
-        if (p.dpre) put(a_pre, at + 2 * other);
+        if (p.dpost) put(a_post.get(j), at);
+        if (p.dres) put(a_res.get(j), at + other);
+        if (p.dpre) put(a_pre.get(j), at + 2 * other);
     }
 }
 
