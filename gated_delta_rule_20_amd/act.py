@@ -38,12 +38,19 @@ def _scale_shape(shape):
     return (*shape[:-1], (shape[-1] + ACT_GROUP - 1) // ACT_GROUP)
 
 
+def _good(t, device, dtype, shape) -> bool:
+    """Whether t is a dense tensor of this kind: a small call's time is mostly the host's, so the good case is one line."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()
+
+
 def _new_packed(shape, device):
     return Packed(torch.empty(shape, dtype=torch.int8, device=device),
                   torch.empty(_scale_shape(shape), dtype=torch.float32, device=device))
 
 
 def _check_packed(p, name, shape, device):
+    if _good(p.codes, device, torch.int8, shape) and _good(p.scales, device, torch.float32, _scale_shape(shape)) and device.type == "cuda":
+        return
     _required(device, torch.int8, **{f"{name}.codes": p.codes})
     _required(device, torch.float32, **{f"{name}.scales": p.scales})
     if tuple(p.codes.shape) != tuple(shape) or tuple(p.scales.shape) != _scale_shape(shape):
@@ -87,6 +94,8 @@ def _row_stride(t, name):
 
 def _rows(t, name, device, dtype, shape):
     """Checks a tensor of rows of any stride; returns (address, stride)."""
+    if _good(t, device, dtype, shape) and device.type == "cuda":
+        return t.data_ptr(), shape[-1]
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise ValueError(f"{name} must be a device tensor")
     if t.device != device:

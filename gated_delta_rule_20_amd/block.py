@@ -16,7 +16,7 @@ from typing import NamedTuple
 import torch
 
 from . import _DTYPES, BlockNormBwdArgs, BlockNormFwdArgs
-from .act import Packed, _packed_out, _rows, _saved, _two
+from .act import Packed, _good, _packed_out, _rows, _saved, _two
 from .linear import _at, _call, _check_tensors, _like, _need, _on_stream, _required, _workspace
 
 
@@ -36,12 +36,15 @@ class BlockNormSaved(NamedTuple):
     gate: Packed | None
 
 
-def _weights(D, device, **weights):
-    for name, w in weights.items():
-        if w is not None:
+def _weights(device, shape, post_weight, res_scale, pre_weight):
+    """Checks the weights, each [D]; returns their addresses."""
+    shape = shape[-1:]
+    for name, w in (("post_weight", post_weight), ("res_scale", res_scale), ("pre_weight", pre_weight)):
+        if w is not None and not _good(w, device, torch.float32, shape):
             _check_tensors(device, torch.float32, **{name: w})
-            if w.shape != (D,):
-                raise ValueError(f"{name} must be [D] = [{D}], got {tuple(w.shape)}")
+            if w.shape != shape:
+                raise ValueError(f"{name} must be [D] = {list(shape)}, got {tuple(w.shape)}")
+    return _at(post_weight), _at(res_scale), _at(pre_weight)
 
 
 def _stream_rows(x, name):
@@ -49,7 +52,8 @@ def _stream_rows(x, name):
         raise ValueError(f"{name} must be a device tensor [..., D]")
     if x.dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {x.dtype}")
-    _required(x.device, x.dtype, **{name: x})
+    if not x.is_cuda or not x.is_contiguous():
+        _required(x.device, x.dtype, **{name: x})
 
 
 @_on_stream
@@ -71,19 +75,19 @@ def block_norm_fwd(x, y=None, *, gate=None, post_weight=None, res_scale=None, sc
         dtype = x.dtype if n_out is None else n_out.dtype
     if dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {dtype}")
-    a = BlockNormFwdArgs(R, D, _DTYPES[dtype], _DTYPES[x.dtype], x.data_ptr(), y_stride=D, gate_stride=D, scale=scale, eps=eps)
+    y_at = x_out_at = gate_at = None
+    y_stride = gate_stride = D
     if y is not None:
-        a.y, a.y_stride = _rows(y, "y", dev, dtype, shape)
+        y_at, y_stride = _rows(y, "y", dev, dtype, shape)
         x_out = _like(x_out, "x_out", x)
-        a.x_out = x_out.data_ptr()
+        x_out_at = x_out.data_ptr()
     elif x_out is not None:
         raise ValueError("x_out without y: there is no new residual stream")
     else:
         x_out = x
     if gate is not None:
-        a.gate, a.gate_stride = _rows(gate, "gate", dev, dtype, shape)
-    _weights(D, dev, post_weight=post_weight, res_scale=res_scale, pre_weight=pre_weight)
-    a.post_weight, a.res_scale, a.pre_weight = _at(post_weight), _at(res_scale), _at(pre_weight)
+        gate_at, gate_stride = _rows(gate, "gate", dev, dtype, shape)
+    weights = _weights(dev, shape, post_weight, res_scale, pre_weight)
     n = None
     if pre_weight is not None:
         if n_out is None:
@@ -93,7 +97,8 @@ def block_norm_fwd(x, y=None, *, gate=None, post_weight=None, res_scale=None, sc
             if n_out.shape != shape:
                 raise ValueError(f"n_out must be {tuple(shape)}, got {tuple(n_out.shape)}")
             n = n_out
-        a.n = n.data_ptr()
+    a = BlockNormFwdArgs(R, D, _DTYPES[dtype], _DTYPES[x.dtype], x.data_ptr(), y_at, y_stride, gate_at, gate_stride, *weights,
+                         scale, eps, x_out_at, _at(n))
     saved = None
     if pack is not None and pack is not False:
         given = pack if isinstance(pack, BlockNormSaved) else (True, y is not None, gate is not None)
@@ -137,41 +142,46 @@ def block_norm_bwd(x_new, y, dx_new, dn=None, *, gate=None, post_weight=None, re
         raise ValueError("gate, post_weight and res_scale belong to y, which is None")
     if dn is not None and pre_weight is None:
         raise ValueError("dn without pre_weight")
-    a = BlockNormBwdArgs(R, D, _DTYPES[dtype], _DTYPES[x_dtype], y_stride=D, gate_stride=D, scale=scale, eps=eps, dy_stride=D,
-                         dgate_stride=D)
+    x_at = x_scales = y_at = y_scales = gate_at = gate_scales = dy_at = dgate_at = None
+    y_stride = gate_stride = dy_stride = dgate_stride = D
     if dn is not None:
         _check_tensors(dev, dtype, dn=dn)
         if dn.shape != shape:
             raise ValueError(f"dn must be {tuple(shape)}, got {tuple(dn.shape)}")
-        a.d_n = dn.data_ptr()
         if isinstance(x_new, Packed):
-            a.x_new, _, a.x_scales = _saved(x_new, "x_new", dev, x_dtype, shape)
+            x_at, _, x_scales = _saved(x_new, "x_new", dev, x_dtype, shape)
         else:
-            _required(dev, x_dtype, x_new=x_new)
-            if x_new.shape != shape:
-                raise ValueError(f"x_new must be {tuple(shape)}, got {tuple(x_new.shape)}")
-            a.x_new = x_new.data_ptr()
-    a.d_x_new = _at(dx_new)
+            if not _good(x_new, dev, x_dtype, shape):
+                _required(dev, x_dtype, x_new=x_new)
+                if x_new.shape != shape:
+                    raise ValueError(f"x_new must be {tuple(shape)}, got {tuple(x_new.shape)}")
+            x_at = x_new.data_ptr()
     if dx is None:
         dx = torch.empty(shape, dtype=x_dtype, device=dev)
     else:
         _check_tensors(dev, x_dtype, dx=dx)
         if dx.shape != shape:
             raise ValueError(f"dx must be {tuple(shape)}, got {tuple(dx.shape)}")
-    a.dx = dx.data_ptr()
     dy, dgate = (dy if y is not None else None), (dgate if gate is not None else None)
     if y is not None:
-        a.y, a.y_stride, a.y_scales = _saved(y, "y", dev, dtype, shape)
-        dy = torch.empty(shape, dtype=dtype, device=dev) if dy is None else dy
-        a.dy, a.dy_stride = _rows(dy, "dy", dev, dtype, shape)
+        y_at, y_stride, y_scales = _saved(y, "y", dev, dtype, shape)
+        if dy is None:
+            dy = torch.empty(shape, dtype=dtype, device=dev)
+            dy_at = dy.data_ptr()
+        else:
+            dy_at, dy_stride = _rows(dy, "dy", dev, dtype, shape)
     if gate is not None:
-        a.gate, a.gate_stride, a.gate_scales = _saved(gate, "gate", dev, dtype, shape)
-        dgate = torch.empty(shape, dtype=dtype, device=dev) if dgate is None else dgate
-        a.dgate, a.dgate_stride = _rows(dgate, "dgate", dev, dtype, shape)
-    _weights(D, dev, post_weight=post_weight, res_scale=res_scale, pre_weight=pre_weight)
-    a.post_weight, a.res_scale, a.pre_weight = _at(post_weight), _at(res_scale), _at(pre_weight)
+        gate_at, gate_stride, gate_scales = _saved(gate, "gate", dev, dtype, shape)
+        if dgate is None:
+            dgate = torch.empty(shape, dtype=dtype, device=dev)
+            dgate_at = dgate.data_ptr()
+        else:
+            dgate_at, dgate_stride = _rows(dgate, "dgate", dev, dtype, shape)
+    weights = _weights(dev, shape, post_weight, res_scale, pre_weight)
     grads = [torch.empty_like(w) if w is not None and need_dweights else None for w in (post_weight, res_scale, pre_weight)]
-    a.d_post_weight, a.d_res_scale, a.d_pre_weight = map(_at, grads)
+    a = BlockNormBwdArgs(R, D, _DTYPES[dtype], _DTYPES[x_dtype], x_at, x_scales, y_at, y_stride, y_scales, gate_at, gate_stride,
+                         gate_scales, *weights, scale, eps, _at(dx_new), _at(dn), dx.data_ptr(), dy_at, dy_stride, dgate_at,
+                         dgate_stride, *map(_at, grads))
     workspace = _workspace("kda_block_norm_bwd_workspace_size", a, workspace, dev)
     _call("kda_block_norm_bwd", (ctypes.byref(a),), dev)
     return BlockNormGrads(dx, dy, dgate, *grads)

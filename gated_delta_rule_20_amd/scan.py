@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import _DTYPES, GatedScanBwdArgs, GatedScanFwdArgs, GatedScanStepArgs
-from .act import Packed, _packed_out, _rows, _saved
+from .act import Packed, _good, _packed_out, _rows, _saved
 from .linear import _at, _call, _check_tensors, _like, _need, _on_stream, _required, _workspace
 
 
@@ -23,7 +23,7 @@ def _decay(g, name, dtype, shape, A_log, device):
         raise ValueError(f"{name} must be a device tensor")
     if g.dtype is not dtype and g.dtype is not torch.float32:
         raise ValueError(f"{name} must be {dtype} or torch.float32, got {g.dtype}")
-    if A_log is not None:
+    if A_log is not None and not _good(A_log, device, torch.float32, shape[-1:]):
         _check_tensors(device, torch.float32, A_log=A_log)
         if A_log.shape != (shape[-1],):
             raise ValueError(f"A_log must be [C] = [{shape[-1]}], got {tuple(A_log.shape)}")
@@ -49,7 +49,7 @@ def _tokens(t, name, cu_seqlens):
 
 
 def _state(t, name, shape, device):
-    if t is not None:
+    if t is not None and not _good(t, device, torch.float32, shape):
         _check_tensors(device, torch.float32, **{name: t})
         if t.shape != shape:
             raise ValueError(f"{name} must be [N, C] = {shape}, got {tuple(t.shape)}")
@@ -106,7 +106,8 @@ def gated_scan_bwd(x, g, h, d_h, *, A_log=None, g_min: float = -5.0, complement:
     ``need_dg``."""
     B, T, C, N = _tokens(d_h, "d_h", cu_seqlens)
     dev, dtype, rows, shape = d_h.device, d_h.dtype, d_h.shape, (N, C)
-    _required(dev, dtype, d_h=d_h)
+    if not d_h.is_contiguous():
+        _required(dev, dtype, d_h=d_h)
     g_at, g_stride, g_dtype = _decay(g, "g", dtype, rows, A_log, dev)
     x_at, x_stride, x_scales = None, C, None
     h_at, h_scales = None, None
@@ -114,10 +115,11 @@ def gated_scan_bwd(x, g, h, d_h, *, A_log=None, g_min: float = -5.0, complement:
         if isinstance(h, Packed):
             h_at, _, h_scales = _saved(h, "h", dev, dtype, rows)
         else:
-            _required(dev, dtype, h=h)
-            if h.shape != rows:
-                raise ValueError(f"h must have d_h's shape {tuple(rows)}, got {tuple(h.shape)}")
-            h_at = _at(h)
+            if not _good(h, dev, dtype, rows):
+                _required(dev, dtype, h=h)
+                if h.shape != rows:
+                    raise ValueError(f"h must have d_h's shape {tuple(rows)}, got {tuple(h.shape)}")
+            h_at = h.data_ptr()
         if complement:
             x_at, x_stride, x_scales = _saved(x, "x", dev, dtype, rows)
     _state(initial_state, "initial_state", shape, dev)
