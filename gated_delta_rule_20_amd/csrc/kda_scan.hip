@@ -349,13 +349,17 @@ template <typename T> struct Held {
     }
 };
 
+// How a backward call's saved activations are stored: known to the kernel they take half the registers of either case.
+enum Saved { ELEMENTS, CODES, EITHER };
+template <Saved S> __device__ __forceinline__ bool is_packed(const Rows &m) { return S == CODES || (S == EITHER && m.scales); }
+
 // The lane's rows of the segment from row r0 on, or (BEFORE) the rows before them, where there is one.
-template <bool BEFORE, typename T>
+template <bool BEFORE, Saved S, typename T>
 __device__ __forceinline__ void load_held(Held<T> *to, const Window &w, const Rows &m, int r0, int c0, int C)
 {
     const int base = BEFORE && r0 > 0 ? r0 - 1 : r0, skip = BEFORE && r0 == 0;
     const unsigned stride = (unsigned)m.stride;
-    if (m.scales) {
+    if (is_packed<S>(m)) {
         const int8_t *codes = (const int8_t *)m.p + (size_t)base * m.stride + c0;
         const float *scales = m.scales + (size_t)base * act_groups(C) + c0 / ACT_GROUP;
 #pragma unroll
@@ -416,6 +420,14 @@ template <bool GATED> struct Gates {
 
 struct Yes { static constexpr bool on = true; };
 struct No { static constexpr bool on = false; };
+
+// What is made from these words is not kept.
+template <typename R> __device__ __forceinline__ void hold(R &raw)
+{
+    static_assert(sizeof(R) % 4 == 0, "whole registers");
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(R) / 4); ++i) asm volatile("" : "+v"(reinterpret_cast<uint32_t *>(&raw)[i]));
+}
 
 // The segment a workgroup takes of its column of channels, by a ticket of that column; false: none (never, unless another call
 // writes to this call's workspace).
@@ -518,7 +530,8 @@ template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bo
 }
 
 // Gradients, from the last row to the first: D_t = d_h_t + e_{t+1}, e_t = a_t D_t; runs, segments and their order mirrored.
-template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(const ScanParams p)
+template <typename T, typename G, bool GATED, bool CHAIN, Saved S>
+__global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 : 2) void scan_bwd_kernel(const ScanParams p)
 {
     __shared__ Joined s;
     __shared__ Marks m;
@@ -574,10 +587,16 @@ template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bo
         put_run(s, run, l, !free.on && last != 0, g, e);
     };
     if (plain) pass(Yes{}); else pass(No{});
+    // the second pass unpacks them again: 16 bits a value instead of 32 while the segment waits
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+        hold(d[i]);
+        hold(z[i]);
+    }
     Held<T> hs[RUN], xs[RUN];
     if (p.dg && p.rows > 0) {
-        load_held<true>(hs, win, p.hs, r0, c0, p.C);
-        if (p.complement) load_held<false>(xs, win, p.x, r0, c0, p.C);
+        load_held<true, S>(hs, win, p.hs, r0, c0, p.C);
+        if (p.complement) load_held<false, S>(xs, win, p.x, r0, c0, p.C);
     }
     join_runs<CHAIN, true>(p, q, c0, m.last[SCAN_ROWS - 1] < 0, s);
     state_of_run<CHAIN>(s, run, l, e);
@@ -603,7 +622,7 @@ template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bo
                 if (free.on) Raw4<T>::store(to_x.at(), CH, out); else win.put(to_x.at(), out);
                 if (p.dg) {
                     float prev[CH];
-                    hs[i].get(p.hs.scales, prev);
+                    hs[i].get(is_packed<S>(p.hs), prev);
                     if (!free.on && (first >> i & 1)) {
                         if (p.h0)
                             load_f4(p.h0 + (size_t)m.first[run * RUN + i] * p.C + c, win.n, prev);
@@ -612,7 +631,7 @@ template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bo
                             for (int j = 0; j < CH; ++j) prev[j] = 0.f;
                     }
                     if (p.complement) {
-                        xs[i].get(p.x.scales, out);
+                        xs[i].get(is_packed<S>(p.x), out);
 #pragma unroll
                         for (int j = 0; j < CH; ++j) prev[j] -= out[j];
                     }
@@ -735,8 +754,15 @@ template <typename T, typename G> static hipError_t launch_bwd_t(ScanParams p, h
     const hipError_t e = launch_clear(p, p.dhT, stream);
     if (e != hipSuccess) return e;
     if (p.state_copy) p.dhT = p.state_copy;
-    const auto kernel = p.A_log ? p.chain.words ? scan_bwd_kernel<T, G, true, true> : scan_bwd_kernel<T, G, true, false>
-                                : p.chain.words ? scan_bwd_kernel<T, G, false, true> : scan_bwd_kernel<T, G, false, false>;
+    const bool packed = p.hs.scales, both = !p.dg || !p.complement || packed == (p.x.scales != nullptr);
+    const auto kernel = p.A_log ? !p.chain.words   ? scan_bwd_kernel<T, G, true, false, EITHER>
+                                  : !both          ? scan_bwd_kernel<T, G, true, true, EITHER>
+                                  : packed         ? scan_bwd_kernel<T, G, true, true, CODES>
+                                                   : scan_bwd_kernel<T, G, true, true, ELEMENTS>
+                        : !p.chain.words ? scan_bwd_kernel<T, G, false, false, EITHER>
+                        : !both          ? scan_bwd_kernel<T, G, false, true, EITHER>
+                        : packed         ? scan_bwd_kernel<T, G, false, true, CODES>
+                                         : scan_bwd_kernel<T, G, false, true, ELEMENTS>;
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
     if (p.dA)
         hipLaunchKernelGGL(scan_sum_kernel, dim3((p.C + 15) / 16), dim3(256), 0, stream, p.dA_part, p.chain.segments, p.C, p.dA);
