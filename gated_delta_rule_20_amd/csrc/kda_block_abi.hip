@@ -88,8 +88,8 @@ kda_status_t check_decay(int C, const float *A_log, float g_min)
 {
     if (C < 1 || C > (1 << 24)) return fail(KDA_ERROR_INVALID_VALUE, "need 1 <= C <= 2^24 (got %d)", C);
     KDA_TRY(check_array(A_log, 4, "A_log"));
-    if (A_log && !(g_min < 0.f && g_min - g_min == 0.f))
-        return fail(KDA_ERROR_INVALID_VALUE, "g_min must be finite and below 0 (got %g)", (double)g_min);
+    if (A_log && !(g_min < 0.f && g_min >= -1e6f))
+        return fail(KDA_ERROR_INVALID_VALUE, "g_min must be below 0 and -1e6 at least (got %g)", (double)g_min);
     return KDA_SUCCESS;
 }
 

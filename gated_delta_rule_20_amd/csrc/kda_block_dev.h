@@ -263,16 +263,17 @@ __device__ __forceinline__ double column_sum(const float *part, int rows, int C,
 }
 
 // A decay e^x (x <= 0, and -0 for 0) kept as one number w: e^x - 1, its sign set, where x > -0.1 (to its own last
-// place: the series to x^5 leaves x^5 / 720 < 2^-25); else e^x, its sign clear.  A state that fades over
-// 10^4 tokens would carry 10^4 times the rounding of e^x itself.
+// place: the cubic is within 1.3e-8 < 2^-25 of (e^x - 1) / x there, fitted to the least largest error); else e^x, its sign clear.
+// A state that fades over 10^4 tokens would carry 10^4 times the rounding of e^x itself.
 struct Decay {
     float w;
     bool near;
 };
+constexpr float NEAR = -0.1f, NEAR1 = 0.4999980032444f, NEAR2 = 0.16656582057476044f, NEAR3 = 0.040039222687482834f;
 __device__ __forceinline__ Decay decay_of(float x)
 {
-    const float m = x * __builtin_fmaf(x, __builtin_fmaf(x, __builtin_fmaf(x, __builtin_fmaf(x, 1.f / 120, 1.f / 24), 1.f / 6), 0.5f), 1.f);
-    const bool near = x > -0.1f;
+    const float m = x * __builtin_fmaf(x, __builtin_fmaf(x, __builtin_fmaf(x, NEAR3, NEAR2), NEAR1), 1.f);
+    const bool near = x > NEAR;
     return {near ? m : __builtin_amdgcn_exp2f(x * LOG2E), near};
 }
 // A log-decay above 0 counts as 0; NaN passes.
@@ -289,14 +290,15 @@ __device__ __forceinline__ Decay decay_product(Decay a, Decay b)
     const bool near = a.near && b.near;
     return near && t < -0.5f ? Decay{1.f + t, false} : Decay{near ? -__builtin_fabsf(t) : t, near};  // (-0 for 1)
 }
-// A token's value times 1 - e^x with complement, else as it is.
-struct Share {
-    bool complement;
-    __device__ __forceinline__ explicit Share(bool c) : complement(c) {}
-    __device__ __forceinline__ float operator()(Decay d, float x) const
-    {
-        return complement ? __builtin_fmaf(-d.w, x, d.near ? 0.f : x) : x;
-    }
-};
+// What a token's value is multiplied by: 1 - e^x with complement, else 1.
+__device__ __forceinline__ float share_of(Decay d, float x, bool complement)
+{
+    return complement ? __builtin_fmaf(-d.w, x, d.near ? 0.f : x) : x;
+}
+// One token: e^x h + v, or with complement e^x h + (1 - e^x) v = v + e^x (h - v).
+__device__ __forceinline__ float decay_step(Decay d, float h, float v, bool complement)
+{
+    return complement ? __builtin_fmaf(d.w, h - v, d.near ? h : v) : decay_apply(d, h, v);
+}
 
 }  // namespace kda

@@ -389,26 +389,41 @@ __device__ __forceinline__ void load_held(Held<T> *to, const Window &w, const Ro
     }
 }
 
-// A channel's gate (eq. (5)), or log-decays as they are.
+// A channel's gate (eq. (5)), or log-decays as they are.  The decay is made from u = Sigmoid(exp(A) z), of which the
+// log-decay is g_min times, or from the log-decay itself.
 template <bool GATED> struct Gates {
     float k[CH];                                            // -e^A log2(e)
-    __device__ __forceinline__ void load(const Window &win, const float *A_log, int c0)
+    float c0, c1, c2, c3, border, to_log2;                  // decay_of's, for u (uniform)
+    __device__ __forceinline__ void load(const Window &win, const float *A_log, int c0_)
     {
         if (!GATED) return;
         Raw4<float> raw;
-        if (win.vec) raw.load(A_log + c0 + win.col, CH); else raw.load(A_log + c0 + win.col, win.n);
+        if (win.vec) raw.load(A_log + c0_ + win.col, CH); else raw.load(A_log + c0_ + win.col, win.n);
 #pragma unroll
         for (int j = 0; j < CH; ++j) k[j] = raw[j];
     }
-    __device__ __forceinline__ void make()
+    __device__ __forceinline__ void make(float g_min)
     {
-        if (GATED)
+        if (!GATED) return;
 #pragma unroll
-            for (int j = 0; j < CH; ++j) k[j] = __expf(k[j]) * -LOG2E;
+        for (int j = 0; j < CH; ++j) k[j] = __expf(k[j]) * -LOG2E;
+        c0 = g_min;
+        c1 = NEAR1 * g_min * g_min;
+        c2 = NEAR2 * g_min * g_min * g_min;
+        c3 = NEAR3 * (g_min * g_min) * (g_min * g_min);
+        border = NEAR / g_min;
+        to_log2 = g_min * LOG2E;
     }
-    __device__ __forceinline__ float log_decay(float z, int j, float g_min) const
+    __device__ __forceinline__ float open(float z, int j) const
     {
-        return GATED ? g_min * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * k[j])) : not_above_0(z);
+        return GATED ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * k[j])) : not_above_0(z);
+    }
+    __device__ __forceinline__ Decay decay(float u) const
+    {
+        if (!GATED) return decay_of(u);
+        const float m = u * __builtin_fmaf(u, __builtin_fmaf(u, __builtin_fmaf(u, c3, c2), c1), c0);
+        const bool near = u < border;
+        return {near ? m : __builtin_amdgcn_exp2f(u * to_log2), near};
     }
     // d log_decay / d z, but for g_min e^A
     __device__ __forceinline__ float slope(float z, int j) const
@@ -454,7 +469,7 @@ template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bo
     if (!take_segment<CHAIN>(p, column, s, &q)) return;
     const int l = threadIdx.x % LANES, run = threadIdx.x / LANES, r0 = q * SCAN_ROWS, c = c0 + l * CH;
     const Window win(p, r0, c0);
-    const Share share(p.complement);
+    const bool complement = p.complement;
     const Offsets offsets(p, r0);
     Gates<GATED> gates;
     gates.load(win, p.A_log, c0);
@@ -465,7 +480,7 @@ template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bo
         win.load<G>(z, (const G *)p.g.p + (size_t)r0 * p.g.stride + c0, p.g.stride);
     }
     mark_rows(p, offsets, r0, q == p.chain.segments - 1, m, p.h0, p.hT, c0);
-    gates.make();
+    gates.make(p.g_min);
     const bool plain = m.any == 0 && r0 >= offsets.begin && r0 + SCAN_ROWS <= offsets.end && win.full;
     unsigned first = 0, last = 0, rows = 0;
     if (!plain) {
@@ -480,7 +495,7 @@ template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bo
 #pragma unroll
             for (int j = 0; j < CH; ++j) h[j] = 0.f;
     };
-    float w[RUN][CH], b[RUN][CH], h[CH] = {};
+    float w[RUN][CH], v[RUN][CH], h[CH] = {};
     const auto pass = [&](auto free) {
         float g[CH] = {};
 #pragma unroll
@@ -491,14 +506,17 @@ template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bo
             }
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const float v = gates.log_decay(z[i][j], j, p.g_min);
-                const Decay d = decay_of(v);
+                const float u = gates.open(z[i][j], j);
+                const Decay d = gates.decay(u);
                 w[i][j] = d.w;
-                g[j] += v;
-                b[i][j] = share(d, x[i][j]);
-                h[j] = decay_apply(d, h[j], b[i][j]);
+                g[j] += u;
+                v[i][j] = x[i][j];
+                h[j] = decay_step(d, h[j], v[i][j], complement);
             }
         }
+        if (GATED)
+#pragma unroll
+            for (int j = 0; j < CH; ++j) g[j] *= p.g_min;
         put_run(s, run, l, !free.on && first != 0, g, h);
     };
     if (plain) pass(Yes{}); else pass(No{});
@@ -512,15 +530,15 @@ template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bo
             if (!free.on && (first >> i & 1)) begin(i, h);
             if (in) {
 #pragma unroll
-                for (int j = 0; j < CH; ++j) h[j] = decay_apply(decay_held(w[i][j]), h[j], b[i][j]);
+                for (int j = 0; j < CH; ++j) h[j] = decay_step(decay_held(w[i][j]), h[j], v[i][j], complement);
                 if (free.on) Raw4<T>::store(out.at(), CH, h); else win.put(out.at(), h);
             }
             out.up();
             if (p.h8.codes) {
-                float v[CH];
+                float o[CH];
 #pragma unroll
-                for (int j = 0; j < CH; ++j) v[j] = free.on || j < win.n ? to_f<T>(from_f<T>(h[j])) : 0.f;
-                store_codes<CH>(p.h8, r0 + win.row0 + i, p.C, c, free.on ? CH : in ? win.n : 0, v);
+                for (int j = 0; j < CH; ++j) o[j] = free.on || j < win.n ? to_f<T>(from_f<T>(h[j])) : 0.f;
+                store_codes<CH>(p.h8, r0 + win.row0 + i, p.C, c, free.on ? CH : in ? win.n : 0, o);
             }
             if (!free.on && (last >> i & 1) && p.hT && win.n > 0)
                 Raw4<float>::store(p.hT + (size_t)m.last[run * RUN + i] * p.C + c, win.n, h);
@@ -540,7 +558,7 @@ __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 
     if (!take_segment<CHAIN>(p, column, s, &q)) return;
     const int l = threadIdx.x % LANES, run = threadIdx.x / LANES, r0 = (p.chain.segments - 1 - q) * SCAN_ROWS, c = c0 + l * CH;
     const Window win(p, r0, c0);
-    const Share share(p.complement);
+    const bool complement = p.complement;
     const Offsets offsets(p, r0);
     Gates<GATED> gates;
     gates.load(win, p.A_log, c0);
@@ -551,7 +569,7 @@ __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 
         win.load<G>(z, (const G *)p.g.p + (size_t)r0 * p.g.stride + c0, p.g.stride);
     }
     mark_rows(p, offsets, r0, q == 0, m, p.dhT, p.dh0, c0);
-    gates.make();
+    gates.make(p.g_min);
     const bool plain = m.any == 0 && r0 >= offsets.begin && r0 + SCAN_ROWS <= offsets.end && win.full;
     unsigned first = 0, last = 0, rows = 0;
     if (!plain) {
@@ -577,13 +595,16 @@ __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 
             }
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const float v = gates.log_decay(z[i][j], j, p.g_min);
-                const Decay k = decay_of(v);
+                const float u = gates.open(z[i][j], j);
+                const Decay k = gates.decay(u);
                 w[i][j] = k.w;
-                g[j] += v;
+                g[j] += u;
                 e[j] = decay_times(k, d[i][j] + e[j]);
             }
         }
+        if (GATED)
+#pragma unroll
+            for (int j = 0; j < CH; ++j) g[j] *= p.g_min;
         put_run(s, run, l, !free.on && last != 0, g, e);
     };
     if (plain) pass(Yes{}); else pass(No{});
@@ -617,7 +638,7 @@ __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 
                     const Decay k = decay_held(w[i][j]);
                     const float D = d[i][j] + e[j];
                     e[j] = decay_times(k, D);
-                    out[j] = share(k, D);
+                    out[j] = share_of(k, D, complement);
                 }
                 if (free.on) Raw4<T>::store(to_x.at(), CH, out); else win.put(to_x.at(), out);
                 if (p.dg) {
@@ -704,7 +725,7 @@ template <typename T, typename G> __global__ __launch_bounds__(256) void scan_st
     if (cnt == 0) return;
     float h[8];
     if (mine) {
-        const Share share(p.complement);
+        const bool complement = p.complement;
         Raw8<T> x;
         Raw8<G> g;
         float A[8];
@@ -715,7 +736,7 @@ template <typename T, typename G> __global__ __launch_bounds__(256) void scan_st
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const Decay d = decay_of(p.A_log ? p.g_min * sigmoid2(__expf(A[i]) * g[i]).s : not_above_0(g[i]));
-            h[i] = decay_apply(d, h[i], share(d, x[i]));
+            h[i] = decay_step(d, h[i], x[i], complement);
         }
         Raw8<float>::store(p.new_state + (size_t)slot * p.C + c, cnt, h);
     } else {

@@ -524,7 +524,7 @@ KDA_API kda_status_t kda_act_unpack(int32_t dtype, const int8_t *codes, const fl
  *   x, h : [B, T, C] of dtype      g : [B, T, C] of g_dtype (dtype or KDA_F32)
  * Decays: with A_log NULL g holds log-decays (above 0 they count as 0; -inf
  * forgets the state); with A_log [C] float32 it holds logits z, and eq. (5) is applied,
- * g_t = g_min Sigmoid(exp(A_log) z_t), g_min finite and below 0.
+ * g_t = g_min Sigmoid(exp(A_log) z_t), g_min in [-1e6, 0).
  * cu_seqlens / N, initial_state, final_state as for kda_chunk_fwd, with states
  * [N, C] float32 (final_state may alias initial_state).  Rows of h outside
  * every sequence are left as they were.
