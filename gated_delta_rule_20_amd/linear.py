@@ -173,13 +173,25 @@ def linear_chunk_fwd(q, k, v, g, *, scale: float = 1.0, cu_seqlens=None, initial
     return out, final_state
 
 
+def _unpacked(t, like):
+    """A saved activation as a tensor: one kept in 8 bits is unpacked to the type of ``like``."""
+    if not isinstance(t, tuple):
+        return t
+    from .act import Packed, act_unpack            # (that module builds on this one)
+    if not isinstance(t, Packed) or not isinstance(like, torch.Tensor):
+        raise ValueError("q, k and v must be device tensors or Packed, d_o a device tensor")
+    return act_unpack(t, dtype=like.dtype)
+
+
 @_on_stream
 def linear_chunk_bwd(q, k, v, g, d_o, *, scale: float = 1.0, cu_seqlens=None, initial_state=None, dfinal_state=None,
                      need_dg: bool = True, dq=None, dk=None, dv=None, dg=None, dinitial_state=None, workspace=None):
     """Gradients of :func:`linear_chunk_fwd` (``kda_linear_chunk_bwd``) for the same arguments, given ``d_o`` (shaped
-    like o, in its dtype) and ``dfinal_state`` ([N, H, Dk, Dv] fp32, None: zeros).  Returns (dq, dk, dv, dg, dinitial_state):
+    like o, in its dtype) and ``dfinal_state`` ([N, H, Dk, Dv] fp32, None: zeros).  q, k, v: tensors, or the :class:`Packed`
+    that the forward pass kept of them (unpacked to d_o's dtype first).  Returns (dq, dk, dv, dg, dinitial_state):
     the first three shaped and typed like q, k, v; dg fp32 shaped like g (None without ``need_dg``).  With ``need_dg`` dq and
     dk of bf16 calls take the state unrounded, without it rounded once, so their last bits differ."""
+    q, k, v = _unpacked(q, d_o), _unpacked(k, d_o), _unpacked(v, d_o)
     H, Hk, Dk, Dv, per_head = _heads(q, k, v, g)
     B, T, N = _sequences(q, v, cu_seqlens)
     dev, shape = q.device, (N, H, Dk, Dv)

@@ -382,6 +382,29 @@ def test_repeats_bit_for_bit_streams_and_graph():
         assert all(torch.equal(a, b) for a, b in zip(kept, both())), i
 
 
+def test_calls_at_once():
+    """Calls on several streams, each with its own workspace, wait for their own segments only; one caller's workspace serves calls
+    that follow one another, of other sizes too."""
+    kda = _kda()
+    sizes = [(6000, 384), (3000, 1024), (9000, 130), (20000, 64)]
+    data = [_inputs((T,), C, BF, BF, True, False, seed=T) for T, C in sizes]
+    call = lambda d, **kw: kda.gated_scan_fwd(d["x"], d["g"], A_log=d["A"], cu_seqlens=d["cu_dev"], **kw)  # noqa: E731
+    want = [call(d) for d in data]
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [call(d, stream=s) for d, s in zip(data, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    need = max(kda.gated_scan_fwd_workspace_size(d["x"], cu_seqlens=d["cu_dev"]) for d in data)
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for d, b in zip(data, want):
+            a = call(d, workspace=ws)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_large_offsets():
     """More than 2^32 bytes of rows: the last rows are computed from their own inputs."""
     kda = _kda()
