@@ -4,6 +4,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,11 +29,7 @@ def hipcc() -> str:
     return os.path.join(rocm, "bin", "hipcc")
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every source into libkda.so (always recompiles)."""
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC,
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -41,6 +39,22 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed:\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source (always, side by side) and link libkda.so."""
+    tmp = LIB + ".tmp"
+    flags = [x for x in HIPCC_FLAGS if x != "-shared"]
+    jobs = min(len(SOURCES), int(os.environ.get("MAX_JOBS", 0)) or os.cpu_count() or 1, 8)
+    with tempfile.TemporaryDirectory() as d, ThreadPoolExecutor(jobs) as pool:
+        objects = [os.path.join(d, s + ".o") for s in SOURCES]
+        # the longest first
+        order = sorted(range(len(SOURCES)), key=lambda i: -os.path.getsize(os.path.join(CSRC, SOURCES[i])))
+        done = [pool.submit(_run, [hipcc(), *flags, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, SOURCES[i]), "-o", objects[i]],
+                            verbose) for i in order]
+        for f in done:
+            f.result()
+        _run([hipcc(), "-fPIC", "-shared", "--offload-arch=gfx950", *objects, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     return LIB
 
