@@ -181,6 +181,7 @@ template <typename A> kda_status_t plan_norm(const A *a, kda::NormParams *p)
     *p = {};
     KDA_TRY(check_dtypes(a->dtype, a->x_dtype, "x_dtype"));
     if (a->R < 0) return fail(KDA_ERROR_INVALID_VALUE, "need R >= 0 (got %d)", a->R);
+    if (a->R > 0x7fff0000) return fail(KDA_ERROR_NOT_SUPPORTED, "too many rows for 32-bit indices");
     if (a->D < 1) return fail(KDA_ERROR_INVALID_VALUE, "need D >= 1 (got %d)", a->D);
     if (a->D > kda::NORM_MAX_D) return fail(KDA_ERROR_NOT_SUPPORTED, "D=%d: at most %d", a->D, kda::NORM_MAX_D);
     if (!(a->eps >= 0.f)) return fail(KDA_ERROR_INVALID_VALUE, "eps must be >= 0");

@@ -91,7 +91,8 @@ def test_scan_step_rejects(lib, over, status, msg):
 
 
 NORM = [
-    (dict(R=-1), 1, "R >= 0"), (dict(D=0), 1, "D >= 1"), (dict(D=16385), 2, "at most"), (dict(dtype=3), 1, "dtype"),
+    (dict(R=-1), 1, "R >= 0"), (dict(R=0x7fffffff), 2, "too many rows"),
+    (dict(D=0), 1, "D >= 1"), (dict(D=16385), 2, "at most"), (dict(dtype=3), 1, "dtype"),
     (dict(dtype=0, x_dtype=1), 2, "x_dtype"), (dict(eps=-1e-6), 1, "eps"), (dict(eps=float("nan")), 1, "eps"),
     (dict(scale=float("inf")), 1, "scale"), (dict(y=None), 1, "belong to y"), (dict(post_weight=A + 2), 1, "post_weight"),
     (dict(res_scale=A + 1), 1, "res_scale"), (dict(pre_weight=A + 2), 1, "pre_weight"), (dict(y=A + 1), 1, "y is not"),

@@ -382,6 +382,58 @@ def test_repeats_bit_for_bit_streams_and_graph():
         assert all(torch.equal(a, b) for a, b in zip(kept, both())), i
 
 
+def test_many_sequences():
+    """Thousands of packed sequences (the offsets are searched), empty ones among them and at the end, also as a batch of equal
+    lengths."""
+    kda = _kda()
+    gen = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 4, (3000,), generator=gen).tolist() + [500] + [0] * 700 + [70, 0, 0]
+    d = _inputs(lens, 36, BF, BF, True, True, seed=1)
+    h, hT = kda.gated_scan_fwd(d["x"], d["g"], A_log=d["A"], cu_seqlens=d["cu_dev"], initial_state=d["h0"])
+    want, wT, tol, tT = _fwd_ref(d, False)
+    ref.close(h, want, tol, BF, "h")
+    ref.close(hT, wT, tT, FP, "final state")
+    hs = torch.from_numpy(want).to(BF).cuda()
+    got = kda.gated_scan_bwd(None, d["g"], hs, d["dh"], A_log=d["A"], cu_seqlens=d["cu_dev"], initial_state=d["h0"],
+                             dfinal_state=d["dhT"])
+    want, tol = ref.scan_bwd(None, ref.f64(d["g"]), ref.f64(hs), ref.f64(d["dh"]), ref.f64(d["A"]), -5.0, False, d["cu"],
+                             ref.f64(d["h0"]), ref.f64(d["dhT"]))
+    for name, a, b, t, ty in zip(("dx", "dg", "dA_log", "dinitial_state"), got, want, tol, (BF, BF, FP, FP)):
+        ref.close(a, b, t, ty, name)
+
+
+def test_one_activation_packed_the_other_not():
+    kda = _kda()
+    d = _inputs((400, 7), 150, BF, BF, True, True, seed=2)
+    h = torch.from_numpy(_fwd_ref(d, True)[0]).to(BF).cuda()
+    for hs, xs in ((kda.act_pack(h), d["x"]), (h, kda.act_pack(d["x"]))):
+        got = kda.gated_scan_bwd(xs, d["g"], hs, d["dh"], A_log=d["A"], complement=True, cu_seqlens=d["cu_dev"], initial_state=d["h0"],
+                                 dfinal_state=d["dhT"])
+        val = lambda t: ref.values(*t) if isinstance(t, kda.Packed) else ref.f64(t)  # noqa: E731
+        want, tol = ref.scan_bwd(val(xs), ref.f64(d["g"]), val(hs), ref.f64(d["dh"]), ref.f64(d["A"]), -5.0, True, d["cu"],
+                                 ref.f64(d["h0"]), ref.f64(d["dhT"]))
+        for name, a, b, t, ty in zip(("dx", "dg", "dA_log", "dinitial_state"), got, want, tol, (BF, BF, FP, FP)):
+            ref.close(a, b, t, ty, name)
+
+
+@pytest.mark.parametrize("g_min", [-0.05, -1.0, -300.0])
+def test_lower_bounds_of_the_gate(g_min):
+    """Decays that never come near e^-0.1, that straddle it, and that underflow."""
+    kda = _kda()
+    for complement in (False, True):
+        d = _inputs((300,), 40, FP, FP, True, True, seed=4)
+        kw = dict(A_log=d["A"], g_min=g_min, complement=complement, cu_seqlens=d["cu_dev"], initial_state=d["h0"])
+        h, hT = kda.gated_scan_fwd(d["x"], d["g"], **kw)
+        want, wT, tol, tT = _fwd_ref(d, complement, g_min)
+        ref.close(h, want, tol, FP, "h")
+        ref.close(hT, wT, tT, FP, "final state")
+        got = kda.gated_scan_bwd(d["x"], d["g"], h, d["dh"], **kw)
+        want, tol = ref.scan_bwd(ref.f64(d["x"]), ref.f64(d["g"]), ref.f64(h), ref.f64(d["dh"]), ref.f64(d["A"]), g_min, complement,
+                                 d["cu"], ref.f64(d["h0"]), None)
+        for name, a, b, t in zip(("dx", "dg", "dA_log", "dinitial_state"), got, want, tol):
+            ref.close(a, b, t, FP, name)
+
+
 def test_calls_at_once():
     """Calls on several streams, each with its own workspace, wait for their own segments only; one caller's workspace serves calls
     that follow one another, of other sizes too."""
