@@ -18,22 +18,24 @@ __device__ __forceinline__ void sequence_of(const ScanParams &p, int s, int *lo,
 
 // ---- segments --------------------------------------------------------------------
 //
-// h_t = a_t h_{t-1} + b_t is associative: a run of tokens maps the state before
-// it to (product of a) h + (state from zero).  A workgroup takes 64 rows of
-// 128 channels: 32 lanes hold 4 channels each, 8 groups of lanes 8 rows each.
-// A lane runs over its rows from zero (keeping the decays), 128 threads join
-// the 8 runs of a channel through LDS, and with the state before it each lane
-// runs over its rows again from registers: x and g are read once, h written
-// once.
+// h_t = a_t h_{t-1} + b_t is associative: a run of tokens maps the state before it to (product of a) h + (state from
+// zero).  A workgroup takes 64 rows of 128 channels: 32 lanes hold 4 channels each, 8 groups of lanes 8 rows each.  A
+// lane runs over its rows from zero (keeping the decays), 128 threads join the 8 runs of a channel through LDS, and with
+// the state before it each lane runs over its rows again from registers: x and g are read once, h written once.  That
+// takes 128 registers forwards and 151 backwards in bf16: four and three waves a SIMD.
 //
-// Segments of a call's packed rows are joined in the same pass.  Workgroups take
-// tickets of their channels (so a segment's predecessors run or have run already) and publish what
-// their rows do to a state, a pair (product of decays, state from zero), before waiting for anything.  The
-// last segment of every 8 joins these pairs and publishes the block's; the last of every 64 publishes the state behind it.  So
-// a segment waits for at most 7 pairs of its block, 7 of blocks and one state, and what has to pass from one to the next is one
-// state every 4096 rows (with one in every 512, as pairs of segments alone allow, 131072 rows x 2048 took 556 us).  The order in which pairs
-// are joined is fixed, so results do not depend on timing.  Where sequences begin, the state is replaced, and what
-// lies before is not waited for.
+// Segments of a call's packed rows are joined in the same pass.  Workgroups take tickets of their channels (so a
+// segment's predecessors run or have run already) and publish what their rows do to a state, a pair (product of decays,
+// state from zero), before waiting for anything.  The last segment of every 8 joins these pairs and publishes the
+// block's; the last of every 64 publishes the state behind it.  So a segment waits for at most 7 pairs of its block, 7 of
+// blocks and one state, and what has to pass from one to the next is one state every 4096 rows (one in every 512: 6% slower).  The order in which pairs are joined is fixed, so results do not depend on timing.  Where sequences
+// begin, the state is replaced, and what lies before is not waited for.
+//
+// Bound by the arithmetic (38 instructions a token with the gate, all passes and the hand-over, units busy for 68% of the time) and
+// by the wait for the segments before, which run at the same time: 131072 rows x 2048 in bf16 with the gate take 503 us,
+// 3.2 TB/s; without waiting they would take about 400.  8192 x 4096: 60 us (3.3 TB/s), with log-decays 57; gradients 102 us, from
+// 8-bit values 98.  With an odd number of channels vectors are read at odd addresses: 8192 x 4001 75 and 152 us.
+// One segment has nothing to join: no tickets, no clearing (one launch less, 13.4 us instead of 17 with the call).
 
 constexpr int CH = 4, LANES = SCAN_CHANNELS / CH;           // channels a lane; lanes of a row
 constexpr int RUN = 8, RUNS = SCAN_ROWS / RUN;
@@ -273,8 +275,9 @@ __device__ __forceinline__ void put_run(Joined &s, int run, int l, bool cut, con
 
 // A lane's part of a segment in memory: rows of CH channels, at 32-bit offsets from the segment's first element
 // (64 rows of at most 2^24 elements).  In segments whose channels all exist, or whose C is a multiple of CH, every lane reads whole
-// vectors (a lane or row without elements those of the last that has some, and nothing looks at them); in others the last lane
-// goes element by element.
+// vectors (a lane or row without elements those of the last that has some, and nothing looks at them); in others every lane
+// goes element by element, the last one again in place of those that are not there
+// (with a condition for each element instead, whose loads wait for one another, 8192 x 4001 took 86 us and its gradients 171).
 struct Window {
     int rows, n;                                            // rows of the segment that there are; the lane's channels
     bool vec, full;                                         // full: all channels of the segment exist
@@ -294,21 +297,24 @@ struct Window {
     {
         const unsigned end = (unsigned)(rows - 1) * (unsigned)stride;
         unsigned off = (unsigned)row0 * (unsigned)stride;
-        if (vec) {
+        const auto rows_of = [&](auto load_row) {
 #pragma unroll
             for (int i = 0; i < RUN; ++i) {
-                raw[i].load(base + (min(off, end) + col), CH);
+                load_row(raw[i], base + (min(off, end) + col));
                 off += (unsigned)stride;
                 asm("" : "+v"(off));                        // one addition a row, not a product
             }
-        } else {
+        };
+        if (vec)
+            rows_of([&](Raw4<T> &r, const T *p) { r.load(p, CH); });
+        else
+            rows_of([&](Raw4<T> &r, const T *p) {
 #pragma unroll
-            for (int i = 0; i < RUN; ++i) {
-                raw[i].load(base + (min(off, end) + col), n);
-                off += (unsigned)stride;
-            }
-        }
+                for (int j = 0; j < CH; ++j) r.v[j] = p[element(j)];
+            });
     }
+    // Of the lane's channels, where they are not read as a vector.
+    __device__ __forceinline__ unsigned element(int j) const { return min(j, max(n, 1) - 1); }
     template <typename T> __device__ __forceinline__ void put(T *at, const float *x) const
     {
         if (vec) {
@@ -372,8 +378,7 @@ __device__ __forceinline__ void load_held(Held<T> *to, const Window &w, const Ro
                 to[i].v[0] = *reinterpret_cast<const u32_any *>(at);
             } else {
 #pragma unroll
-                for (int j = 0; j < CH; ++j)
-                    if (j < w.n) to[i].v[0] |= (uint32_t)(uint8_t)at[j] << (8 * j);
+                for (int j = 0; j < CH; ++j) to[i].v[0] |= (uint32_t)(uint8_t)at[w.element(j)] << (8 * j);
             }
             to[i].v[1] = __builtin_bit_cast(uint32_t, scales[r * (unsigned)act_groups(C)]);
         }
@@ -384,7 +389,12 @@ __device__ __forceinline__ void load_held(Held<T> *to, const Window &w, const Ro
     for (int i = 0; i < RUN; ++i) {
         const unsigned r = (unsigned)max(min(w.row0 + i, w.rows - 1) - skip, 0);
         Raw4<T> raw;
-        if (w.vec) raw.load(rows + (r * stride + w.col), CH); else raw.load(rows + (r * stride + w.col), w.n);
+        const T *at = rows + (r * stride + w.col);
+        if (w.vec)
+            raw.load(at, CH);
+        else
+#pragma unroll
+            for (int j = 0; j < CH; ++j) raw.v[j] = at[w.element(j)];
         __builtin_memcpy(to[i].v, &raw, sizeof(raw));
     }
 }
@@ -398,7 +408,11 @@ template <bool GATED> struct Gates {
     {
         if (!GATED) return;
         Raw4<float> raw;
-        if (win.vec) raw.load(A_log + c0_ + win.col, CH); else raw.load(A_log + c0_ + win.col, win.n);
+        if (win.vec)
+            raw.load(A_log + c0_ + win.col, CH);
+        else
+#pragma unroll
+            for (int j = 0; j < CH; ++j) raw.v[j] = A_log[c0_ + win.col + win.element(j)];
 #pragma unroll
         for (int j = 0; j < CH; ++j) k[j] = raw[j];
     }
@@ -451,16 +465,18 @@ template <bool CHAIN> __device__ __forceinline__ bool take_segment(const ScanPar
     *q = 0;
     if (CHAIN) {
         if (threadIdx.x == 0)
-            s.ticket = __hip_atomic_fetch_add(p.chain.tickets + (size_t)column * TICKET_STEP, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            s.ticket = __hip_atomic_fetch_add(p.chain.tickets + (size_t)column * TICKET_STEP, 1u, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
         lds_barrier();
         *q = (int)__builtin_amdgcn_readfirstlane(s.ticket);
     }
     return (unsigned)*q < (unsigned)p.chain.segments;
 }
 
-// Each pass has a form for segments that lie inside a sequence and whose channels all exist, with no questions
-// asked, and one for all others.
-template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 ? 4 : 3) void scan_fwd_kernel(const ScanParams p)
+// Forward.  Each pass has a form for segments that lie inside a sequence and whose channels all exist, with no questions asked,
+// and one for all others.
+template <typename T, typename G, bool GATED, bool CHAIN>
+__global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 ? 4 : 3) void scan_fwd_kernel(const ScanParams p)
 {
     __shared__ Joined s;
     __shared__ Marks m;
@@ -548,6 +564,9 @@ template <typename T, typename G, bool GATED, bool CHAIN> __global__ __launch_bo
 }
 
 // Gradients, from the last row to the first: D_t = d_h_t + e_{t+1}, e_t = a_t D_t; runs, segments and their order mirrored.
+// h and x are asked for before the wait.  Saved values of a kind that the kernel knows leave room for three waves a SIMD: 8192 x 4096
+// 102 us in bf16, 98 from 8 bits; with a kernel for either, at the time, 180 instead of 114 and 132 instead of 110.  One that finds h in one form and x in the
+// other, or a single segment, takes that kernel.
 template <typename T, typename G, bool GATED, bool CHAIN, Saved S>
 __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 : 2) void scan_bwd_kernel(const ScanParams p)
 {
@@ -556,6 +575,7 @@ __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 
     const int column = blockIdx.x % ((p.C + SCAN_CHANNELS - 1) / SCAN_CHANNELS), c0 = column * SCAN_CHANNELS;
     int q;
     if (!take_segment<CHAIN>(p, column, s, &q)) return;
+    __builtin_amdgcn_s_setprio(2);                          // others wait for what comes before the join (99 us for 102)
     const int l = threadIdx.x % LANES, run = threadIdx.x / LANES, r0 = (p.chain.segments - 1 - q) * SCAN_ROWS, c = c0 + l * CH;
     const Window win(p, r0, c0);
     const bool complement = p.complement;
@@ -673,6 +693,7 @@ __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 
             to_g.down();
         }
     };
+    __builtin_amdgcn_s_setprio(0);
     if (plain) finish(Yes{}); else finish(No{});
     if (GATED && p.dA) {                                    // the segment's part of dA: runs in their order
         lds_barrier();
@@ -698,7 +719,7 @@ __global__ __launch_bounds__(256) void scan_clear_kernel(ScanChain k, const floa
     for (size_t i = at; i < states; i += step) to[i] = from[i];
 }
 
-// Sums of the segments' parts, in their order.
+// Sums of the segments' parts, in their order: 4.7 us for 128 x 4096.
 __global__ __launch_bounds__(256) void scan_sum_kernel(const float *part, int parts, int C, float *out)
 {
     __shared__ double s_part[16][16];
@@ -707,7 +728,9 @@ __global__ __launch_bounds__(256) void scan_sum_kernel(const float *part, int pa
     if (threadIdx.x < 16 && c < C) out[c] = (float)sum;
 }
 
-// One token a sequence: 8 channels a lane.  Slots as for kda_linear_recurrent_step.
+// One token a sequence: 8 channels a lane, so that a lane's loads are 16 and 32 bytes.  Bound by memory and by the latency of
+// two dependent reads, the slot's and its state's: 512 x 8192 12.0 us (58 MB, 4.8 TB/s), 3 x 2048 3.2 us.
+// Slots as for kda_linear_recurrent_step.
 template <typename T, typename G> __global__ __launch_bounds__(256) void scan_step_kernel(const ScanStepParams p)
 {
     const int blocks = (p.C + 2047) / 2048;

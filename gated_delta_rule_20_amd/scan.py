@@ -182,16 +182,22 @@ def gated_scan_step(x, g, state, *, A_log=None, g_min: float = -5.0, complement:
     return out
 
 
-def gated_scan_fwd_workspace_size(x, *, g_dtype=None, cu_seqlens=None) -> int:
-    """Workspace bytes :func:`gated_scan_fwd` needs for x [B, T, C] (or [T, C] with cu_seqlens) and g of ``g_dtype`` (None: x's)."""
+def gated_scan_fwd_workspace_size(x, *, g_dtype=None, cu_seqlens=None, same_states: bool = False) -> int:
+    """Workspace bytes :func:`gated_scan_fwd` needs for x [B, T, C] (or [T, C] with cu_seqlens) and g of ``g_dtype`` (None: x's);
+    ``same_states``: initial_state is final_state."""
     B, T, C, N = _tokens(x, "x", cu_seqlens)
     a = GatedScanFwdArgs(B, T, C, _DTYPES[x.dtype], _DTYPES[g_dtype or x.dtype], cu_seqlens=_at(cu_seqlens), N=N)
+    if same_states:                            # only whether they overlap is read
+        a.initial_state = a.final_state = 16
     return _need("kda_gated_scan_fwd_workspace_size", a)
 
 
-def gated_scan_bwd_workspace_size(d_h, *, g_dtype=None, cu_seqlens=None, A_log: bool = False) -> int:
-    """Workspace bytes :func:`gated_scan_bwd` needs for d_h [B, T, C] (or [T, C] with cu_seqlens); ``A_log``: its gradient is wanted."""
+def gated_scan_bwd_workspace_size(d_h, *, g_dtype=None, cu_seqlens=None, A_log: bool = False, same_states: bool = False) -> int:
+    """Workspace bytes :func:`gated_scan_bwd` needs for d_h [B, T, C] (or [T, C] with cu_seqlens); ``A_log``: its gradient is wanted;
+    ``same_states``: dinitial_state is dfinal_state."""
     B, T, C, N = _tokens(d_h, "d_h", cu_seqlens)
     a = GatedScanBwdArgs(B, T, C, _DTYPES[d_h.dtype], _DTYPES[g_dtype or d_h.dtype], cu_seqlens=_at(cu_seqlens), N=N)
     a.dA_log = 16 if A_log else None           # only whether it is given is read
+    if same_states:
+        a.d_initial_state = a.d_final_state = 16
     return _need("kda_gated_scan_bwd_workspace_size", a)

@@ -494,11 +494,13 @@ KDA_API kda_status_t kda_cache_compact(const kda_cache_pool_t *pools, int32_t n_
  * serving.  The conventions at the top of this header hold, with these differences:
  *   - Arrays need no more than their elements' alignment, and rows any length.
  *     Where a stride is named, it is the number of elements from one row to the
- *     next (at least the row), so that rows may be parts of wider ones; all
+ *     next (at least the row, at most 2^24), so that rows may be parts of wider ones; all
  *     other arrays are dense.
  *   - Arithmetic, states and sums are float32 or more; each result is rounded
  *     once to its type.
  *   - Outputs must not overlap inputs or one another, but where it is said.
+ *   - Calls that may run at the same time need workspaces of their own.  (Scans
+ *     that share one all the same end, with NaN or rows left unwritten.)
  *
  * Activations in 8 bits: a row of D values is D int8 codes and one float32
  * scale for each KDA_ACT_GROUP consecutive values (the last group may be shorter).
@@ -532,6 +534,8 @@ KDA_API kda_status_t kda_act_unpack(int32_t dtype, const int8_t *codes, const fl
  * States are accurate to float32 however slowly they fade: e^g - 1 is kept to
  * its own last place where e^g is near 1.  A NaN or infinity reaches the tokens behind it in its own
  * channel and sequence only; an infinite state may turn into NaN.
+ * The workspace holds a copy of the entering states where final_state overlaps initial_state (the backward
+ * pass: d_initial_state and d_final_state).
  */
 typedef struct {
     int32_t B, T, C;

@@ -66,7 +66,7 @@ class Decay:
         # e^g: g's error, two roundings of its argument, the exponential
         self.e_a = fin * (eg + 2 * U) + 2 * U
         near = self.g > -0.1
-        # e^g - 1 by its series where e^g is near 1: five steps and what is cut off (U / 2); else by subtraction
+        # e^g - 1 by a cubic where e^g is near 1: five steps at most and its own error (below U / 2); else by subtraction
         e_rest = np.where(near, eg + 7 * U, (self.e_a * self.a + U) / np.maximum(self.rest, 0.09))
         self.e_rest = e_rest
         # error of a h relative to |h|: through e^g - 1 or through e^g

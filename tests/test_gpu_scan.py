@@ -274,6 +274,20 @@ def test_states_in_place_and_empty_calls():
     gb = kda.gated_scan_bwd(None, d["g"], a[0], d["dh"], cu_seqlens=d["cu_dev"], initial_state=d["h0"], dfinal_state=grad,
                             dinitial_state=grad)
     assert torch.equal(ga[0], gb[0]) and torch.equal(ga[1], gb[1]) and torch.equal(ga[3], grad)
+    # workspaces of the user's: overlapping states need a copy there
+    size = kda.gated_scan_fwd_workspace_size(d["x"], cu_seqlens=d["cu_dev"], same_states=True)
+    state = d["h0"].clone()
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    b = kda.gated_scan_fwd(d["x"], d["g"], cu_seqlens=d["cu_dev"], initial_state=state, final_state=state, workspace=ws)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], state)
+    with pytest.raises(kda.KDAError, match="workspace"):
+        kda.gated_scan_fwd(d["x"], d["g"], cu_seqlens=d["cu_dev"], initial_state=state, final_state=state,
+                           workspace=ws[:kda.gated_scan_fwd_workspace_size(d["x"], cu_seqlens=d["cu_dev"])])
+    grad = d["dhT"].clone()
+    ws = torch.empty(kda.gated_scan_bwd_workspace_size(d["dh"], cu_seqlens=d["cu_dev"], same_states=True), dtype=torch.uint8, device="cuda")
+    gb = kda.gated_scan_bwd(None, d["g"], a[0], d["dh"], cu_seqlens=d["cu_dev"], initial_state=d["h0"], dfinal_state=grad,
+                            dinitial_state=grad, workspace=ws)
+    assert torch.equal(ga[0], gb[0]) and torch.equal(ga[3], grad)
     e = torch.empty(2, 0, 50, dtype=BF, device="cuda")
     h, hT = kda.gated_scan_fwd(e, e, initial_state=d["h0"][:2].contiguous())
     assert h.shape == (2, 0, 50) and torch.equal(hT, d["h0"][:2])
