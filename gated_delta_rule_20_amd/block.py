@@ -188,7 +188,7 @@ def block_norm_bwd(x_new, y, dx_new, dn=None, *, gate=None, post_weight=None, re
 
 
 def block_norm_bwd_workspace_size(x_new, *, weights: int = 3) -> int:
-    """Workspace bytes :func:`block_norm_bwd` needs for x_new [..., D] when gradients of ``weights`` weights are wanted (0: none)."""
+    """Workspace bytes :func:`block_norm_bwd` needs for x_new [..., D] when gradients of ``weights`` weights are wanted."""
     R, D = _two(x_new.codes if isinstance(x_new, Packed) else x_new)
     a = BlockNormBwdArgs(R, D, scale=1.0)
     a.d_pre_weight = 16 if weights else None   # only whether one is given is read

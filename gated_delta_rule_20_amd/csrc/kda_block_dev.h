@@ -149,19 +149,6 @@ __device__ __forceinline__ void load_codes(const int8_t *row, const float *scale
     for (int i = 0; i < 8; ++i) x[i] = i < n ? (float)row[c + i] * s : 0.f;
 }
 
-// Channels [c, c + n) of row r as float32, whatever they are stored as.
-template <typename T> __device__ __forceinline__ void load_row8(const Rows &m, size_t r, int C, int c, int n, float *x)
-{
-    if (m.scales) {
-        load_codes((const int8_t *)m.p + r * m.stride, m.scales + r * act_groups(C), c, n, x);
-        return;
-    }
-    Raw8<T> raw;
-    raw.load((const T *)m.p + r * m.stride + c, n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = raw[i];
-}
-
 __device__ __forceinline__ void load_f8(const float *p, int n, float *x)
 {
     Raw8<float> raw;

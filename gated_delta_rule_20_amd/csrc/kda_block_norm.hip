@@ -5,33 +5,28 @@
 
 namespace kda {
 
-// Sums of K values over the NW waves that hold a row, on every lane.  The waves' sums pass through LDS, where each
+// The sum of a value over the NW waves that hold a row, on every lane.  The waves' sums pass through LDS, where each
 // 16 lanes read one a lane and add them up among themselves; two buffers in turn, so that one barrier a sum is enough.
-template <int NW, int K> struct RowSum {
-    float (*lds)[K][NW];
+template <int NW> struct RowSum {
+    float (*lds)[NW];
     int turn;
-    __device__ __forceinline__ void operator()(float *v)
+    __device__ __forceinline__ float operator()(float v)
     {
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
+        v = wave_sum(v);
         if constexpr (NW > 1) {
             const int wave = threadIdx.x / 64 % NW;        // of the row
-            if (lane_id() == 0)
-#pragma unroll
-                for (int k = 0; k < K; ++k) lds[turn][k][wave] = v[k];
+            if (lane_id() == 0) lds[turn][wave] = v;
             lds_barrier();
             const int w = threadIdx.x % 16;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float x = lds[turn][k][w % NW];
-                x = w < NW ? x : 0.f;
-                x = dpp_add<0xB1, 0xF>(x);                 // quad_perm [1, 0, 3, 2]
-                x = dpp_add<0x4E, 0xF>(x);                 // quad_perm [2, 3, 0, 1]
-                x = dpp_add<0x141, 0xF>(x);                // row_half_mirror
-                v[k] = dpp_add<0x140, 0xF>(x);             // row_mirror
-            }
+            float x = lds[turn][w % NW];
+            x = w < NW ? x : 0.f;
+            x = dpp_add<0xB1, 0xF>(x);                     // quad_perm [1, 0, 3, 2]
+            x = dpp_add<0x4E, 0xF>(x);                     // quad_perm [2, 3, 0, 1]
+            x = dpp_add<0x141, 0xF>(x);                    // row_half_mirror
+            v = dpp_add<0x140, 0xF>(x);                    // row_mirror
             turn ^= 1;
         }
+        return v;
     }
 };
 
@@ -169,17 +164,17 @@ __device__ __forceinline__ void load_weight(const float *w, int c, int n, float 
     for (int i = 0; i < 8; ++i) x[i] = otherwise;
 }
 
-// Bound by memory (10 bytes an element in bf16, 13 to 16 backwards).  NW waves hold a row, 8 NCH channels a lane; a
-// workgroup of ROWS such rows side by side goes through its rows with the weights in registers and the next rows'
-// values on their way.
+// Forward.  Bound by memory, 10 bytes an element in bf16: 8192 x 4096 63 us (336 MB, 5.3 TB/s).  NW waves hold a row, 8 NCH channels
+// a lane (16-byte loads of bf16); a workgroup of ROWS such rows side by side goes through its rows with the weights in registers and
+// the next rows' values on their way.
 
 template <typename T, typename X, int NW, int ROWS, int NCH>
 __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_fwd_kernel(const NormParams p)
 {
     constexpr int NT = 64 * NW;                            // threads of a row
-    __shared__ float s_sum[ROWS][2][1][NW];
+    __shared__ float s_sum[ROWS][2][NW];
     const int t = threadIdx.x % NT, side = threadIdx.x / NT;
-    RowSum<NW, 1> sum = {s_sum[side], 0};
+    RowSum<NW> sum = {s_sum[side], 0};
     constexpr bool HELD = NCH == 1;                        // weights and the next row stay in registers
     int cnt[NCH];
     float wpost[8], wres[8], wpre[8];
@@ -222,7 +217,7 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_fwd_kernel(const NormP
         const size_t r = min(row, p.R - 1);
         if (!HELD) load(row);
         float x[NCH][8], u[NCH][8], g[NCH][8];
-        float ss[1] = {0.f};
+        float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < NCH; ++j)
 #pragma unroll
@@ -238,9 +233,8 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_fwd_kernel(const NormP
 #pragma unroll
                 for (int j = 0; j < NCH; ++j)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) ss[0] += u[j][i] * u[j][i];
-                sum(ss);
-                rs = rstd_of(ss[0] * inv_d + p.eps);
+                    for (int i = 0; i < 8; ++i) ss += u[j][i] * u[j][i];
+                rs = rstd_of(sum(ss) * inv_d + p.eps);
             }
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
@@ -262,13 +256,12 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_fwd_kernel(const NormP
             for (int j = 0; j < NCH; ++j)
                 store_codes<LANE_CH>(p.x8, r, p.D, (j * NT + t) * LANE_CH, in ? cnt[j] : 0, x[j]);
         if (p.pre) {
-            ss[0] = 0.f;
+            ss = 0.f;
 #pragma unroll
             for (int j = 0; j < NCH; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss[0] += x[j][i] * x[j][i];
-            sum(ss);
-            const float rs = rstd_of(ss[0] * inv_d + p.eps);
+                for (int i = 0; i < 8; ++i) ss += x[j][i] * x[j][i];
+            const float rs = rstd_of(sum(ss) * inv_d + p.eps);
 #pragma unroll
             for (int j = 0; j < NCH; ++j) {
                 const int c = (j * NT + t) * LANE_CH;
@@ -279,6 +272,148 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_fwd_kernel(const NormP
             }
         }
     }
+}
+
+// Four channels of a row's values, for the gradients: zeros (an open gate) where there is no such part.
+struct Floats {
+    float x[4], y[4], dx[4], dn[4];
+    Sigmoid gate[4];
+};
+
+// Weights of channels [c, c + n): post, res times scale, pre.
+__device__ __forceinline__ void load_weights(const NormParams &p, unsigned c, int n, f32x4 &post, f32x4 &res, f32x4 &pre)
+{
+    float w[3][4] = {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}};
+    if (p.post) load_f4(at_byte(p.post, 4 * c), n, w[0]);
+    if (p.res) load_f4(at_byte(p.res, 4 * c), n, w[1]);
+    if (p.pre) load_f4(at_byte(p.pre, 4 * c), n, w[2]);
+    post = f32x4{w[0][0], w[0][1], w[0][2], w[0][3]};
+    res = f32x4{w[1][0], w[1][1], w[1][2], w[1][3]} * p.scale;
+    pre = f32x4{w[2][0], w[2][1], w[2][2], w[2][3]};
+}
+
+// Adds to the row's sums: y^2, x^2, w_pre dn x, A dx, A w_pre dn, A x.
+__device__ __forceinline__ void add_sums(const Floats &f, f32x4 wpost, f32x4 wres, f32x4 wpre, float *s)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float d = wpre[i] * f.dn[i], A = wpost[i] * wres[i] * (f.y[i] * f.gate[i].s);
+        s[0] += f.y[i] * f.y[i];
+        s[1] += f.x[i] * f.x[i];
+        s[2] += d * f.x[i];
+        s[3] += A * f.dx[i];
+        s[4] += A * d;
+        s[5] += A * f.x[i];
+    }
+}
+
+// 1 / rms of y and x', the means of w_pre dn x^ and of w_post du y^.
+struct RowNumbers {
+    float ry, rx, mx, my;
+    __device__ __forceinline__ RowNumbers(const NormParams &p, bool pre, const float *s)
+    {
+        const float inv_d = 1.f / (float)p.D;
+        ry = p.post ? rstd_of(s[0] * inv_d + p.eps) : 1.f;
+        rx = pre ? rstd_of(s[1] * inv_d + p.eps) : 0.f;
+        mx = s[2] * rx * inv_d;
+        my = p.post ? (s[3] + rx * (s[4] - rx * mx * s[5])) * ry * inv_d : 0.f;
+    }
+    __device__ __forceinline__ explicit RowNumbers(f32x4 v) : ry(v[0]), rx(v[1]), mx(v[2]), my(v[3]) {}
+};
+
+// The gradients at four channels, and their parts of the weights' (res times scale at the end).
+__device__ __forceinline__ void gradients(const Floats &f, const RowNumbers &k, f32x4 wpost, f32x4 wres, f32x4 wpre, f32x4 &post,
+                                          f32x4 &res, f32x4 &pre, float *G, float *dy, float *dgate)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float xh = f.x[i] * k.rx, yh = f.y[i] * k.ry, u = wpost[i] * yh;
+        pre[i] += f.dn[i] * xh;
+        G[i] = f.dx[i] + k.rx * (wpre[i] * f.dn[i] - xh * k.mx);
+        const float dr = G[i] * wres[i], du = dr * f.gate[i].s;
+        res[i] += G[i] * (f.gate[i].s * u);
+        post[i] += du * yh;
+        dgate[i] = dr * u * (f.gate[i].s * f.gate[i].r);
+        dy[i] = k.ry * (wpost[i] * du - yh * k.my);
+    }
+}
+
+// Four or eight channels of a row of all that the gradients read, as it is stored.
+template <typename T, typename X, int V> struct Values {
+    HeldV<X, V> x, dx;
+    HeldV<T, V> y, gate, dn;
+    __device__ __forceinline__ void load(const NormParams &p, size_t r, unsigned c, int n)
+    {
+        if (p.y.p) y.load(p.y, r, p.D, c, n);
+        if (p.pre && p.d_n) {
+            x.load(p.x, r, p.D, c, n);
+            dn.load({p.d_n, nullptr, p.D}, r, p.D, c, n);
+        }
+        if (p.d_x) dx.load({p.d_x, nullptr, p.D}, r, p.D, c, n);
+        if (p.gate.p) gate.load(p.gate, r, p.D, c, n);
+    }
+    // Channels [4 k, 4 k + 4), or zeros.
+    __device__ __forceinline__ void get(const NormParams &p, int k, bool in, Floats &f) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f.x[i] = f.y[i] = f.dn[i] = f.dx[i] = 0.f;
+            f.gate[i] = Sigmoid{1.f, 0.f};
+        }
+        if (!in) return;
+        if (p.y.p) y.get(p.y.scales, k, f.y);
+        if (p.gate.p) {
+            float z[4];
+            gate.get(p.gate.scales, k, z);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f.gate[i] = sigmoid2(z[i]);
+        }
+        if (p.pre && p.d_n) {
+            x.get(p.x.scales, k, f.x);
+            dn.get(false, k, f.dn);
+        }
+        if (p.d_x) dx.get(false, k, f.dx);
+    }
+    __device__ __forceinline__ void clear()
+    {
+        x.clear();
+        y.clear();
+        gate.clear();
+        dx.clear();
+        dn.clear();
+    }
+    __device__ __forceinline__ void hold()
+    {
+        x.hold();
+        y.hold();
+        gate.hold();
+        dx.hold();
+        dn.hold();
+    }
+};
+
+// n of four channels' gradients.
+template <typename T, typename X>
+__device__ __forceinline__ void store_gradients(const NormParams &p, size_t r, unsigned c, int n, const float *G, const float *dy,
+                                                const float *dgate)
+{
+    Raw4<X>::store(at_byte((X *)p.dx + r * p.D, c * sizeof(X)), n, G);
+    if (p.y.p) Raw4<T>::store(at_byte((T *)p.dy + r * p.dy_stride, c * sizeof(T)), n, dy);
+    if (p.gate.p) Raw4<T>::store(at_byte((T *)p.dgate + r * p.dgate_stride, c * sizeof(T)), n, dgate);
+}
+
+// A workgroup's sums of the weights' gradients.
+__device__ __forceinline__ void store_sums(const NormParams &p, int part, unsigned c, int n, f32x4 post, f32x4 res, f32x4 pre)
+{
+    float *at = p.part + (size_t)part * p.D + c;
+    const size_t other = (size_t)p.parts * p.D;
+    const auto put = [&](f32x4 q, float *to) {
+        const float v[4] = {q[0], q[1], q[2], q[3]};
+        Raw4<float>::store(to, n, v);
+    };
+    if (p.dpost) put(post, at);
+    if (p.dres) put(res, at + other);
+    if (p.dpre) put(pre, at + 2 * other);
 }
 
 // Four floats a lane for each of NQ pieces: in registers, or in LDS, where a lane reads and writes its own places only.
@@ -300,106 +435,49 @@ template <int NT, int NQ> struct Quads<NT, NQ, true> {
 //   sum of w_post du y = sum A dx + rx sum A w_pre dn - rx^2 mx sum A x,
 // so a row has one barrier between its two looks at the values (two: 160 us for 8192 x 4096 from 8 bits).  NW waves hold a row,
 // NQ times 4 channels a lane.  With 4 (up to 4096 channels) the weights, their sums, a row and the next one as it is stored fit
-// 128 registers, so that 16 waves a unit hide the sum (8 channels a lane and 8 waves: 143 us).  With 8 the weights lie in LDS, with 16 two of
-// the sums do and the weights are read again for every row; either unpacks the row's values a second time for the second look.
+// 128 registers, so that 16 waves a unit hide the sum: 99 us from 8 bits (439 MB, 4.4 TB/s) and 144 in bf16 (8 channels a lane and 8 waves:
+// 143 us from 8 bits).  With 8 the weights lie in LDS, and the
+// row's values are unpacked a second time for the second look.
 template <typename T, typename X, int NW, int ROWS, int NQ>
 __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormParams p)
 {
-    constexpr int NT = 64 * NW, V = NQ == 1 ? 4 : 8, NV = 4 * NQ / V;
+    constexpr int NT = 64 * NW, V = NQ == 1 ? 4 : 8;
     constexpr bool KEEP = NQ == 1;                         // numbers stay from look to look, the next row is on its way
-    extern __shared__ __align__(16) float s_mem[];         // NQ 2: weights [3][2][NT][4]; 4: sums [2][4][NT][4]; at the end [ROWS - 1][3][NT][4]
+    static_assert(NQ <= 2, "one piece of V channels a lane");
+    extern __shared__ __align__(16) float s_mem[];         // NQ 2: weights [3][2][NT][4]; at the end [ROWS - 1][3][NT][4]
     __shared__ float s_sum[ROWS][2][NW][8];
     const int t = threadIdx.x % NT, side = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
     RowSum6<NW> total = {s_sum[side], 0};
-    const bool block = p.y.p, pre = p.pre && p.d_n, gated = p.gate.p;
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     // With D a multiple of V a lane has V channels or none, and asks nothing more; else the last one goes by elements.
     const bool whole = p.D % V == 0;
-    int cnt[NV];
-#pragma unroll
-    for (int g = 0; g < NV; ++g) cnt[g] = max(0, min(V, p.D - (g * NT + t) * V));
-    const auto channel = [&](int j) { return (unsigned)((4 * j / V * NT + t) * V + 4 * j % V); };
-    Quads<NT, NQ, NQ == 2> w_post, w_res, w_pre;
-    Quads<NT, NQ, NQ == 4> a_post, a_res;
-    Quads<NT, NQ, false> a_pre;
-    a_post.begin(s_mem);
-    a_res.begin(s_mem + 4 * NQ * NT);
+    const int cnt = max(0, min(V, p.D - t * V));
+    const auto channel = [&](int j) { return (unsigned)(t * V + 4 * j); };
+    const auto count = [&](int j) { return max(0, min(4, p.D - (int)channel(j))); };
+    Quads<NT, NQ, !KEEP> w_post, w_res, w_pre;
+    f32x4 a_post[NQ], a_res[NQ], a_pre[NQ];
     w_post.begin(s_mem);
     w_res.begin(s_mem + 4 * NQ * NT);
     w_pre.begin(s_mem + 8 * NQ * NT);
-    const auto weights = [&](int j, f32x4 &post, f32x4 &res, f32x4 &pre_) {
-        const unsigned c = channel(j);
-        const int n = max(0, min(4, p.D - (int)c));
-        float w[3][4] = {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}};
-        if (p.post) load_f4(at_byte(p.post, 4 * c), n, w[0]);
-        if (p.res) load_f4(at_byte(p.res, 4 * c), n, w[1]);
-        if (p.pre) load_f4(at_byte(p.pre, 4 * c), n, w[2]);
-        post = f32x4{w[0][0], w[0][1], w[0][2], w[0][3]};
-        res = f32x4{w[1][0], w[1][1], w[1][2], w[1][3]} * p.scale;
-        pre_ = f32x4{w[2][0], w[2][1], w[2][2], w[2][3]};
-    };
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
-        if (NQ <= 2) {
-            f32x4 a, b, c;
-            weights(j, a, b, c);
-            w_post.put(j, a);
-            w_res.put(j, b);
-            w_pre.put(j, c);
-        }
-        a_post.put(j, zero);
-        a_res.put(j, zero);
-        a_pre.put(j, zero);
+        f32x4 a, b, c;
+        load_weights(p, channel(j), count(j), a, b, c);
+        w_post.put(j, a);
+        w_res.put(j, b);
+        w_pre.put(j, c);
+        a_post[j] = a_res[j] = a_pre[j] = zero;
     }
-    const auto weight = [&](int j, f32x4 &post, f32x4 &res, f32x4 &pre_) {
-        if (NQ > 2) {
-            weights(j, post, res, pre_);
-        } else {
-            post = w_post.get(j);
-            res = w_res.get(j);
-            pre_ = w_pre.get(j);
-        }
-    };
-    struct Values {
-        HeldV<X, V> x[NV], dx[NV];
-        HeldV<T, V> y[NV], gate[NV], dn[NV];
-    };
-    Values next;
-    const Rows d_n = {p.d_n, nullptr, p.D}, d_x = {p.d_x, nullptr, p.D};
-    const auto load_some = [&](size_t r, int g, int n) {
-        const unsigned c = (g * NT + t) * V;
-        if (block) next.y[g].load(p.y, r, p.D, c, n);
-        if (pre) {
-            next.x[g].load(p.x, r, p.D, c, n);
-            next.dn[g].load(d_n, r, p.D, c, n);
-        }
-        if (p.d_x) next.dx[g].load(d_x, r, p.D, c, n);
-        if (gated) next.gate[g].load(p.gate, r, p.D, c, n);
-    };
+    Values<T, X, V> next;
     const auto load = [&](int row) {
         const size_t r = min(row, p.R - 1);
-#pragma unroll
-        for (int g = 0; g < NV; ++g) {
-            if (whole) {
-                if (cnt[g] > 0) load_some(r, g, V);
-            } else {
-                load_some(r, g, cnt[g]);
-            }
+        if (whole) {
+            if (cnt > 0) next.load(p, r, t * V, V);
+        } else {
+            next.load(p, r, t * V, cnt);
         }
     };
-#pragma unroll
-    for (int g = 0; g < NV; ++g) {                         // lanes without channels keep zeros
-        next.y[g].clear();
-        next.x[g].clear();
-        next.dn[g].clear();
-        next.dx[g].clear();
-        next.gate[g].clear();
-    }
-    struct Floats {                                        // zeros (an open gate) where there is no such part
-        float x[4], y[4], dx[4], dn[4];
-        Sigmoid gate[4];
-    };
-    const float inv_d = 1.f / (float)p.D;
+    next.clear();                                          // lanes without channels keep zeros
     const int step = p.parts * ROWS;
     if (KEEP) load(blockIdx.x * ROWS + side);
     for (int row0 = blockIdx.x * ROWS; row0 < p.R; row0 += step) {
@@ -407,133 +485,115 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
         const bool in = ROWS == 1 || row < p.R;            // a side without a row adds zeros
         const size_t r = min(row, p.R - 1);
         if (!KEEP) load(row);
-        Values now = next;
+        Values<T, X, V> now = next;
         if (KEEP && row0 + step < p.R) load(row + step);
-        const auto floats = [&](int j, Floats &f) {
-            const int g = 4 * j / V, k = j - g * V / 4;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f.x[i] = f.y[i] = f.dn[i] = f.dx[i] = 0.f;
-                f.gate[i] = Sigmoid{1.f, 0.f};
-            }
-            if (!in) return;
-            if (block) now.y[g].get(p.y.scales, k, f.y);
-            if (gated) {
-                float z[4];
-                now.gate[g].get(p.gate.scales, k, z);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f.gate[i] = sigmoid2(z[i]);
-            }
-            if (pre) {
-                now.x[g].get(p.x.scales, k, f.x);
-                now.dn[g].get(false, k, f.dn);
-            }
-            if (p.d_x) now.dx[g].get(false, k, f.dx);
-        };
-        float s[6] = {};                                   // y^2, x^2, w_pre dn x, A dx, A w_pre dn, A x
+        float s[6] = {};
         Floats f;
-        f32x4 wpost, wres, wpre;
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            weight(j, wpost, wres, wpre);
-            floats(j, f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float d = wpre[i] * f.dn[i], A = wpost[i] * wres[i] * (f.y[i] * f.gate[i].s);
-                s[0] += f.y[i] * f.y[i];
-                s[1] += f.x[i] * f.x[i];
-                s[2] += d * f.x[i];
-                s[3] += A * f.dx[i];
-                s[4] += A * d;
-                s[5] += A * f.x[i];
-            }
+            now.get(p, j, in, f);
+            add_sums(f, w_post.get(j), w_res.get(j), w_pre.get(j), s);
             if (!KEEP) __builtin_amdgcn_sched_barrier(0);
         }
         total(s);
-        const float ry = p.post ? rstd_of(s[0] * inv_d + p.eps) : 1.f;
-        const float rx = pre ? rstd_of(s[1] * inv_d + p.eps) : 0.f;
-        const float mx = s[2] * rx * inv_d;                // mean of w_pre dn x^
-        const float my = p.post ? (s[3] + rx * (s[4] - rx * mx * s[5])) * ry * inv_d : 0.f;
-        if (!KEEP)
-#pragma unroll
-            for (int g = 0; g < NV; ++g) {
-                now.x[g].hold();
-                now.y[g].hold();
-                now.gate[g].hold();
-                now.dx[g].hold();
-                now.dn[g].hold();
-            }
+        const RowNumbers k(p, p.pre && p.d_n, s);
+        if (!KEEP) now.hold();
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const unsigned c = channel(j);
-            const int n = in ? max(0, min(4, p.D - (int)c)) : 0;
-            if (!KEEP) {
-                weight(j, wpost, wres, wpre);
-                floats(j, f);
-            }
+            const int n = in ? count(j) : 0;
+            if (!KEEP) now.get(p, j, in, f);
             float G[4], dy[4], dgate[4];
-            f32x4 sum = a_pre.get(j), post = a_post.get(j), res = a_res.get(j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float xh = f.x[i] * rx, yh = f.y[i] * ry, u = wpost[i] * yh;
-                sum[i] += f.dn[i] * xh;
-                G[i] = f.dx[i] + rx * (wpre[i] * f.dn[i] - xh * mx);
-                const float dr = G[i] * wres[i], du = dr * f.gate[i].s;
-                res[i] += G[i] * (f.gate[i].s * u);        // (times scale at the end)
-                post[i] += du * yh;
-                dgate[i] = dr * u * (f.gate[i].s * f.gate[i].r);
-                dy[i] = ry * (wpost[i] * du - yh * my);
-            }
-            a_pre.put(j, sum);
-            a_post.put(j, post);
-            a_res.put(j, res);
-            const auto store = [&](int m) {
-                Raw4<X>::store(at_byte((X *)p.dx + r * p.D, c * sizeof(X)), m, G);
-                if (block) Raw4<T>::store(at_byte((T *)p.dy + r * p.dy_stride, c * sizeof(T)), m, dy);
-                if (gated) Raw4<T>::store(at_byte((T *)p.dgate + r * p.dgate_stride, c * sizeof(T)), m, dgate);
-            };
+            gradients(f, k, w_post.get(j), w_res.get(j), w_pre.get(j), a_post[j], a_res[j], a_pre[j], G, dy, dgate);
             if (n > 0) {
-                if (whole) store(4); else store(n);
+                if (whole) store_gradients<T, X>(p, r, channel(j), 4, G, dy, dgate);
+                else store_gradients<T, X>(p, r, channel(j), n, G, dy, dgate);
             }
             if (!KEEP) __builtin_amdgcn_sched_barrier(0);
         }
     }
-#pragma unroll
-    for (int j = 0; j < NQ; ++j) a_res.put(j, a_res.get(j) * p.scale);
     if (ROWS > 1) {                                        // the sides' sums, in their order (NQ 1)
         f32x4 *at = reinterpret_cast<f32x4 *>(s_mem) + t;
         if (side > 0) {
-            at[(side - 1) * 3 * NT] = a_post.get(0);
-            at[((side - 1) * 3 + 1) * NT] = a_res.get(0);
-            at[((side - 1) * 3 + 2) * NT] = a_pre.get(0);
+            at[(side - 1) * 3 * NT] = a_post[0];
+            at[((side - 1) * 3 + 1) * NT] = a_res[0];
+            at[((side - 1) * 3 + 2) * NT] = a_pre[0];
         }
         __syncthreads();
         if (side > 0) return;
         for (int k = 0; k < ROWS - 1; ++k) {
-            a_post.put(0, a_post.get(0) + at[k * 3 * NT]);
-            a_res.put(0, a_res.get(0) + at[(k * 3 + 1) * NT]);
-            a_pre.put(0, a_pre.get(0) + at[(k * 3 + 2) * NT]);
+            a_post[0] += at[k * 3 * NT];
+            a_res[0] += at[(k * 3 + 1) * NT];
+            a_pre[0] += at[(k * 3 + 2) * NT];
         }
     }
 #pragma unroll
-    for (int j = 0; j < NQ; ++j) {
-        const unsigned c = channel(j);
-        const int n = max(0, min(4, p.D - (int)c));
-        if (n == 0) continue;
-        float *at = p.part + (size_t)blockIdx.x * p.D + c;
-        const size_t other = (size_t)p.parts * p.D;
-        const auto put = [&](f32x4 q, float *to) {
-            const float v[4] = {q[0], q[1], q[2], q[3]};
-            Raw4<float>::store(to, n, v);
-        };
-        if (p.dpost) put(a_post.get(j), at);
-        if (p.dres) put(a_res.get(j), at + other);
-        if (p.dpre) put(a_pre.get(j), at + 2 * other);
+    for (int j = 0; j < NQ; ++j)
+        if (count(j) > 0) store_sums(p, blockIdx.x, channel(j), count(j), a_post[j], a_res[j] * p.scale, a_pre[j]);
+}
+
+// Rows of more than NORM_ROW_D channels do not fit a workgroup's registers next to the weights and their sums (as one such kernel
+// with the sums in LDS 2048 x 16384 took 447 us, 64 rows 130): a first kernel forms each row's numbers, a second goes
+// through columns of 1024 channels with the weights and sums in registers and no barrier.  The values are read twice: 235 us, 3.3 TB/s
+// with the second reading; 64 rows 29 us.
+constexpr int WIDE_WAVES = 8;
+template <typename T, typename X> __global__ __launch_bounds__(64 * WIDE_WAVES, 4) void norm_numbers_kernel(const NormParams p)
+{
+    constexpr int NT = 64 * WIDE_WAVES, BATCH = 4;         // pieces of 4 channels a lane on their way
+    __shared__ float s_sum[2][WIDE_WAVES][8];
+    RowSum6<WIDE_WAVES> total = {s_sum, 0};
+    for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
+        float s[6] = {};
+        for (int c0 = 0; c0 < p.D; c0 += 4 * NT * BATCH) {
+            Values<T, X, 4> v[BATCH];
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const int c = c0 + 4 * (j * NT + (int)threadIdx.x);
+                v[j].clear();
+                if (c < p.D) v[j].load(p, r, c, min(4, p.D - c));
+            }
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const int c = c0 + 4 * (j * NT + (int)threadIdx.x);
+                f32x4 wpost, wres, wpre;
+                Floats f;
+                if (c < p.D) {
+                    load_weights(p, c, min(4, p.D - c), wpost, wres, wpre);
+                    v[j].get(p, 0, true, f);
+                    add_sums(f, wpost, wres, wpre, s);
+                }
+            }
+        }
+        total(s);
+        const RowNumbers k(p, p.pre && p.d_n, s);
+        if (threadIdx.x == 0) p.numbers[r] = f32x4{k.ry, k.rx, k.mx, k.my};
     }
+}
+template <typename T, typename X> __global__ __launch_bounds__(256, 4) void norm_columns_kernel(const NormParams p)
+{
+    const int columns = (p.D + NORM_COLUMN - 1) / NORM_COLUMN, part = blockIdx.x / columns;
+    const int c = (blockIdx.x % columns) * NORM_COLUMN + threadIdx.x * 4, n = max(0, min(4, p.D - c));
+    if (n == 0) return;
+    f32x4 wpost, wres, wpre, post = {0.f, 0.f, 0.f, 0.f}, res = post, pre = post;
+    load_weights(p, c, n, wpost, wres, wpre);
+    Values<T, X, 4> next;
+    next.clear();
+    if (part < p.R) next.load(p, part, c, n);
+    for (int r = part; r < p.R; r += p.parts) {
+        const Values<T, X, 4> now = next;
+        const RowNumbers k(p.numbers[r]);
+        if (r + p.parts < p.R) next.load(p, r + p.parts, c, n);
+        Floats f;
+        now.get(p, 0, true, f);
+        float G[4], dy[4], dgate[4];
+        gradients(f, k, wpost, wres, wpre, post, res, pre, G, dy, dgate);
+        store_gradients<T, X>(p, r, c, n, G, dy, dgate);
+    }
+    store_sums(p, part, c, n, post, res * p.scale, pre);
 }
 
 // The weights' gradients from the workgroups' sums, in their order.  16 columns a workgroup (64 bytes of a row), 16 threads down
-// each, eight rows on their way: with 64 columns and 4 threads, one row at a time, it took 36 us of 512 x 3 x 4096 sums.
+// each, eight rows on their way: 7.3 us for 256 x 3 x 4096 sums (with 64 columns and 4 threads, one row at a time, 36 us
+// for twice as many).
 __global__ __launch_bounds__(256) void norm_sum_kernel(const NormParams p)
 {
     __shared__ double s_part[16][16];
@@ -551,24 +611,42 @@ template <typename T, typename X, int NW, int ROWS, int NCH> static hipError_t l
     return hipGetLastError();
 }
 
-template <typename T, typename X, int NW, int ROWS, int NQ> static hipError_t launch_bwd_t(const NormParams &p, hipStream_t stream)
+static hipError_t launch_sum(const NormParams &p, hipStream_t stream)
 {
-    static_assert(NW * ROWS == norm_waves(256 * NW * NQ) && ROWS == norm_rows(256 * NW * NQ), "as planned");
-    constexpr size_t row = sizeof(float) * 256 * NW * NQ;                            // of floats
-    constexpr size_t lds = row * (NQ == 1 ? 3 * (ROWS - 1) : NQ == 2 ? 3 : 2);
-    if (p.R > 0) {
-        if (lds > 0) {
-            const hipError_t e = hipFuncSetAttribute((const void *)norm_bwd_kernel<T, X, NW, ROWS, NQ>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-            if (e != hipSuccess) return e;
-        }
-        hipLaunchKernelGGL((norm_bwd_kernel<T, X, NW, ROWS, NQ>), dim3(p.parts), dim3(64 * NW * ROWS), lds, stream, p);
-    }
     if (p.dpost || p.dres || p.dpre)
         hipLaunchKernelGGL(norm_sum_kernel, dim3((p.D + 15) / 16, 3), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
-// Forward: 8 channels a lane, up to 16 waves a row, then twice that.
+template <typename T, typename X> static hipError_t launch_bwd_wide(const NormParams &p, hipStream_t stream)
+{
+    if (p.R > 0) {
+        const int most = 256 * 4;                                                    // two a unit at a time, in two turns
+        hipLaunchKernelGGL((norm_numbers_kernel<T, X>), dim3(p.R < most ? p.R : most), dim3(64 * WIDE_WAVES), 0, stream, p);
+        hipLaunchKernelGGL((norm_columns_kernel<T, X>), dim3(p.parts * ((p.D + NORM_COLUMN - 1) / NORM_COLUMN)), dim3(256), 0, stream, p);
+    }
+    return launch_sum(p, stream);
+}
+
+template <typename T, typename X, int NW, int ROWS, int NQ> static hipError_t launch_bwd_t(const NormParams &p, hipStream_t stream)
+{
+    static_assert(NW * ROWS == norm_waves(256 * NW * NQ) && ROWS == norm_rows(256 * NW * NQ), "as planned");
+    constexpr size_t row = sizeof(float) * 256 * NW * NQ;                            // of floats
+    constexpr size_t lds = row * (NQ == 1 ? 3 * (ROWS - 1) : 3);
+    if (p.R > 0) {
+        const auto kernel = norm_bwd_kernel<T, X, NW, ROWS, NQ>;
+        if (lds > 0) {
+            const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+            if (e != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL(kernel, dim3(p.parts), dim3(64 * NW * ROWS), lds, stream, p);
+    }
+    return launch_sum(p, stream);
+}
+
+// Forward: 8 channels a lane, as few waves a row as that takes, up to 16; then twice the channels.  Fewer lanes without channels,
+// and sums over fewer waves: 2^25 elements in rows of 512, 1024, 2048, 4096, 8192 channels take 61 to 63 us; as the next
+// wider form 77 to 78, of 8192 channels 108.
 template <typename T, typename X> static hipError_t launch_fwd_x(const NormParams &p, hipStream_t stream)
 {
     if (p.D <= 512) return launch_fwd_t<T, X, 1, 4, 1>(p, stream);
@@ -579,7 +657,8 @@ template <typename T, typename X> static hipError_t launch_fwd_x(const NormParam
     return launch_fwd_t<T, X, 16, 1, 2>(p, stream);
 }
 
-// Backward: 4 channels a lane, up to 16 waves a row, then more.
+// Backward: 4 channels a lane, as few waves a row as that takes, up to 16; then more channels.  2^25 elements of bf16 in rows of 256
+// to 8192 channels take 138 to 146 us; as the next wider form 217 to 228 (up to 1024 channels), 192 (2048), 177 (4096).
 template <typename T, typename X> static hipError_t launch_bwd_x(const NormParams &p, hipStream_t stream)
 {
     if (p.D <= 256) return launch_bwd_t<T, X, 1, 4, 1>(p, stream);
@@ -587,8 +666,8 @@ template <typename T, typename X> static hipError_t launch_bwd_x(const NormParam
     if (p.D <= 1024) return launch_bwd_t<T, X, 4, 1, 1>(p, stream);
     if (p.D <= 2048) return launch_bwd_t<T, X, 8, 1, 1>(p, stream);
     if (p.D <= 4096) return launch_bwd_t<T, X, 16, 1, 1>(p, stream);
-    if (p.D <= 8192) return launch_bwd_t<T, X, 16, 1, 2>(p, stream);
-    return launch_bwd_t<T, X, 16, 1, 4>(p, stream);
+    if (p.D <= NORM_ROW_D) return launch_bwd_t<T, X, 16, 1, 2>(p, stream);
+    return launch_bwd_wide<T, X>(p, stream);
 }
 
 hipError_t launch_norm_fwd(int is_bf16, int x_bf16, const NormParams &p, hipStream_t stream)

@@ -213,6 +213,41 @@ def test_repeats_streams_and_graph():
         assert all(torch.equal(a, b) for a, b in zip(kept, both())), i
 
 
+def test_many_wide_rows():
+    """Rows too wide for one workgroup's registers, more of them than workgroups; rows do not depend on their neighbours, dx over
+    dx', one weight's gradient only, a captured call."""
+    kda = _kda()
+    R, D = 1100, 8201
+    d = _inputs(R, D, BF, BF, True, True, True, True, seed=5)
+    x1, _, saved = kda.block_norm_fwd(d["x"], d["y"], pack=True, **_kw(d))
+    got = kda.block_norm_bwd(x1, d["y"], d["dx"], d["dn"], **_kw(d))
+    want, tol = ref.norm_bwd(*(ref.f64(t) for t in (x1, d["y"], d["gate"], d["post"], d["res"], d["pre"])), 0.7, 1e-6,
+                             ref.f64(d["dx"]), ref.f64(d["dn"]))
+    for name, t, ty in zip(("dx", "dy", "dgate", "dpost", "dres", "dpre"), got, (BF, BF, BF, FP, FP, FP)):
+        ref.close(t, want[name], tol[name], ty, name)
+    cut = slice(1030, 1041)
+    kw = _kw(d)
+    kw["gate"] = d["gate"][cut]
+    dx = d["dx"][cut].clone()
+    part = kda.block_norm_bwd(x1[cut], d["y"][cut], dx, d["dn"][cut], dx=dx, **kw)
+    assert all(torch.equal(a[cut], b) for a, b in zip(got[:3], part[:3]))
+    assert kda.block_norm_bwd_workspace_size(x1, weights=0) > 0
+    none = kda.block_norm_bwd(x1, d["y"], d["dx"], d["dn"], need_dweights=False, **_kw(d))
+    assert all(torch.equal(a, b) for a, b in zip(got[:3], none[:3])) and none[3:] == (None, None, None)
+    kw["gate"] = saved.gate
+    ws = torch.empty(kda.block_norm_bwd_workspace_size(saved.x_new), dtype=torch.uint8, device="cuda")
+    call = lambda: kda.block_norm_bwd(saved.x_new, saved.y, d["dx"], d["dn"], workspace=ws, **kw)  # noqa: E731
+    first = call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for _ in range(3):
+        ws.fill_(0xA5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
 def test_large_offsets():
     """Rows behind 2^32 bytes give what the same rows give alone."""
     kda = _kda()
