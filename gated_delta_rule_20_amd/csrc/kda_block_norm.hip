@@ -104,11 +104,11 @@ template <typename T, int V> struct HeldV {
     static constexpr int WORDS = V * sizeof(T) / 4;
     typedef typename Pick<V, Raw4<T>, Raw8<T>>::type Raw;
     uint32_t v[WORDS];
-    // r is uniform
-    __device__ __forceinline__ void load(const Rows &m, size_t r, int D, unsigned c, int n)
+    // Channels [c, c + n), r uniform; or all V from `from` on, before c, with c's scale.
+    __device__ __forceinline__ void load(const Rows &m, size_t r, int D, unsigned c, unsigned from, int n)
     {
         if (m.scales) {
-            const int8_t *at = (const int8_t *)m.p + r * m.stride + c;
+            const int8_t *at = (const int8_t *)m.p + r * m.stride + from;
             if (n == V) {
                 typedef uint32_t codes_any __attribute__((ext_vector_type(V / 4), aligned(1)));
                 const codes_any q = *reinterpret_cast<const codes_any *>(at);
@@ -124,8 +124,30 @@ template <typename T, int V> struct HeldV {
             return;
         }
         Raw raw;
-        raw.load(at_byte((const T *)m.p + r * m.stride, c * sizeof(T)), n);
+        raw.load(at_byte((const T *)m.p + r * m.stride, from * sizeof(T)), n);
         __builtin_memcpy(v, &raw, sizeof(raw));
+    }
+    // Takes the first e of four channels off, zeros behind the others.
+    __device__ __forceinline__ void drop(bool packed, int e)
+    {
+        static_assert(V == 4, "codes of one word");
+        if (packed) {
+            v[0] >>= 8 * e;
+            return;
+        }
+        if (sizeof(T) == 2) {
+            const uint64_t q = ((uint64_t)v[1] << 32 | v[0]) >> 16 * e;
+            v[0] = (uint32_t)q;
+            v[1] = (uint32_t)(q >> 32);
+            return;
+        }
+#pragma unroll
+        for (int step = 1; step < WORDS; step *= 2)
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                const uint32_t other = i + step < WORDS ? v[i + step] : 0;
+                v[i] = e & step ? other : v[i];
+            }
     }
     // channels [4 k, 4 k + 4)
     __device__ __forceinline__ void get(bool packed, int k, float *x) const
@@ -342,15 +364,26 @@ __device__ __forceinline__ void gradients(const Floats &f, const RowNumbers &k, 
 template <typename T, typename X, int V> struct Values {
     HeldV<X, V> x, dx;
     HeldV<T, V> y, gate, dn;
-    __device__ __forceinline__ void load(const NormParams &p, size_t r, unsigned c, int n)
+    __device__ __forceinline__ void load(const NormParams &p, size_t r, unsigned c, unsigned from, int n)
     {
-        if (p.y.p) y.load(p.y, r, p.D, c, n);
+        if (p.y.p) y.load(p.y, r, p.D, c, from, n);
         if (p.pre && p.d_n) {
-            x.load(p.x, r, p.D, c, n);
-            dn.load({p.d_n, nullptr, p.D}, r, p.D, c, n);
+            x.load(p.x, r, p.D, c, from, n);
+            dn.load({p.d_n, nullptr, p.D}, r, p.D, c, from, n);
         }
-        if (p.d_x) dx.load({p.d_x, nullptr, p.D}, r, p.D, c, n);
-        if (p.gate.p) gate.load(p.gate, r, p.D, c, n);
+        if (p.d_x) dx.load({p.d_x, nullptr, p.D}, r, p.D, c, from, n);
+        if (p.gate.p) gate.load(p.gate, r, p.D, c, from, n);
+    }
+    __device__ __forceinline__ void load(const NormParams &p, size_t r, unsigned c, int n) { load(p, r, c, c, n); }
+    __device__ __forceinline__ void drop(const NormParams &p, int e)
+    {
+        if (p.y.p) y.drop(p.y.scales, e);
+        if (p.pre && p.d_n) {
+            x.drop(p.x.scales, e);
+            dn.drop(false, e);
+        }
+        if (p.d_x) dx.drop(false, e);
+        if (p.gate.p) gate.drop(p.gate.scales, e);
     }
     // Channels [4 k, 4 k + 4), or zeros.
     __device__ __forceinline__ void get(const NormParams &p, int k, bool in, Floats &f) const
@@ -438,7 +471,12 @@ template <int NT, int NQ> struct Quads<NT, NQ, true> {
 // 128 registers, so that 16 waves a unit hide the sum: 99 us from 8 bits (439 MB, 4.4 TB/s) and 144 in bf16 (8 channels a lane and 8 waves:
 // 143 us from 8 bits).  With 8 the weights lie in LDS, and the
 // row's values are unpacked a second time for the second look.
-template <typename T, typename X, int NW, int ROWS, int NQ>
+// RAGGED: the last channels of a row are fewer than a lane's four.  The lane loads the row's last four all the same and takes those before
+// its own off where it needs the values, since loads of single channels, each with its condition, wait for one another: 8192 x 4002
+// 143 us instead of 198, 8192 x 4001 from 8 bits 119 instead of 186.  (A kernel that asks for either at run time takes 152 instead of
+// 135 us for whole rows; with 8 channels a lane the same is slower, 201 us instead of 180 for 4096 x 8001: there the last lane
+// goes by elements.)
+template <typename T, typename X, int NW, int ROWS, int NQ, bool RAGGED>
 __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormParams p)
 {
     constexpr int NT = 64 * NW, V = NQ == 1 ? 4 : 8;
@@ -450,8 +488,9 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
     RowSum6<NW> total = {s_sum[side], 0};
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     // With D a multiple of V a lane has V channels or none, and asks nothing more; else the last one goes by elements.
-    const bool whole = p.D % V == 0;
+    const bool whole = !RAGGED && p.D % V == 0;
     const int cnt = max(0, min(V, p.D - t * V));
+    const bool ragged = RAGGED && __any(cnt > 0 && cnt < V);
     const auto channel = [&](int j) { return (unsigned)(t * V + 4 * j); };
     const auto count = [&](int j) { return max(0, min(4, p.D - (int)channel(j))); };
     Quads<NT, NQ, !KEEP> w_post, w_res, w_pre;
@@ -471,7 +510,9 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
     Values<T, X, V> next;
     const auto load = [&](int row) {
         const size_t r = min(row, p.R - 1);
-        if (whole) {
+        if (RAGGED) {
+            if (cnt > 0) next.load(p, r, t * V, min(t * V, p.D - V), V);
+        } else if (whole) {
             if (cnt > 0) next.load(p, r, t * V, V);
         } else {
             next.load(p, r, t * V, cnt);
@@ -486,6 +527,8 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
         const size_t r = min(row, p.R - 1);
         if (!KEEP) load(row);
         Values<T, X, V> now = next;
+        if constexpr (RAGGED)
+            if (ragged) now.drop(p, cnt > 0 ? V - cnt : 0);
         if (KEEP && row0 + step < p.R) load(row + step);
         float s[6] = {};
         Floats f;
@@ -634,7 +677,8 @@ template <typename T, typename X, int NW, int ROWS, int NQ> static hipError_t la
     constexpr size_t row = sizeof(float) * 256 * NW * NQ;                            // of floats
     constexpr size_t lds = row * (NQ == 1 ? 3 * (ROWS - 1) : 3);
     if (p.R > 0) {
-        const auto kernel = norm_bwd_kernel<T, X, NW, ROWS, NQ>;
+        const auto kernel = NQ == 1 && p.D % 4 != 0 && p.D > 4 ? norm_bwd_kernel<T, X, NW, ROWS, NQ, NQ == 1>
+                                                                  : norm_bwd_kernel<T, X, NW, ROWS, NQ, false>;
         if (lds > 0) {
             const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
             if (e != hipSuccess) return e;
