@@ -190,6 +190,10 @@ def block_norm_bwd(x_new, y, dx_new, dn=None, *, gate=None, post_weight=None, re
 def block_norm_bwd_workspace_size(x_new, *, weights: int = 3) -> int:
     """Workspace bytes :func:`block_norm_bwd` needs for x_new [..., D] when gradients of ``weights`` weights are wanted."""
     R, D = _two(x_new.codes if isinstance(x_new, Packed) else x_new)
-    a = BlockNormBwdArgs(R, D, scale=1.0)
+    # float32 blocks need the most
+    dtype = torch.float32 if isinstance(x_new, Packed) else x_new.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    a = BlockNormBwdArgs(R, D, _DTYPES[dtype], _DTYPES[dtype], scale=1.0)
     a.d_pre_weight = 16 if weights else None   # only whether one is given is read
     return _need("kda_block_norm_bwd_workspace_size", a)

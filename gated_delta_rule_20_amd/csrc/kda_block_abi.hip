@@ -205,20 +205,21 @@ template <typename A> kda_status_t plan_norm(const A *a, kda::NormParams *p)
 // its own sums of the weights' gradients.
 // Workgroups of the gradients, each with sums of its own: four rows a side at least, 16 waves (of columns: 32) on each of 256 units at most.
 // (One row at least: 256 x 4096 23.5 us either way, with four times the sums; 16: 42.5.)
-int norm_parts(int R, int D)
+int norm_parts(int R, int D, bool columns)
 {
     const int rows = 4 * kda::norm_rows(D);
-    const int most = D > kda::NORM_ROW_D ? 256 * 8 / ((D + kda::NORM_COLUMN - 1) / kda::NORM_COLUMN) : 256 * 16 / kda::norm_waves(D);
+    const int most = columns ? 256 * 8 / ((D + kda::NORM_COLUMN - 1) / kda::NORM_COLUMN) : 256 * 16 / kda::norm_waves(D);
     const int n = R / rows + (R % rows != 0);
     return n < most ? n : most;
 }
 
 size_t plan_norm_bwd(const kda_block_norm_bwd_args_t *a, kda::NormParams *p)
 {
-    p->parts = norm_parts(a->R, a->D);
+    const bool columns = a->D > kda::norm_row_d(a->dtype == KDA_F32);
+    p->parts = norm_parts(a->R, a->D, columns);
     Carver c(a->workspace);
     if (a->d_post_weight || a->d_res_scale || a->d_pre_weight) p->part = (float *)c.take(sizeof(float) * 3 * (size_t)p->parts * a->D);
-    if (a->D > kda::NORM_ROW_D) p->numbers = (decltype(p->numbers))c.take(16 * (size_t)a->R);
+    if (columns) p->numbers = (decltype(p->numbers))c.take(16 * (size_t)a->R);
     return c.used;
 }
 

@@ -574,7 +574,7 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
         if (count(j) > 0) store_sums(p, blockIdx.x, channel(j), count(j), a_post[j], a_res[j] * p.scale, a_pre[j]);
 }
 
-// Rows of more than NORM_ROW_D channels do not fit a workgroup's registers next to the weights and their sums (as one such kernel
+// Rows of more than norm_row_d channels do not fit a workgroup's registers next to the weights and their sums (as one such kernel
 // with the sums in LDS 2048 x 16384 took 447 us, 64 rows 130): a first kernel forms each row's numbers, a second goes
 // through columns of 1024 channels with the weights and sums in registers and no barrier.  The values are read twice: 235 us, 3.3 TB/s
 // with the second reading; 64 rows 29 us.
@@ -710,7 +710,8 @@ template <typename T, typename X> static hipError_t launch_bwd_x(const NormParam
     if (p.D <= 1024) return launch_bwd_t<T, X, 4, 1, 1>(p, stream);
     if (p.D <= 2048) return launch_bwd_t<T, X, 8, 1, 1>(p, stream);
     if (p.D <= 4096) return launch_bwd_t<T, X, 16, 1, 1>(p, stream);
-    if (p.D <= NORM_ROW_D) return launch_bwd_t<T, X, 16, 1, 2>(p, stream);
+    if constexpr (norm_row_d(sizeof(T) == 4) > 4096)
+        if (p.D <= norm_row_d(sizeof(T) == 4)) return launch_bwd_t<T, X, 16, 1, 2>(p, stream);
     return launch_bwd_wide<T, X>(p, stream);
 }
 

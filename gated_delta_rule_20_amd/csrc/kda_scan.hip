@@ -31,7 +31,7 @@ __device__ __forceinline__ void sequence_of(const ScanParams &p, int s, int *lo,
 // blocks and one state, and what has to pass from one to the next is one state every 4096 rows (one in every 512: 6% slower).  The order in which pairs are joined is fixed, so results do not depend on timing.  Where sequences
 // begin, the state is replaced, and what lies before is not waited for.
 //
-// Bound by the arithmetic (38 instructions a token with the gate, all passes and the hand-over, units busy for 68% of the time) and
+// Bound by the arithmetic (38 instructions a token with the gate, all passes and the hand-over, units busy for about 70% of the time) and
 // by the wait for the segments before, which run at the same time: 131072 rows x 2048 in bf16 with the gate take 503 us,
 // 3.2 TB/s; without waiting they would take about 400.  8192 x 4096: 60 us (3.3 TB/s), with log-decays 57; gradients 102 us, from
 // 8-bit values 98.  With an odd number of channels vectors are read at odd addresses: 8192 x 4001 75 and 152 us.

@@ -213,6 +213,20 @@ def test_repeats_streams_and_graph():
         assert all(torch.equal(a, b) for a, b in zip(kept, both())), i
 
 
+@pytest.mark.parametrize("types", TYPES, ids=["fp32", "bf16", "bf16-fp32"])
+def test_workspace_size_is_enough(types):
+    kda = _kda()
+    for R, D in ((3, 16), (700, 4095), (700, 4097), (2000, 5000), (300, 8192), (40, 8193)):
+        d = _inputs(R, D, *types, False, True, True, True, seed=1)
+        x1, _, saved = kda.block_norm_fwd(d["x"], d["y"], pack=True, **_kw(d))
+        want = kda.block_norm_bwd(x1, d["y"], d["dx"], d["dn"], **_kw(d))
+        for x in (x1, saved.x_new):
+            ws = torch.empty(kda.block_norm_bwd_workspace_size(x), dtype=torch.uint8, device="cuda")
+            kda.block_norm_bwd(x, d["y"], d["dx"], d["dn"], workspace=ws, **_kw(d))
+        got = kda.block_norm_bwd(x1, d["y"], d["dx"], d["dn"], workspace=ws, **_kw(d))
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_many_wide_rows():
     """Rows too wide for one workgroup's registers, more of them than workgroups; rows do not depend on their neighbours, dx over
     dx', one weight's gradient only, a captured call."""
