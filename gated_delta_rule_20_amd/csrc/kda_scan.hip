@@ -28,8 +28,9 @@ __device__ __forceinline__ void sequence_of(const ScanParams &p, int s, int *lo,
 // segment's predecessors run or have run already) and publish what their rows do to a state, a pair (product of decays,
 // state from zero), before waiting for anything.  The last segment of every 8 joins these pairs and publishes the
 // block's; the last of every 64 publishes the state behind it.  So a segment waits for at most 7 pairs of its block, 7 of
-// blocks and one state, and what has to pass from one to the next is one state every 4096 rows (one in every 512: 6% slower).  The order in which pairs are joined is fixed, so results do not depend on timing.  Where sequences
-// begin, the state is replaced, and what lies before is not waited for.
+// blocks and one state, and what has to pass from one to the next is one state every 4096 rows (one in every 512: 6%
+// slower).  The order in which pairs are joined is fixed, so results do not depend on timing.  Where sequences begin, the
+// state is replaced, and what lies before is not waited for.
 //
 // Bound by the arithmetic (38 instructions a token with the gate, all passes and the hand-over, units busy for about 70% of the time) and
 // by the wait for the segments before, which run at the same time: 131072 rows x 2048 in bf16 with the gate take 503 us,
@@ -565,8 +566,8 @@ __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 ? 4 : 3) void scan_
 
 // Gradients, from the last row to the first: D_t = d_h_t + e_{t+1}, e_t = a_t D_t; runs, segments and their order mirrored.
 // h and x are asked for before the wait.  Saved values of a kind that the kernel knows leave room for three waves a SIMD: 8192 x 4096
-// 102 us in bf16, 98 from 8 bits; with a kernel for either, at the time, 180 instead of 114 and 132 instead of 110.  One that finds h in one form and x in the
-// other, or a single segment, takes that kernel.
+// 102 us in bf16, 98 from 8 bits; with a kernel for either, at the time, 180 instead of 114 and 132 instead of 110.  One
+// that finds h in one form and x in the other, or a single segment, takes that kernel.
 template <typename T, typename G, bool GATED, bool CHAIN, Saved S>
 __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 : 2) void scan_bwd_kernel(const ScanParams p)
 {

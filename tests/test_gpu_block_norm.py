@@ -37,7 +37,7 @@ def _kw(d, scale=0.7, eps=1e-6):
 
 
 SIZES = [(1, 1), (3, 5), (2, 8), (5, 127), (7, 512), (4, 513), (9, 1000), (130, 1024), (3, 2051), (600, 64), (33, 4096), (2, 4097),
-         (5, 8192), (3, 10001), (2, 16384)]
+         (5, 8192), (3, 10001), (2, 16384), (7, 390), (6, 511), (11, 1999), (4, 3001), (3, 6), (9, 4094)]
 TYPES = [(FP, FP), (BF, BF), (BF, FP)]
 PARTS = [(True, True, True, True), (True, False, False, True), (False, True, False, True), (False, False, True, False),
          (True, True, False, False), (False, False, False, True)]
