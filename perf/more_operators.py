@@ -250,8 +250,10 @@ def _own_norm_fwd(s):
 
 
 def _own_norm_bwd(s):
+    # codes and scales do not say which type the block has, and without pre no gradient of n does
     return tuple(_kda().block_norm_bwd(_packed(s["x"]), _packed(s["y"]), s["dx"], s["dn"], gate=_packed(s["gate"]),
-                                       post_weight=s["post"], res_scale=s["res"], scale=s["scale"], pre_weight=s["pre"], eps=EPS))
+                                       post_weight=s["post"], res_scale=s["res"], scale=s["scale"], pre_weight=s["pre"], eps=EPS,
+                                       dtype=DTYPES[s["case"]["dtype"]]))
 
 
 def _own_act(s):
