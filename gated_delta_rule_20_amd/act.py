@@ -17,10 +17,27 @@ from .linear import _call, _check_tensors, _on_stream, _required
 ACT_GROUP = 128  # KDA_ACT_GROUP
 
 
-class Packed(NamedTuple):
-    """A tensor [..., D] in 8 bits: ``codes`` [..., D] int8, ``scales`` [..., ceil(D / 128)] fp32; a value is code * scale."""
+class _Pair(NamedTuple):
     codes: torch.Tensor
     scales: torch.Tensor
+
+
+class Packed(_Pair):
+    """A tensor [..., D] in 8 bits: ``codes`` [..., D] int8, ``scales`` [..., ceil(D / 128)] fp32; a value is code * scale.
+
+    ``dtype``: that of the tensor it was made from (calls that pack set it, also of one given to write to), which a backward call goes by
+    where no tensor of its arguments says what type its gradients have; None where it was put together without."""
+    dtype = None
+
+    def __new__(cls, codes, scales, dtype=None):
+        if dtype is not None and dtype not in _DTYPES:
+            raise ValueError(f"unsupported dtype {dtype}")
+        self = super().__new__(cls, codes, scales)
+        self.dtype = dtype
+        return self
+
+    def _replace(self, **fields):
+        return Packed(fields.pop("codes", self.codes), fields.pop("scales", self.scales), fields.pop("dtype", self.dtype), **fields)
 
     @property
     def shape(self):
@@ -43,9 +60,9 @@ def _good(t, device, dtype, shape) -> bool:
     return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()
 
 
-def _new_packed(shape, device):
+def _new_packed(shape, device, dtype):
     return Packed(torch.empty(shape, dtype=torch.int8, device=device),
-                  torch.empty(_scale_shape(shape), dtype=torch.float32, device=device))
+                  torch.empty(_scale_shape(shape), dtype=torch.float32, device=device), dtype)
 
 
 def _check_packed(p, name, shape, device):
@@ -58,13 +75,14 @@ def _check_packed(p, name, shape, device):
                          f"and {tuple(p.scales.shape)}")
 
 
-def _packed_out(pack, name, shape, device):
-    """A forward's 8-bit copy: allocated for True, checked when given, None for False."""
+def _packed_out(pack, name, shape, device, dtype):
+    """A forward's 8-bit copy of a tensor of dtype: allocated for True, checked when given, None for False."""
     if pack is None or pack is False:
         return None
     if pack is True:
-        return _new_packed(shape, device)
+        return _new_packed(shape, device, dtype)
     _check_packed(pack, name, shape, device)
+    pack.dtype = dtype
     return pack
 
 
@@ -130,7 +148,7 @@ def act_pack(x, *, out=None):
         raise ValueError(f"unsupported dtype {x.dtype}")
     at, stride = _rows(x, "x", x.device, x.dtype, x.shape)
     R, D = _two(x)
-    out = _packed_out(True if out is None else out, "out", x.shape, x.device)
+    out = _packed_out(True if out is None else out, "out", x.shape, x.device, x.dtype)
     _call("kda_act_pack", (_DTYPES[x.dtype], at, stride, R, D, out.codes.data_ptr(), out.scales.data_ptr()), x.device)
     return out
 

@@ -104,15 +104,40 @@ def block_norm_fwd(x, y=None, *, gate=None, post_weight=None, res_scale=None, sc
         given = pack if isinstance(pack, BlockNormSaved) else (True, y is not None, gate is not None)
         if (given[1] is None and y is not None) or (given[2] is None and gate is not None):
             raise ValueError("pack must hold a Packed for each of x_new, y and gate that there is")
-        saved = BlockNormSaved(_packed_out(given[0], "pack.x_new", shape, dev),
-                               _packed_out(given[1] if y is not None else None, "pack.y", shape, dev),
-                               _packed_out(given[2] if gate is not None else None, "pack.gate", shape, dev))
+        saved = BlockNormSaved(_packed_out(given[0], "pack.x_new", shape, dev, x.dtype),
+                               _packed_out(given[1] if y is not None else None, "pack.y", shape, dev, dtype),
+                               _packed_out(given[2] if gate is not None else None, "pack.gate", shape, dev, dtype))
         for name, p in zip(("x", "y", "gate"), saved):
             if p is not None:
                 setattr(a, name + "_codes", p.codes.data_ptr())
                 setattr(a, name + "_scales", p.scales.data_ptr())
     _call("kda_block_norm_fwd", (ctypes.byref(a),), dev)
     return (x_out, n, saved) if saved is not None else (x_out, n)
+
+
+def _types(x_new, y, gate, dx_new, dn, dtype, dx, dy, dgate):
+    """(the blocks' dtype, the residual stream's) as the arguments name them: tensors first, since a call checks them, then what a
+    Packed says it was made from, then what the one type settles of the other."""
+    def named(*args):
+        for kind in (torch.Tensor, Packed):
+            for t in args:
+                if isinstance(t, kind) and t.dtype is not None:
+                    return t.dtype
+        return None
+    x_dtype = named(dx_new, x_new, dx)
+    if dtype is None:
+        dtype = named(dn, y, gate, dy, dgate)
+    if dtype is None and (x_dtype is torch.bfloat16 or (y is None and dn is None)):
+        dtype = x_dtype                        # a bf16 stream has bf16 blocks; without blocks no value is of their type
+    if x_dtype is None and dtype is torch.float32:
+        x_dtype = dtype                        # fp32 blocks have an fp32 stream
+    if dtype is None:
+        raise ValueError("nothing names the blocks' dtype: give dtype, or y or the gate as a Packed with its dtype")
+    if x_dtype is None:
+        raise ValueError("nothing names the residual stream's dtype: give dx, or x_new as a Packed with its dtype")
+    if dtype not in _DTYPES or x_dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtypes {dtype}, {x_dtype}")
+    return dtype, x_dtype
 
 
 @_on_stream
@@ -123,21 +148,17 @@ def block_norm_bwd(x_new, y, dx_new, dn=None, *, gate=None, post_weight=None, re
     (gradient of n, the blocks' dtype), one of which may be None (zeros).
 
     x_new: x' as the forward returned it (read, and required, with ``dn`` only); y, gate: its inputs; each a tensor or a
-    :class:`Packed`.  ``dtype``: the blocks' dtype (None: that of dn, else of y, the gate or dy where they are tensors, else of
-    dx_new).  dx may be dx_new; dy and dgate may go to rows of any even spacing.  Returns a
-    :class:`BlockNormGrads`; the weights' gradients are fp32, None where there is no weight or without ``need_dweights``."""
+    :class:`Packed`.  ``dtype``: the blocks' dtype (None: that of dn, y, the gate, dy or dgate; the stream's is that of dx_new,
+    x_new or dx).  A type that none of these names (a Packed may not know its own) is not guessed: the call is refused.  dx may be dx_new;
+    dy and dgate may go to rows of any even spacing.  Returns a :class:`BlockNormGrads`, dx in the stream's dtype, dy and dgate in the
+    blocks'; the weights' gradients are fp32, None where there is no weight or without ``need_dweights``."""
     ref = dx_new if dx_new is not None else dn
     _stream_rows(ref, "dx_new" if dx_new is not None else "dn")
     dev, shape = ref.device, ref.shape
     R, D = _two(ref)
     if dn is not None:
         _stream_rows(dn, "dn")
-    if dtype is None:
-        dtype = next((t.dtype for t in (dn, y, gate, dy) if isinstance(t, torch.Tensor)), ref.dtype)
-    x_dtype = dx_new.dtype if dx_new is not None else x_new.dtype if isinstance(x_new, torch.Tensor) else \
-        dx.dtype if dx is not None else dtype
-    if dtype not in _DTYPES or x_dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtypes {dtype}, {x_dtype}")
+    dtype, x_dtype = _types(x_new, y, gate, dx_new, dn, dtype, dx, dy, dgate)
     if y is None and (gate is not None or post_weight is not None or res_scale is not None):
         raise ValueError("gate, post_weight and res_scale belong to y, which is None")
     if dn is not None and pre_weight is None:

@@ -84,7 +84,7 @@ def gated_scan_fwd(x, g, *, A_log=None, g_min: float = -5.0, complement: bool = 
     if final_state is None and output_final_state:
         final_state = torch.empty(shape, dtype=torch.float32, device=dev)
     _state(final_state, "final_state", shape, dev)
-    h8 = _packed_out(pack, "pack", x.shape, dev)
+    h8 = _packed_out(pack, "pack", x.shape, dev, x.dtype)
     a = GatedScanFwdArgs(B, T, C, _DTYPES[x.dtype], g_dtype, x_at, x_stride, g_at, g_stride, _at(A_log), g_min, complement,
                          _at(cu_seqlens), N, _at(initial_state), _at(out), _at(final_state),
                          _at(h8.codes) if h8 else None, _at(h8.scales) if h8 else None, None, 0)
