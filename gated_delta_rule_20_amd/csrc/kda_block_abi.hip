@@ -459,6 +459,8 @@ static kda_status_t check_act(int dtype, int64_t R, int32_t D)
 {
     KDA_TRY(check_dtype(dtype, "dtype"));
     if (R < 0 || D < 1) return fail(KDA_ERROR_INVALID_VALUE, "need R >= 0 and D >= 1 (got %lld, %d)", (long long)R, D);
+    // channels are indexed in 32 bits, and R * per below stays within 64
+    if (D > (1 << 24)) return fail(KDA_ERROR_NOT_SUPPORTED, "D=%d: at most 2^24", D);
     // one workgroup packs 16 groups
     const int64_t per = ((int64_t)D + kda::ACT_GROUP - 1) / kda::ACT_GROUP;
     if (R > ((int64_t)1 << 40) || !launchable((R * per + 15) / 16, 256)) return fail(KDA_ERROR_NOT_SUPPORTED, "R * D too large for one call");

@@ -513,7 +513,7 @@ KDA_API kda_status_t kda_cache_compact(const kda_cache_pool_t *pools, int32_t n_
  */
 #define KDA_ACT_GROUP 128
 
-/* Packs R rows of D values (x_stride elements apart) of type dtype; unpacks to dense rows. */
+/* Packs R rows of 1 <= D <= 2^24 values (x_stride elements apart) of type dtype; unpacks to dense rows. */
 KDA_API kda_status_t kda_act_pack(int32_t dtype, const void *x, int64_t x_stride, int64_t R, int32_t D, int8_t *codes,
                                   float *scales, void *stream);
 KDA_API kda_status_t kda_act_unpack(int32_t dtype, const int8_t *codes, const float *scales, int64_t R, int32_t D, void *x,
