@@ -211,10 +211,13 @@ def block_norm_bwd(x_new, y, dx_new, dn=None, *, gate=None, post_weight=None, re
 def block_norm_bwd_workspace_size(x_new, *, weights: int = 3) -> int:
     """Workspace bytes :func:`block_norm_bwd` needs for x_new [..., D] when gradients of ``weights`` weights are wanted."""
     R, D = _two(x_new.codes if isinstance(x_new, Packed) else x_new)
-    # float32 blocks need the most
-    dtype = torch.float32 if isinstance(x_new, Packed) else x_new.dtype
-    if dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {dtype}")
-    a = BlockNormBwdArgs(R, D, _DTYPES[dtype], _DTYPES[dtype], scale=1.0)
-    a.d_pre_weight = 16 if weights else None   # only whether one is given is read
-    return _need("kda_block_norm_bwd_workspace_size", a)
+    x_dtype = x_new.dtype
+    if x_dtype is not None and x_dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {x_dtype}")
+    need = 0
+    # the stream does not say what blocks it has, but for a bf16 one
+    for dtype in (torch.bfloat16,) if x_dtype is torch.bfloat16 else (torch.bfloat16, torch.float32):
+        a = BlockNormBwdArgs(R, D, _DTYPES[dtype], _DTYPES[dtype], scale=1.0)
+        a.d_pre_weight = 16 if weights else None   # only whether one is given is read
+        need = max(need, _need("kda_block_norm_bwd_workspace_size", a))
+    return need

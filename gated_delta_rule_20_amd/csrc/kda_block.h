@@ -9,13 +9,16 @@
 namespace kda {
 
 constexpr int ACT_GROUP = 128;        // channels that share a scale
-constexpr int NORM_MAX_D = 16384;     // channels of a row that block norms hold in registers
+constexpr int NORM_MAX_D = 16384;     // channels of a row
 
 // Block norms backwards: up to norm_row_d channels a workgroup holds whole rows, beyond columns of NORM_COLUMN channels.  In
 // float32 a row of 8192 does not fit the registers next to its sums: 4096 x 8192 412 us by rows, 370 by columns, 16 x 8192 48 and 27.
 // With bf16 it does: 141 and 230 us, 27 and 28 (next to a float32 stream 231 and 282, 38 and 27).
 constexpr int norm_row_d(bool f32) { return f32 ? 4096 : 8192; }
 constexpr int NORM_COLUMN = 1024;
+
+// Rows that the gradients add up in float32 (64 roundings); such sums are joined in float64.
+constexpr int NORM_CHAIN = 64;
 
 // Rows that a workgroup holds side by side, and its waves.
 constexpr int norm_rows(int D) { return D <= 256 ? 4 : D <= 512 ? 2 : 1; }
@@ -106,9 +109,9 @@ struct NormParams {
     void *dx, *dy, *dgate;
     int64_t dy_stride, dgate_stride;
     float *dpost, *dres, *dpre;       // [D] or null
-    float *part;                      // [3, parts, D]
+    float *part;                      // [3, parts, D]: rows of up to norm_row_d channels leave several for each workgroup, in turn
     float __attribute__((ext_vector_type(4))) *numbers;  // [R], beyond norm_row_d channels
-    int parts;
+    int parts, groups;                // sums; workgroups a column
 };
 
 hipError_t launch_norm_fwd(int bf16, int x_bf16, const NormParams &p, hipStream_t stream);

@@ -201,26 +201,34 @@ template <typename A> kda_status_t plan_norm(const A *a, kda::NormParams *p)
     return KDA_SUCCESS;
 }
 
-// Workgroups of the backward pass: 16 waves on each of 256 units, and four rows at least for each, since each leaves
-// its own sums of the weights' gradients.
-// Workgroups of the gradients, each with sums of its own: four rows a side at least, 16 waves (of columns: 32) on each of 256 units at most.
+// Workgroups of the gradients, and the float32 sums of the weights' gradients that they leave: four rows a side at least for a workgroup,
+// 16 waves (of columns: 32) on each of 256 units at most.  A sum is of NORM_CHAIN rows a side at most, so that what it may be off by does not
+// grow with the rows: by rows a workgroup leaves one after the other, by columns there are more workgroups.  (65536 x 4096 1019 us; with
+// one sum a workgroup 968, then of equal rows off by 64 roundings instead of 16; 2^20 x 256 927 and 908.)
 // (One row at least: 256 x 4096 23.5 us either way, with four times the sums; 16: 42.5.)
-int norm_parts(int R, int D, bool columns)
+void norm_parts(int R, int D, bool columns, kda::NormParams *p)
 {
-    const int rows = 4 * kda::norm_rows(D);
+    const int side = kda::norm_rows(D), rows = 4 * side;
     const int most = columns ? 256 * 8 / ((D + kda::NORM_COLUMN - 1) / kda::NORM_COLUMN) : 256 * 16 / kda::norm_waves(D);
     const int n = R / rows + (R % rows != 0);
-    return n < most ? n : most;
+    p->groups = p->parts = n < most ? n : most;
+    const int turn = most * side * kda::NORM_CHAIN;        // rows (2^18 at most)
+    if (R > turn) p->parts = most * (R / turn + (R % turn != 0));
+    if (columns) p->groups = p->parts;
 }
 
-size_t plan_norm_bwd(const kda_block_norm_bwd_args_t *a, kda::NormParams *p)
+kda_status_t plan_norm_bwd(const kda_block_norm_bwd_args_t *a, kda::NormParams *p, size_t *bytes)
 {
     const bool columns = a->D > kda::norm_row_d(a->dtype == KDA_F32);
-    p->parts = norm_parts(a->R, a->D, columns);
+    norm_parts(a->R, a->D, columns, p);
+    const long long wide = (a->D + kda::NORM_COLUMN - 1) / kda::NORM_COLUMN;
+    if (columns && !launchable(p->groups * wide, 256))
+        return fail(KDA_ERROR_NOT_SUPPORTED, "R * D too large for one call");
     Carver c(a->workspace);
     if (a->d_post_weight || a->d_res_scale || a->d_pre_weight) p->part = (float *)c.take(sizeof(float) * 3 * (size_t)p->parts * a->D);
     if (columns) p->numbers = (decltype(p->numbers))c.take(16 * (size_t)a->R);
-    return c.used;
+    *bytes = c.used;
+    return KDA_SUCCESS;
 }
 
 }  // namespace
@@ -397,7 +405,7 @@ kda_status_t kda_block_norm_bwd_workspace_size(const kda_block_norm_bwd_args_t *
     if (!a || !bytes) return fail(KDA_ERROR_INVALID_VALUE, "args or bytes is NULL");
     kda::NormParams p;
     KDA_TRY(plan_norm(a, &p));
-    *bytes = plan_norm_bwd(a, &p);
+    KDA_TRY(plan_norm_bwd(a, &p, bytes));
     return ok();
 }
 
@@ -448,7 +456,9 @@ kda_status_t kda_block_norm_bwd(const kda_block_norm_bwd_args_t *a, void *stream
     p.dpost = a->d_post_weight;
     p.dres = a->d_res_scale;
     p.dpre = a->d_pre_weight;
-    KDA_TRY(check_workspace(a->workspace, a->workspace_bytes, plan_norm_bwd(a, &p)));
+    size_t need = 0;
+    KDA_TRY(plan_norm_bwd(a, &p, &need));
+    KDA_TRY(check_workspace(a->workspace, a->workspace_bytes, need));
     if (p.R == 0 && !p.dpost && !p.dres && !p.dpre) return ok();
     const hipError_t e = kda::launch_norm_bwd(a->dtype == KDA_BF16, a->x_dtype == KDA_BF16, p, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "kda_block_norm_bwd launch");

@@ -229,23 +229,23 @@ __device__ __forceinline__ Sigmoid sigmoid2(float x)
     return {shut ? 0.f : s, e * s};
 }
 
-// The sum over `rows` rows of column blockIdx.x * 16 + thread % 16 of a matrix of C columns, on threads 0 .. 15 of 256: in
+// The sum over `rows` rows of column blockIdx.x * 16 + thread % 16 of a matrix of C columns, on threads 0 .. 15 of 16 SLICES: in
 // float64, in a fixed order.
-__device__ __forceinline__ double column_sum(const float *part, int rows, int C, double (*s)[16])
+template <int SLICES> __device__ __forceinline__ double column_sum(const float *part, int rows, int C, double (*s)[16])
 {
     const int l = threadIdx.x & 15, slice = threadIdx.x >> 4, c = blockIdx.x * 16 + l;
     double sum = 0.0;
-    for (int i = slice; i < rows; i += 8 * 16) {
+    for (int i = slice; i < rows; i += 8 * SLICES) {
         float v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = c < C && i + 16 * u < rows ? part[(size_t)(i + 16 * u) * C + c] : 0.f;
+        for (int u = 0; u < 8; ++u) v[u] = c < C && i + SLICES * u < rows ? part[(size_t)(i + SLICES * u) * C + c] : 0.f;
 #pragma unroll
         for (int u = 0; u < 8; ++u) sum += v[u];
     }
     s[slice][l] = sum;
     __syncthreads();
     if (slice > 0) return 0.0;
-    for (int k = 1; k < 16; ++k) sum += s[k][l];
+    for (int k = 1; k < SLICES; ++k) sum += s[k][l];
     return sum;
 }
 

@@ -519,9 +519,43 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
         }
     };
     next.clear();                                          // lanes without channels keep zeros
-    const int step = p.parts * ROWS;
+    // The sums so far, of all sides in their order, to the next of the workgroup's places.
+    int part = blockIdx.x;
+    const auto flush = [&]() {
+        bool stores = true;
+        if constexpr (ROWS > 1) {                          // (NQ 1)
+            f32x4 *at = reinterpret_cast<f32x4 *>(s_mem) + t;
+            if (side > 0) {
+                at[(side - 1) * 3 * NT] = a_post[0];
+                at[((side - 1) * 3 + 1) * NT] = a_res[0];
+                at[((side - 1) * 3 + 2) * NT] = a_pre[0];
+                stores = false;
+            }
+            __syncthreads();
+            if (stores)
+                for (int k = 0; k < ROWS - 1; ++k) {
+                    a_post[0] += at[k * 3 * NT];
+                    a_res[0] += at[(k * 3 + 1) * NT];
+                    a_pre[0] += at[(k * 3 + 2) * NT];
+                }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            if (stores && count(j) > 0) store_sums(p, part, channel(j), count(j), a_post[j], a_res[j] * p.scale, a_pre[j]);
+            a_post[j] = a_res[j] = a_pre[j] = zero;
+        }
+        part += gridDim.x;
+    };
+    const unsigned step = gridDim.x * ROWS;
+    int held = 0;                                          // rows of a side that the sums hold
     if (KEEP) load(blockIdx.x * ROWS + side);
-    for (int row0 = blockIdx.x * ROWS; row0 < p.R; row0 += step) {
+    for (unsigned row0 = blockIdx.x * ROWS; row0 < (unsigned)p.R; row0 += step) {
+        if (held == NORM_CHAIN) {
+            flush();
+            held = 0;
+        }
+        ++held;
         const int row = row0 + side;
         const bool in = ROWS == 1 || row < p.R;            // a side without a row adds zeros
         const size_t r = min(row, p.R - 1);
@@ -529,7 +563,7 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
         Values<T, X, V> now = next;
         if constexpr (RAGGED)
             if (ragged) now.drop(p, cnt > 0 ? V - cnt : 0);
-        if (KEEP && row0 + step < p.R) load(row + step);
+        if (KEEP && row0 + step < (unsigned)p.R) load(row + step);
         float s[6] = {};
         Floats f;
 #pragma unroll
@@ -554,24 +588,8 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
             if (!KEEP) __builtin_amdgcn_sched_barrier(0);
         }
     }
-    if (ROWS > 1) {                                        // the sides' sums, in their order (NQ 1)
-        f32x4 *at = reinterpret_cast<f32x4 *>(s_mem) + t;
-        if (side > 0) {
-            at[(side - 1) * 3 * NT] = a_post[0];
-            at[((side - 1) * 3 + 1) * NT] = a_res[0];
-            at[((side - 1) * 3 + 2) * NT] = a_pre[0];
-        }
-        __syncthreads();
-        if (side > 0) return;
-        for (int k = 0; k < ROWS - 1; ++k) {
-            a_post[0] += at[k * 3 * NT];
-            a_res[0] += at[(k * 3 + 1) * NT];
-            a_pre[0] += at[(k * 3 + 2) * NT];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < NQ; ++j)
-        if (count(j) > 0) store_sums(p, blockIdx.x, channel(j), count(j), a_post[j], a_res[j] * p.scale, a_pre[j]);
+    flush();
+    if (part < p.parts) flush();                           // others had a row more, one place further: zeros
 }
 
 // Rows of more than norm_row_d channels do not fit a workgroup's registers next to the weights and their sums (as one such kernel
@@ -621,10 +639,10 @@ template <typename T, typename X> __global__ __launch_bounds__(256, 4) void norm
     Values<T, X, 4> next;
     next.clear();
     if (part < p.R) next.load(p, part, c, n);
-    for (int r = part; r < p.R; r += p.parts) {
+    for (unsigned r = part; r < (unsigned)p.R; r += p.parts) {
         const Values<T, X, 4> now = next;
         const RowNumbers k(p.numbers[r]);
-        if (r + p.parts < p.R) next.load(p, r + p.parts, c, n);
+        if (r + p.parts < (unsigned)p.R) next.load(p, r + p.parts, c, n);
         Floats f;
         now.get(p, 0, true, f);
         float G[4], dy[4], dgate[4];
@@ -634,15 +652,16 @@ template <typename T, typename X> __global__ __launch_bounds__(256, 4) void norm
     store_sums(p, part, c, n, post, res * p.scale, pre);
 }
 
-// The weights' gradients from the workgroups' sums, in their order.  16 columns a workgroup (64 bytes of a row), 16 threads down
-// each, eight rows on their way: 7.3 us for 256 x 3 x 4096 sums (with 64 columns and 4 threads, one row at a time, 36 us
-// for twice as many).
-__global__ __launch_bounds__(256) void norm_sum_kernel(const NormParams p)
+// The weights' gradients from the workgroups' sums, in their order.  16 columns a workgroup (64 bytes of a row), SLICES threads down
+// each, eight rows on their way: 7.4 us for 256 x 3 x 4096 sums (with 64 columns and 4 threads, one row at a time, 36 us
+// for twice as many).  The many sums of very many rows, over few columns, take four times the threads: 4096 x 3 x 256 33 us (with 16
+// threads 68).
+template <int SLICES> __global__ __launch_bounds__(16 * SLICES) void norm_sum_kernel(const NormParams p)
 {
-    __shared__ double s_part[16][16];
+    __shared__ double s_part[SLICES][16];
     float *out = blockIdx.y == 0 ? p.dpost : blockIdx.y == 1 ? p.dres : p.dpre;
     if (!out) return;
-    const double sum = column_sum(p.part + (size_t)blockIdx.y * p.parts * p.D, p.parts, p.D, s_part);
+    const double sum = column_sum<SLICES>(p.part + (size_t)blockIdx.y * p.parts * p.D, p.parts, p.D, s_part);
     const int c = blockIdx.x * 16 + threadIdx.x;
     if (threadIdx.x < 16 && c < p.D) out[c] = (float)sum;
 }
@@ -656,8 +675,13 @@ template <typename T, typename X, int NW, int ROWS, int NCH> static hipError_t l
 
 static hipError_t launch_sum(const NormParams &p, hipStream_t stream)
 {
-    if (p.dpost || p.dres || p.dpre)
-        hipLaunchKernelGGL(norm_sum_kernel, dim3((p.D + 15) / 16, 3), dim3(256), 0, stream, p);
+    if (p.dpost || p.dres || p.dpre) {
+        const dim3 grid((p.D + 15) / 16, 3);
+        if (p.parts > 1024)
+            hipLaunchKernelGGL((norm_sum_kernel<64>), grid, dim3(1024), 0, stream, p);
+        else
+            hipLaunchKernelGGL((norm_sum_kernel<16>), grid, dim3(256), 0, stream, p);
+    }
     return hipGetLastError();
 }
 
@@ -683,7 +707,7 @@ template <typename T, typename X, int NW, int ROWS, int NQ> static hipError_t la
             const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
             if (e != hipSuccess) return e;
         }
-        hipLaunchKernelGGL(kernel, dim3(p.parts), dim3(64 * NW * ROWS), lds, stream, p);
+        hipLaunchKernelGGL(kernel, dim3(p.groups), dim3(64 * NW * ROWS), lds, stream, p);
     }
     return launch_sum(p, stream);
 }

@@ -724,7 +724,7 @@ __global__ __launch_bounds__(256) void scan_clear_kernel(ScanChain k, const floa
 __global__ __launch_bounds__(256) void scan_sum_kernel(const float *part, int parts, int C, float *out)
 {
     __shared__ double s_part[16][16];
-    const double sum = column_sum(part, parts, C, s_part);
+    const double sum = column_sum<16>(part, parts, C, s_part);
     const int c = blockIdx.x * 16 + threadIdx.x;
     if (threadIdx.x < 16 && c < C) out[c] = (float)sum;
 }

@@ -679,7 +679,9 @@ KDA_API kda_status_t kda_block_norm_fwd(const kda_block_norm_fwd_args_t *args, v
  *   dgate = dr u S (1 - S) (dtype, dgate_stride) du = dr S
  *   d_post_weight = sum du y^                    d_pre_weight = sum d_n x^   (sums over the rows, [D] float32, or NULL)
  *   dy = (post_weight du - y^ mean(post_weight du y^)) / rms(y), or du   (dtype, dy_stride)
- * x_new is read only with d_n.  Results do not depend on the order in which workgroups run.
+ * x_new is read only with d_n.  Sums over the rows are of 64 rows at most (a workgroup's side) in float32, four of these at most
+ * added in float32, and in float64 from there, so their error does not grow with R.  Results do not depend on the order in which
+ * workgroups run.  The workspace grows by 12 D bytes for every 64 rows or more.
  */
 typedef struct {
     int32_t R, D;
