@@ -66,6 +66,8 @@ def block_norm_fwd(x, y=None, *, gate=None, post_weight=None, res_scale=None, sc
     (without pre_weight there is no n).  Without y there is no block before: x' is x itself and only n is computed (in
     ``n_out``'s dtype when given, else x's).  x_out may be x.  ``pack`` (True or a :class:`BlockNormSaved` to write to): x', y
     and the gate in 8 bits as well.  Returns (x', n or None), with ``pack`` (x', n or None, BlockNormSaved)."""
+    if n_out is not None and pre_weight is None:
+        raise ValueError("n_out without pre_weight: there is no n")
     _stream_rows(x, "x")
     dev, shape = x.device, x.shape
     R, D = _two(x)
@@ -152,6 +154,10 @@ def block_norm_bwd(x_new, y, dx_new, dn=None, *, gate=None, post_weight=None, re
     x_new or dx).  A type that none of these names (a Packed may not know its own) is not guessed: the call is refused.  dx may be dx_new;
     dy and dgate may go to rows of any even spacing.  Returns a :class:`BlockNormGrads`, dx in the stream's dtype, dy and dgate in the
     blocks'; the weights' gradients are fp32, None where there is no weight or without ``need_dweights``."""
+    if dy is not None and y is None:
+        raise ValueError("dy without y: there is no such gradient")
+    if dgate is not None and gate is None:
+        raise ValueError("dgate without gate: there is no such gradient")
     ref = dx_new if dx_new is not None else dn
     _stream_rows(ref, "dx_new" if dx_new is not None else "dn")
     dev, shape = ref.device, ref.shape
@@ -183,7 +189,6 @@ def block_norm_bwd(x_new, y, dx_new, dn=None, *, gate=None, post_weight=None, re
         _check_tensors(dev, x_dtype, dx=dx)
         if dx.shape != shape:
             raise ValueError(f"dx must be {tuple(shape)}, got {tuple(dx.shape)}")
-    dy, dgate = (dy if y is not None else None), (dgate if gate is not None else None)
     if y is not None:
         y_at, y_stride, y_scales = _saved(y, "y", dev, dtype, shape)
         if dy is None:
