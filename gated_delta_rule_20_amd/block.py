@@ -15,7 +15,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _DTYPES, BlockNormBwdArgs, BlockNormFwdArgs
+from . import _DTYPES, BlockNormBwdArgs, BlockNormFwdArgs, _dev
 from .act import Packed, _good, _packed_out, _rows, _saved, _two
 from .linear import _at, _call, _check_tensors, _like, _need, _on_stream, _required, _workspace
 
@@ -53,7 +53,7 @@ def _stream_rows(x, name):
     if x.dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {x.dtype}")
     if not x.is_cuda or not x.is_contiguous():
-        _required(x.device, x.dtype, **{name: x})
+        _dev(x, name)
 
 
 @_on_stream

@@ -1,5 +1,5 @@
-"""Buffers for results that a call does not compute, and 8-bit copies asked for by something else than a Packed, are refused with a
-ValueError before anything else is looked at (CPU only)."""
+"""Buffers for results that a call does not compute, host tensors and 8-bit copies asked for by something else than a Packed are refused with a
+ValueError (CPU only)."""
 import pytest
 import torch
 
@@ -17,4 +17,14 @@ P = kda.Packed(torch.zeros(4, 8, dtype=torch.int8), torch.zeros(4, 1))
 ])
 def test_results_that_are_not_computed(call, name):
     with pytest.raises(ValueError, match=name):
+        call()
+
+
+@pytest.mark.parametrize("call", [
+    lambda: kda.block_norm_fwd(X, pre_weight=W), lambda: kda.block_norm_fwd(X, pre_weight=W, n_out=X), lambda: kda.block_norm_fwd(X),
+    lambda: kda.block_norm_bwd(X, None, X, X, pre_weight=W), lambda: kda.block_norm_bwd(X, None, None, X, pre_weight=W),
+    lambda: kda.block_norm_bwd(None, None, X), lambda: kda.block_norm_bwd(P, None, X, X, pre_weight=W),
+])
+def test_host_tensors_without_a_block(call):
+    with pytest.raises(ValueError, match="device tensor"):
         call()
