@@ -81,6 +81,8 @@ def _packed_out(pack, name, shape, device, dtype):
         return None
     if pack is True:
         return _new_packed(shape, device, dtype)
+    if not isinstance(pack, Packed):
+        raise ValueError(f"{name} must be a Packed")
     _check_packed(pack, name, shape, device)
     pack.dtype = dtype
     return pack

@@ -68,6 +68,8 @@ def block_norm_fwd(x, y=None, *, gate=None, post_weight=None, res_scale=None, sc
     and the gate in 8 bits as well.  Returns (x', n or None), with ``pack`` (x', n or None, BlockNormSaved)."""
     if n_out is not None and pre_weight is None:
         raise ValueError("n_out without pre_weight: there is no n")
+    if pack is not None and not isinstance(pack, (bool, BlockNormSaved)):
+        raise ValueError("pack must be True, False or a BlockNormSaved")
     _stream_rows(x, "x")
     dev, shape = x.device, x.shape
     R, D = _two(x)
@@ -214,7 +216,10 @@ def block_norm_bwd(x_new, y, dx_new, dn=None, *, gate=None, post_weight=None, re
 
 
 def block_norm_bwd_workspace_size(x_new, *, weights: int = 3) -> int:
-    """Workspace bytes :func:`block_norm_bwd` needs for x_new [..., D] when gradients of ``weights`` weights are wanted."""
+    """Workspace bytes :func:`block_norm_bwd` needs for x_new [..., D] (where the call has none: dx_new) when gradients of ``weights``
+    weights are wanted."""
+    if not isinstance(x_new, (torch.Tensor, Packed)):
+        raise ValueError("x_new must be a tensor or a Packed; without one give dx_new")
     R, D = _two(x_new.codes if isinstance(x_new, Packed) else x_new)
     x_dtype = x_new.dtype
     if x_dtype is not None and x_dtype not in _DTYPES:

@@ -28,3 +28,21 @@ def test_results_that_are_not_computed(call, name):
 def test_host_tensors_without_a_block(call):
     with pytest.raises(ValueError, match="device tensor"):
         call()
+
+
+@pytest.mark.parametrize("pack", [P, (P, P, P), [P, P, P], 1, X, "yes"])
+def test_norm_copies_go_to_a_BlockNormSaved(pack):
+    with pytest.raises(ValueError, match="pack must be"):
+        kda.block_norm_fwd(X, X, pack=pack)
+
+
+@pytest.mark.parametrize("pack", [1, X, (P.codes, P.scales), "yes"])
+def test_other_copies_go_to_a_Packed(pack):
+    from gated_delta_rule_20_amd.act import _packed_out
+    with pytest.raises(ValueError, match="pack must be"):
+        _packed_out(pack, "pack", X.shape, X.device, X.dtype)
+
+
+def test_workspace_size_without_a_stream():
+    with pytest.raises(ValueError, match="x_new"):
+        kda.block_norm_bwd_workspace_size(None)
