@@ -43,6 +43,11 @@ constexpr int SCAN_ROWS = 64, SCAN_CHANNELS = 128;
 // Segments that join their pairs, and blocks of them that join theirs; counters that lie 128 bytes apart.
 constexpr int SCAN_BLOCK = 8, SCAN_TICKET_STEP = 32;
 
+// Up to so many packed sequences, segments go through the offsets that fall among their rows and pass on the states of empty sequences
+// themselves; of more, they search the offsets and a kernel of its own passes the states on.  (2^16 empty sequences in one place take
+// 14 ms of one workgroup, for which the segments behind wait; 2^22 740 ms, longer than they do.)
+constexpr int SCAN_MANY = 1 << 16;
+
 // Hand-over between segments, cleared at the start of a call: pairs of decay and state for each segment and each
 // SCAN_BLOCK segments [.., C], the state behind every SCAN_BLOCK^2 [.., C]; the tickets of each SCAN_CHANNELS channels;
 // whether a wait was given up.

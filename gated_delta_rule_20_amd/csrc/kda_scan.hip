@@ -71,7 +71,7 @@ struct Offsets {
     }
 };
 
-// Notes where sequences begin and end among rows [r0, r0 + SCAN_ROWS).  Sequences without rows that fall here (into
+// Notes where sequences begin and end among rows [r0, r0 + SCAN_ROWS).  Of up to SCAN_MANY sequences those without rows that fall here (into
 // the last segment: or behind it) get their resulting state at once, for channels [c0, c0 + SCAN_CHANNELS).
 __device__ __forceinline__ void mark_rows(const ScanParams &p, const Offsets &o, int r0, bool tail, Marks &m, const float *from,
                                           float *to, int c0)
@@ -94,6 +94,18 @@ __device__ __forceinline__ void mark_rows(const ScanParams &p, const Offsets &o,
         }
         if (p.T == 0 && to)
             for (int s = t; s < p.N; s += 256) pass_on(s);
+    } else if (p.N > SCAN_MANY) {
+        const int r = r0 + t;
+        if (t < SCAN_ROWS && r < p.rows) {
+            int s = o.lo, a, b;                             // the last sequence that begins at row r or before
+            for (int hi = p.N; hi - s > 1;) {
+                const int mid = s + (hi - s) / 2;
+                if (p.cu[mid] <= r) s = mid; else hi = mid;
+            }
+            sequence_of(p, s, &a, &b);
+            if (r == a && b > a) m.first[t] = s, any = true;
+            if (r == b - 1 && b > a) m.last[t] = s, any = true;
+        }
     } else {
         int a = o.a, b = o.b;
         for (int s = o.lo + t; s < p.N; s += 256) {
@@ -720,6 +732,17 @@ __global__ __launch_bounds__(256) void scan_clear_kernel(ScanChain k, const floa
     for (size_t i = at; i < states; i += step) to[i] = from[i];
 }
 
+// More than SCAN_MANY sequences: those without rows keep their state.  A wave a sequence.
+__global__ __launch_bounds__(256) void scan_empty_kernel(const ScanParams p, const float *from, float *to)
+{
+    for (size_t s = (size_t)blockIdx.x * 4 + threadIdx.x / 64; s < (size_t)p.N; s += (size_t)gridDim.x * 4) {
+        int a, b;
+        sequence_of(p, (int)s, &a, &b);
+        if (b > a) continue;
+        for (int c = threadIdx.x % 64; c < p.C; c += 64) to[s * p.C + c] = from ? from[s * p.C + c] : 0.f;
+    }
+}
+
 // Sums of the segments' parts, in their order: 4.7 us for 128 x 4096.
 __global__ __launch_bounds__(256) void scan_sum_kernel(const float *part, int parts, int C, float *out)
 {
@@ -781,6 +804,13 @@ static hipError_t launch_clear(const ScanParams &p, const float *states, hipStre
     return hipGetLastError();
 }
 
+static void launch_empty(const ScanParams &p, const float *from, float *to, hipStream_t stream)
+{
+    if (!p.cu || p.N <= SCAN_MANY || !to) return;
+    const int grid = p.N / 4 < 8192 ? p.N / 4 : 8192;
+    hipLaunchKernelGGL(scan_empty_kernel, dim3(grid), dim3(256), 0, stream, p, from, to);
+}
+
 template <typename T, typename G> static hipError_t launch_fwd_t(ScanParams p, hipStream_t stream)
 {
     const dim3 grid((unsigned)p.chain.segments * ((p.C + SCAN_CHANNELS - 1) / SCAN_CHANNELS));
@@ -790,6 +820,7 @@ template <typename T, typename G> static hipError_t launch_fwd_t(ScanParams p, h
     const auto kernel = p.A_log ? p.chain.words ? scan_fwd_kernel<T, G, true, true> : scan_fwd_kernel<T, G, true, false>
                                 : p.chain.words ? scan_fwd_kernel<T, G, false, true> : scan_fwd_kernel<T, G, false, false>;
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
+    launch_empty(p, p.h0, p.hT, stream);
     return hipGetLastError();
 }
 
@@ -809,6 +840,7 @@ template <typename T, typename G> static hipError_t launch_bwd_t(ScanParams p, h
                         : packed         ? scan_bwd_kernel<T, G, false, true, CODES>
                                          : scan_bwd_kernel<T, G, false, true, ELEMENTS>;
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
+    launch_empty(p, p.dhT, p.dh0, stream);
     if (p.dA)
         hipLaunchKernelGGL(scan_sum_kernel, dim3((p.C + 15) / 16), dim3(256), 0, stream, p.dA_part, p.chain.segments, p.C, p.dA);
     return hipGetLastError();
