@@ -1,5 +1,7 @@
 // kda_scan.hip -- the gated scan  h_t = a_t h_{t-1} + m_t x_t  per channel:
 // whole sequences, their gradients, one token.
+#include <float.h>
+
 #include "kda_block_dev.h"
 
 namespace kda {
@@ -455,7 +457,8 @@ template <bool GATED> struct Gates {
     // d log_decay / d z, but for g_min e^A
     __device__ __forceinline__ float slope(float z, int j) const
     {
-        const float e = __builtin_amdgcn_exp2f(fminf(z * k[j], 120.f)), s = __builtin_amdgcn_rcpf(1.f + e);
+        // e^-|y| (1 / (1 + e^-|y|))^2: 0 far out on either side
+        const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(z * k[j])), s = __builtin_amdgcn_rcpf(1.f + e);
         return s * (e * s);
     }
 };
@@ -694,7 +697,8 @@ __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 
                         out[j] = e[j] * prev[j];
                         if (GATED) {
                             out[j] *= unit[j] * gates.slope(z[i][j], j);
-                            dA[j] += out[j] * z[i][j];
+                            // (a logit of infinity has no gradient: 0 times the largest number)
+                            dA[j] += out[j] * __builtin_amdgcn_fmed3f(z[i][j], -FLT_MAX, FLT_MAX);
                         }
                     }
                     if (free.on) Raw4<G>::store(to_g.at(), CH, out); else win.put(to_g.at(), out);

@@ -101,7 +101,8 @@ def gated_scan_bwd(x, g, h, d_h, *, A_log=None, g_min: float = -5.0, complement:
     ``dfinal_state`` ([N, C] fp32, None: zeros).
 
     h: what the forward returned, or its :class:`Packed`; read (and required) with ``need_dg`` only.  x: read with ``complement``
-    and ``need_dg`` only (None otherwise), a tensor or a Packed.  dx, dg: results may go to rows of any even spacing.
+    and ``need_dg`` only (None otherwise), a tensor or a Packed.  dx, dg: results may go to rows of any even spacing.  A log-decay above 0,
+    which the forward counts as 0, gets the gradient at 0 (not the 0 of a clamped value); an infinite logit has none.
     Returns (dx, dg, dA_log, dinitial_state); dg, of g's dtype, is None without ``need_dg``, dA_log fp32 None without A_log or
     ``need_dg``."""
     B, T, C, N = _tokens(d_h, "d_h", cu_seqlens)

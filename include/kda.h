@@ -568,7 +568,7 @@ KDA_API kda_status_t kda_gated_scan_fwd(const kda_gated_scan_fwd_args_t *args, v
  *   dx_t = m_t D_t   (dtype, dx_stride)
  *   dg_t = e_t (h_{t-1} - [complement] x_t), through the gate to the logits with A_log
  *          (g_dtype, dg_stride), or dg NULL if not wanted.  A g above 0 gets the gradient of
- *          the 0 it counts as.
+ *          the 0 it counts as (not 0); an infinite logit has none and adds nothing to dA_log.
  *   dA_log : [C] float32, the sum of z_t dz_t over all tokens, or NULL; needs dg
  *   d_initial_state : [N, C] float32 e of the first token, or NULL; it may alias d_final_state
  * h is what the forward returned, elements or (h_scales) 8-bit codes; dg uses these
