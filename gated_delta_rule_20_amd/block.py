@@ -128,9 +128,9 @@ def _types(x_new, y, gate, dx_new, dn, dtype, dx, dy, dgate):
                 if isinstance(t, kind) and t.dtype is not None:
                     return t.dtype
         return None
-    x_dtype = named(dx_new, x_new, dx)
+    x_dtype = dx_new.dtype if isinstance(dx_new, torch.Tensor) else named(x_new, dx)
     if dtype is None:
-        dtype = named(dn, y, gate, dy, dgate)
+        dtype = dn.dtype if isinstance(dn, torch.Tensor) else named(y, gate, dy, dgate)
     if dtype is None and (x_dtype is torch.bfloat16 or (y is None and dn is None)):
         dtype = x_dtype                        # a bf16 stream has bf16 blocks; without blocks no value is of their type
     if x_dtype is None and dtype is torch.float32:

@@ -114,9 +114,9 @@ struct NormParams {
     void *dx, *dy, *dgate;
     int64_t dy_stride, dgate_stride;
     float *dpost, *dres, *dpre;       // [D] or null
-    float *part;                      // [3, parts, D]: rows of up to norm_row_d channels leave several for each workgroup, in turn
+    float *part;                      // [3, parts, D]
     float __attribute__((ext_vector_type(4))) *numbers;  // [R], beyond norm_row_d channels
-    int parts, groups;                // sums; workgroups a column
+    int parts, groups;                // workgroups (of a column); those that run at a time
 };
 
 hipError_t launch_norm_fwd(int bf16, int x_bf16, const NormParams &p, hipStream_t stream);

@@ -201,10 +201,10 @@ template <typename A> kda_status_t plan_norm(const A *a, kda::NormParams *p)
     return KDA_SUCCESS;
 }
 
-// Workgroups of the gradients, and the float32 sums of the weights' gradients that they leave: four rows a side at least for a workgroup,
-// 16 waves (of columns: 32) on each of 256 units at most.  A sum is of NORM_CHAIN rows a side at most, so that what it may be off by does not
-// grow with the rows: by rows a workgroup leaves one after the other, by columns there are more workgroups.  (65536 x 4096 1019 us; with
-// one sum a workgroup 968, then of equal rows off by 64 roundings instead of 16; 2^20 x 256 927 and 908.)
+// Workgroups of the gradients, each with float32 sums of its own of the weights' gradients: four rows a side at least, 16 waves (of columns:
+// 32) on each of 256 units at most, or as many times these as leave no side more than NORM_CHAIN rows, so that what the sums may be off by
+// does not grow with the rows: 65536 x 4096 1006 us, with 256 rows in a sum (equal rows off by 64 roundings instead of 16) 967; 2^20 x 256
+// 916 and 905.
 // (One row at least: 256 x 4096 23.5 us either way, with four times the sums; 16: 42.5.)
 void norm_parts(int R, int D, bool columns, kda::NormParams *p)
 {
@@ -214,15 +214,14 @@ void norm_parts(int R, int D, bool columns, kda::NormParams *p)
     p->groups = p->parts = n < most ? n : most;
     const int turn = most * side * kda::NORM_CHAIN;        // rows (2^18 at most)
     if (R > turn) p->parts = most * (R / turn + (R % turn != 0));
-    if (columns) p->groups = p->parts;
 }
 
 kda_status_t plan_norm_bwd(const kda_block_norm_bwd_args_t *a, kda::NormParams *p, size_t *bytes)
 {
     const bool columns = a->D > kda::norm_row_d(a->dtype == KDA_F32);
     norm_parts(a->R, a->D, columns, p);
-    const long long wide = (a->D + kda::NORM_COLUMN - 1) / kda::NORM_COLUMN;
-    if (columns && !launchable(p->groups * wide, 256))
+    const long long wide = columns ? (a->D + kda::NORM_COLUMN - 1) / kda::NORM_COLUMN : 1;
+    if (!launchable(p->parts * wide, columns ? 256 : 64 * kda::norm_waves(a->D)))
         return fail(KDA_ERROR_NOT_SUPPORTED, "R * D too large for one call");
     Carver c(a->workspace);
     if (a->d_post_weight || a->d_res_scale || a->d_pre_weight) p->part = (float *)c.take(sizeof(float) * 3 * (size_t)p->parts * a->D);
