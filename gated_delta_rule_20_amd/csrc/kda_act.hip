@@ -5,7 +5,7 @@ namespace kda {
 
 // A lane packs 8 channels (one 16-byte load of bf16), 16 lanes a group, so that its largest value is four steps among the lanes of a
 // row of the register file; a workgroup takes 16 groups of consecutive rows' groups.  Bound by memory: 8192 x 4096 in bf16 packs in
-// 20.6 us (102 MB, 4.9 TB/s) and unpacks in 17.0 (6.0 TB/s, the codes partly from a cache).
+// 21 us (102 MB, 4.9 TB/s) and unpacks in 17.3 (5.9 TB/s, the codes partly from a cache).
 template <typename T> __global__ __launch_bounds__(256) void act_pack_kernel(Rows x, long long groups, int D, PackedOut out)
 {
     const int per = act_groups(D);

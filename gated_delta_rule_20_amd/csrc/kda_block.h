@@ -13,7 +13,7 @@ constexpr int NORM_MAX_D = 16384;     // channels of a row
 
 // Block norms backwards: up to norm_row_d channels a workgroup holds whole rows, beyond columns of NORM_COLUMN channels.  In
 // float32 a row of 8192 does not fit the registers next to its sums: 4096 x 8192 412 us by rows, 370 by columns, 16 x 8192 48 and 27.
-// With bf16 it does: 141 and 230 us, 27 and 28 (next to a float32 stream 231 and 282, 38 and 27).
+// With bf16 it does: 141 and 230 us, 27 and 28 (next to a float32 stream 231 and 282, but 38 and 27: the rule goes by the blocks' type alone).
 constexpr int norm_row_d(bool f32) { return f32 ? 4096 : 8192; }
 constexpr int NORM_COLUMN = 1024;
 

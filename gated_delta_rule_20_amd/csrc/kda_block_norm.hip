@@ -186,7 +186,7 @@ __device__ __forceinline__ void load_weight(const float *w, int c, int n, float 
     for (int i = 0; i < 8; ++i) x[i] = otherwise;
 }
 
-// Forward.  Bound by memory, 10 bytes an element in bf16: 8192 x 4096 63 us (336 MB, 5.3 TB/s).  NW waves hold a row, 8 NCH channels
+// Forward.  Bound by memory, 10 bytes an element in bf16: 8192 x 4096 62 to 66 us (336 MB, 5.1 TB/s or more).  NW waves hold a row, 8 NCH channels
 // a lane (16-byte loads of bf16); a workgroup of ROWS such rows side by side goes through its rows with the weights in registers and
 // the next rows' values on their way.
 
@@ -468,7 +468,7 @@ template <int NT, int NQ> struct Quads<NT, NQ, true> {
 //   sum of w_post du y = sum A dx + rx sum A w_pre dn - rx^2 mx sum A x,
 // so a row has one barrier between its two looks at the values (two: 160 us for 8192 x 4096 from 8 bits).  NW waves hold a row,
 // NQ times 4 channels a lane.  With 4 (up to 4096 channels) the weights, their sums, a row and the next one as it is stored fit
-// 128 registers, so that 16 waves a unit hide the sum: 99 us from 8 bits (439 MB, 4.4 TB/s) and 144 in bf16 (8 channels a lane and 8 waves:
+// 128 registers, so that 16 waves a unit hide the sum: 98 to 105 us from 8 bits (439 MB, 4.2 TB/s or more) and 131 in bf16 (8 channels a lane and 8 waves:
 // 143 us from 8 bits).  With 8 the weights lie in LDS, and the
 // row's values are unpacked a second time for the second look.
 // RAGGED: the last channels of a row are fewer than a lane's four.  The lane loads the row's last four all the same and takes those before
@@ -584,8 +584,8 @@ __global__ __launch_bounds__(64 * NW * ROWS, 4) void norm_bwd_kernel(const NormP
 
 // Rows of more than norm_row_d channels do not fit a workgroup's registers next to the weights and their sums (as one such kernel
 // with the sums in LDS 2048 x 16384 took 447 us, 64 rows 130): a first kernel forms each row's numbers, a second goes
-// through columns of 1024 channels with the weights and sums in registers and no barrier.  The values are read twice: 235 us, 3.3 TB/s
-// with the second reading; 64 rows 29 us.
+// through columns of 1024 channels with the weights and sums in registers and no barrier.  The values are read twice: 240 us, 3.2 TB/s
+// with the second reading; 64 rows 33 us.
 constexpr int WIDE_WAVES = 8;
 template <typename T, typename X> __global__ __launch_bounds__(64 * WIDE_WAVES, 4) void norm_numbers_kernel(const NormParams p)
 {

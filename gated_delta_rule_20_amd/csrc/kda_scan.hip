@@ -34,10 +34,11 @@ __device__ __forceinline__ void sequence_of(const ScanParams &p, int s, int *lo,
 // slower).  The order in which pairs are joined is fixed, so results do not depend on timing.  Where sequences begin, the
 // state is replaced, and what lies before is not waited for.
 //
-// Bound by the arithmetic (38 instructions a token with the gate, all passes and the hand-over, units busy for about 70% of the time) and
-// by the wait for the segments before, which run at the same time: 131072 rows x 2048 in bf16 with the gate take 503 us,
-// 3.2 TB/s; without waiting they would take about 400.  8192 x 4096: 60 us (3.3 TB/s), with log-decays 57; gradients 102 us, from
-// 8-bit values 98.  With an odd number of channels vectors are read at odd addresses: 8192 x 4001 75 and 152 us.
+// Bound by no unit alone: a workgroup's load, pass, wait and store follow one another, and the four of a compute unit do not fill each
+// other's gaps.  131072 rows x 2048 in bf16 with the gate take 504 us (3.2 TB/s; a copy would take 327), of which the vector units issue
+// 61% of the time and a wave waits 61% (38 instructions a token with the gate, all passes and the hand-over).  8192 x 4096: 62 us, 70 on
+// tensors that no cache holds, without the gate 66; gradients 104 us, from 8-bit values 98 (vector units 77%).  With an odd number of channels
+// vectors are read at odd addresses: 8192 x 4001 77 and 154 us.
 // One segment has nothing to join: no tickets, no clearing (one launch less, 13.4 us instead of 17 with the call).
 
 constexpr int CH = 4, LANES = SCAN_CHANNELS / CH;           // channels a lane; lanes of a row
@@ -47,7 +48,7 @@ constexpr uint32_t EMPTY = 0xffffffffu;                     // no decay has thes
 constexpr float CUT = 2.f;                                  // in place of a decay: a sequence began among the rows
 constexpr int BLOCK = SCAN_BLOCK;
 constexpr int TICKET_STEP = SCAN_TICKET_STEP;
-constexpr int SPINS = 1 << 20;                              // about a second
+constexpr int SPINS = 1 << 20;                              // some tenths of a second
 
 struct Marks {
     int first[SCAN_ROWS], last[SCAN_ROWS];                  // the sequence that begins / ends at a row, or -1
@@ -156,7 +157,7 @@ __device__ __forceinline__ void publish(uint64_t *p, uint64_t v)
     asm volatile("" ::: "memory");                          // before any wait that follows
 }
 
-// Waits for the pairs at(0) .. at(n - 1), n <= BLOCK.  A wait that lasts about a second (another call writes to this call's
+// Waits for the pairs at(0) .. at(n - 1), n <= BLOCK.  A wait that lasts some tenths of a second (another call writes to this call's
 // workspace) is given up, by all waits of the call: the pair counts as a cut with NaN.
 template <typename F> __device__ __forceinline__ void await_pairs(const ScanChain &k, int n, F at, uint64_t *v)
 {
@@ -581,7 +582,7 @@ __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 ? 4 : 3) void scan_
 
 // Gradients, from the last row to the first: D_t = d_h_t + e_{t+1}, e_t = a_t D_t; runs, segments and their order mirrored.
 // h and x are asked for before the wait.  Saved values of a kind that the kernel knows leave room for three waves a SIMD: 8192 x 4096
-// 102 us in bf16, 98 from 8 bits; with a kernel for either, at the time, 180 instead of 114 and 132 instead of 110.  One
+// 104 us in bf16, 98 from 8 bits; with a kernel for either, at the time, 180 instead of 114 and 132 instead of 110.  One
 // that finds h in one form and x in the other, or a single segment, takes that kernel.
 template <typename T, typename G, bool GATED, bool CHAIN, Saved S>
 __global__ __launch_bounds__(256, sizeof(T) + sizeof(G) == 4 && S != EITHER ? 3 : 2) void scan_bwd_kernel(const ScanParams p)
